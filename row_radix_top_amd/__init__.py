@@ -30,3 +30,10 @@ from .binding import (  # noqa: F401
     workspace_size,
     workspace_status,
 )
+from .attention import (  # noqa: F401
+    Layout,
+    latent_append,
+    paged_append,
+    paged_attention,
+    paged_layout,
+)

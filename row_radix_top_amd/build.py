@@ -25,8 +25,7 @@ OBJDIR = os.path.join(PKG, "_build")
 
 
 def sources() -> list[str]:
-    hips = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-    return [os.path.join(CSRC, "topk_host.cpp"), *hips]
+    return [*sorted(glob.glob(os.path.join(CSRC, "*.cpp"))), *sorted(glob.glob(os.path.join(CSRC, "*.hip")))]
 
 
 HIP_FLAGS = [

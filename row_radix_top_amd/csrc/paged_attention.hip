@@ -1,0 +1,459 @@
+// Attention of single tokens over a paged cache of keys and values, and the
+// join of rows that were split over several workgroups.
+
+#include "paged_device.hpp"
+
+namespace rrt {
+
+// ---------------------------------------------------------------------------
+// o = softmax(s q K^T) V in one pass over K and V, with the running maximum m
+// (of base-2 logarithms) and sum l of each query column.
+//
+// A workgroup takes one part of one key-value head's positions; its four
+// wavefronts take tiles of 32 tokens in turn, each with its own m, l and
+// output, and join them in LDS at the end.  The columns of a tile are the
+// query heads that share the key-value head, for every row of the sequence
+// (multi-token rows read the cache once).
+//
+// Nothing passes through LDS on the way in.  With S^T = K Q^T the K operand's
+// lane layout (row l % 16, 8 consecutive dims) is what a 16-byte load of a
+// cache row gives, and S^T's layout (column l % 16, rows l / 16 * 4 + i) is
+// the layout of the P operand of O^T = V^T P if lane group g = l / 16 counts
+// tokens g*4 .. g*4+3 and 16+g*4 .. 16+g*4+3 as its eight: the order of the
+// summed-over tokens is free as long as V follows it.  So each lane loads V
+// rows of those eight tokens (a load of a wavefront covers four whole rows)
+// and transposes its own 8 x 8 block with byte permutes.  m, l, P and O^T then
+// all live in the lane of their column: no exchange but the maximum's.
+//
+// P is rounded to the 16-bit type for the matrix instruction (half a step
+// relative to each weight); m, l, S and O stay fp32.
+// ---------------------------------------------------------------------------
+constexpr int kAttnBlock = 256;
+constexpr int kTok = 32;  // tokens of a wavefront's tile
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
+  return x;
+}
+
+// The longest row of a group, all lanes.
+__device__ __forceinline__ int32_t group_length(const AttnParams& p, int32_t r0, int64_t most, int lane) {
+  int32_t n = 0;
+  for (int32_t j = lane; j < p.group_rows; j += 64) {
+    const int32_t x = clamp_to(p.a.lengths[r0 + j], most);
+    n = x > n ? x : n;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const int32_t x = __shfl_xor(n, off);
+    n = x > n ? x : n;
+  }
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+template <bool F8, int D>
+struct KvTile {
+  static constexpr int KL = F8 ? D / 64 : D / 32;                // 16-byte key loads per token of a lane group
+  static constexpr int VW = F8 ? D / 64 : D / 32;                // words of a lane's value dims
+  u32x4 k[2][KL];
+  uint32_t v[8][VW];
+  uint32_t valid;  // bit i: token i of the tile is in the cache and inside the part
+};
+
+template <bool F8, int D>
+__device__ __forceinline__ void load_tile(KvTile<F8, D>& b, const char* k, const char* v, int64_t off, int lane) {
+  using Tile = KvTile<F8, D>;
+  constexpr int SZ = F8 ? 1 : 2;
+  const int row = lane & 15, g = lane >> 4;
+  b.valid = (uint32_t)__builtin_amdgcn_ballot_w64(off >= 0);
+  const int64_t at = off < 0 ? 0 : off * SZ;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const char* kp = k + shfl64(at, u * 16 + row) + g * 16;
+#pragma unroll
+    for (int i = 0; i < Tile::KL; ++i) b.k[u][i] = *(const u32x4*)(kp + i * 64);
+  }
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const char* vp = v + shfl64(at, (t >> 2) * 16 + g * 4 + (t & 3)) + row * (Tile::VW * 4);
+    if constexpr (Tile::VW == 4) {
+      const u32x4 x = *(const u32x4*)vp;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b.v[t][i] = x[i];
+    } else if constexpr (Tile::VW == 2) {
+      const u32x2 x = *(const u32x2*)vp;
+      b.v[t][0] = x[0], b.v[t][1] = x[1];
+    } else {
+      b.v[t][0] = *(const uint32_t*)vp;
+    }
+  }
+}
+
+template <typename T, bool F8, int D, bool CHOSEN, int NT>
+__global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnParams p) {
+  constexpr int KS = D / 32;  // matrix steps over the key dims
+  constexpr int VD = D / 16;  // value dims of a lane
+  constexpr int SZ = F8 ? 1 : 2;
+  constexpr int LD = D + 4;   // row pitch of the joined outputs in LDS
+  __shared__ float so[4][16][LD];
+  __shared__ float sm[4][16], sl[4][16];
+  const paged_attention_args& a = p.a;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col16 = lane & 15, g = lane >> 4;
+
+  const int32_t units = p.groups * a.num_kv_heads * p.col_tiles;
+  const int32_t part = (int32_t)(blockIdx.x / (uint32_t)units);
+  int32_t unit = (int32_t)(blockIdx.x - (uint32_t)part * (uint32_t)units);
+  const int32_t kvh = unit % a.num_kv_heads;
+  unit /= a.num_kv_heads;
+  const int32_t tile = unit % p.col_tiles, group = unit / p.col_tiles;
+  const int32_t r0 = group * p.group_rows;
+  const int32_t heads_per = a.num_heads / a.num_kv_heads;
+  const int64_t most = table_tokens(a.table_width, a.page_size);
+
+  const int32_t n = CHOSEN ? a.num_chosen : group_length(p, r0, most, lane);
+  const Split sp = split_of(n, p.most, p.least, p.unit);
+  if (part >= sp.parts) return;
+  const int32_t begin = part * sp.chunk;
+  const int32_t end = n - begin < sp.chunk ? n : begin + sp.chunk;
+
+  // Columns: (row of the group, head of the key-value head).
+  int32_t collen[NT], colrow[NT];
+  u32x4 q[NT][KS];
+  int32_t shortest = INT32_MAX, jlo = INT32_MAX, jhi = -1;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int32_t c = (tile * NT + t) * 16 + col16;
+    const bool real = c < p.group_rows * heads_per;
+    const int32_t j = real ? c / heads_per : 0;
+    collen[t] = real ? clamp_to(a.lengths[r0 + j], most) : 0;
+    colrow[t] = real ? j : -1;
+    if (real) {
+      shortest = collen[t] < shortest ? collen[t] : shortest;
+      jlo = j < jlo ? j : jlo;
+      jhi = j > jhi ? j : jhi;
+    }
+    const int32_t head = kvh * heads_per + (c - j * heads_per);
+    const char* qp = (const char*)a.q + 2 * ((int64_t)(r0 + j) * a.q_row_stride + (int64_t)head * a.q_head_stride);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      // The dims that the lane's key words hold at matrix step i.
+      const int dim = F8 ? (i >> 1) * 64 + g * 16 + (i & 1) * 8 : i * 32 + g * 8;
+      q[t][i] = real ? *(const u32x4*)(qp + 2 * dim) : u32x4{0, 0, 0, 0};
+    }
+  }
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) {
+    const int32_t x = __shfl_xor(shortest, off), y = __shfl_xor(jlo, off), z = __shfl_xor(jhi, off);
+    shortest = x < shortest ? x : shortest;
+    jlo = y < jlo ? y : jlo;
+    jhi = z > jhi ? z : jhi;
+  }
+  shortest = __builtin_amdgcn_readfirstlane(shortest);
+  jlo = __builtin_amdgcn_readfirstlane(jlo);
+  jhi = __builtin_amdgcn_readfirstlane(jhi);
+
+  const float scale = p.scale_log2 * (F8 && a.k_scales != nullptr ? a.k_scales[kvh] : 1.0f);
+  const char* kbase = (const char*)a.k + (int64_t)kvh * a.head_stride * SZ;
+  const char* vbase = (const char*)a.v + (int64_t)kvh * a.head_stride * SZ;
+  const int32_t* table = a.block_table + (int64_t)(r0 / a.next_n) * a.table_stride;
+  const int32_t* chosen = CHOSEN ? a.chosen + (int64_t)r0 * a.chosen_stride : nullptr;
+  const int32_t seen = CHOSEN ? clamp_to(a.lengths[r0], most) : 0;
+
+  // Place of the lane's token (both halves of the wavefront hold the same 32).
+  auto place = [&](int32_t t) -> int64_t {
+    const int32_t i = t + (lane & 31);
+    if (i >= end) return -1;
+    const int32_t pos = CHOSEN ? chosen[i] : i;
+    if (CHOSEN && (uint32_t)pos >= (uint32_t)seen) return -1;
+    return locate(table, a.page_size, a.num_pages, a.page_stride, a.token_stride, pos);
+  };
+
+  float m[NT], l[NT];
+  f32x4 o[NT][VD];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -INFINITY, l[t] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < VD; ++d) o[t][d] = f32x4{0, 0, 0, 0};
+  }
+
+  auto compute = [&](const KvTile<F8, D>& b, int32_t t0) {
+    const bool whole = b.valid == 0xffffffffu;
+    const bool ragged = !CHOSEN && t0 + kTok > shortest;  // some column ends inside the tile, or before it
+    if (b.valid == 0) return;
+    f32x4 s[NT][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      u32x4 kk[KS];
+      if constexpr (F8) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) kk[i] = widen<T>(u32x2{b.k[u][i >> 1][(i & 1) * 2], b.k[u][i >> 1][(i & 1) * 2 + 1]});
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) kk[i] = b.k[u][i];
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        s[t][u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < KS; ++i) s[t][u] = T::mfma16(kk[i], q[t][i], s[t][u]);
+      }
+    }
+    u32x4 pk[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = s[t][e >> 2][e & 3] * scale;
+      if (!whole || ragged) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = (e >> 2) * 16 + g * 4 + (e & 3);
+          const bool in = ((b.valid >> i) & 1u) != 0 && (CHOSEN || t0 + i < collen[t]);
+          x[e] = in ? x[e] : -INFINITY;
+        }
+      }
+      float mt = x[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) mt = fmaxf(mt, x[e]);
+      mt = fmaxf(mt, __shfl_xor(mt, 16));
+      mt = fmaxf(mt, __shfl_xor(mt, 32));
+      if (__builtin_amdgcn_ballot_w64(mt > m[t]) != 0) {
+        const float mn = fmaxf(m[t], mt);
+        const float by = mn == m[t] ? 1.0f : exp2_fast(m[t] - mn);
+        m[t] = mn;
+        l[t] *= by;
+#pragma unroll
+        for (int d = 0; d < VD; ++d) o[t][d] *= by;
+      }
+      const float ref = m[t] == -INFINITY ? 0.0f : m[t];
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = exp2_fast(x[e] - ref);
+        sum += x[e];
+      }
+      l[t] += sum;
+      pk[t] = u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
+    }
+    // Values as 16-bit pairs of dims.  Tokens that do not count become zeros
+    // below: their places may hold NaN, which a weight of zero would not stop.
+    uint32_t v[8][VD / 2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int i = 0; i < VD / 2; ++i) {
+        if constexpr (F8)
+          v[e][i] = (i & 1) ? T::template from_e4m3<true>(b.v[e][i >> 1]) : T::template from_e4m3<false>(b.v[e][i >> 1]);
+        else
+          v[e][i] = b.v[e][i];
+      }
+    // One matrix step for value dim d of each lane's block; the words of
+    // `keep` are all ones where the pair's tokens count.
+    auto accumulate = [&](int d, bool masked, u32x4 keep, f32x4(&out)[NT]) {
+      const uint32_t sel = (d & 1) ? 0x07060302u : 0x05040100u;
+      const int i = d >> 1;
+      u32x4 vt = {__builtin_amdgcn_perm(v[1][i], v[0][i], sel), __builtin_amdgcn_perm(v[3][i], v[2][i], sel),
+                  __builtin_amdgcn_perm(v[5][i], v[4][i], sel), __builtin_amdgcn_perm(v[7][i], v[6][i], sel)};
+      if (masked) vt &= keep;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) out[t] = T::mfma16(vt, pk[t], o[t][d]);
+    };
+    auto keep_words = [&](uint32_t bits) {  // bits: the tile's tokens that count
+      u32x4 k;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = (e >> 1) * 16 + g * 4 + (e & 1) * 2;
+        k[e] = ((bits >> i) & 1u ? 0x0000ffffu : 0u) | ((bits >> i) & 2u ? 0xffff0000u : 0u);
+      }
+      return k;
+    };
+    if (!ragged || p.group_rows == 1) {
+      if (whole) {
+#pragma unroll
+        for (int d = 0; d < VD; ++d) {
+          f32x4 out[NT];
+          accumulate(d, false, u32x4{}, out);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) o[t][d] = out[t];
+        }
+      } else {
+        const u32x4 keep = keep_words(b.valid);
+#pragma unroll
+        for (int d = 0; d < VD; ++d) {
+          f32x4 out[NT];
+          accumulate(d, true, keep, out);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) o[t][d] = out[t];
+        }
+      }
+      return;
+    }
+    // Rows of the sequence end at different places in this tile: one row's
+    // columns at a time, with the tokens that the row does not see as zeros.
+    for (int32_t j = jlo; j <= jhi; ++j) {
+      const int32_t left = clamp_to(a.lengths[r0 + j], most) - t0;
+      if (left <= 0) continue;  // its weights in this tile are zeros
+      const u32x4 keep = keep_words(left >= 32 ? b.valid : b.valid & ((1u << left) - 1u));
+#pragma unroll
+      for (int d = 0; d < VD; ++d) {
+        f32x4 out[NT];
+        accumulate(d, true, keep, out);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[t][d][i] = colrow[t] == j ? out[t][i] : o[t][d][i];
+      }
+    }
+  };
+
+  // Two tiles in flight: one being read, one being used.
+  constexpr int kStep = 4 * kTok;
+  KvTile<F8, D> b0, b1;
+  int32_t t = begin + w * kTok;
+  int64_t next = t < end ? place(t) : -1;
+  if (t < end) {
+    load_tile<F8, D>(b0, kbase, vbase, next, lane);
+    next = place(t + kStep);
+    while (true) {
+      if (t + kStep < end) load_tile<F8, D>(b1, kbase, vbase, next, lane);
+      next = place(t + 2 * kStep);
+      compute(b0, t);
+      t += kStep;
+      if (t >= end) break;
+      if (t + kStep < end) load_tile<F8, D>(b0, kbase, vbase, next, lane);
+      next = place(t + 2 * kStep);
+      compute(b1, t);
+      t += kStep;
+      if (t >= end) break;
+    }
+  }
+
+  const float v_scale = F8 && a.v_scales != nullptr ? a.v_scales[kvh] : 1.0f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (t > 0) __syncthreads();
+    if (lane < 16) sm[w][lane] = m[t], sl[w][lane] = l[t];
+    __syncthreads();
+    const float top = fmaxf(fmaxf(sm[0][col16], sm[1][col16]), fmaxf(sm[2][col16], sm[3][col16]));
+    const float by = (m[t] == top ? 1.0f : exp2_fast(m[t] - top)) * v_scale;
+#pragma unroll
+    for (int d = 0; d < VD; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) so[w][col16][(g * 4 + i) * VD + d] = o[t][d][i] * by;
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < 16 * (D / 2); i += kAttnBlock) {
+      const int32_t c16 = i / (D / 2), dim = (i - c16 * (D / 2)) * 2;
+      const int32_t c = (tile * NT + t) * 16 + c16;
+      if (c >= p.group_rows * heads_per) continue;
+      const int32_t j = c / heads_per;
+      const int64_t at = (int64_t)(r0 + j) * a.num_heads + kvh * heads_per + (c - j * heads_per);
+      const float cm = fmaxf(fmaxf(sm[0][c16], sm[1][c16]), fmaxf(sm[2][c16], sm[3][c16]));
+      float sum = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum += sl[k][c16] * (sm[k][c16] == cm ? 1.0f : exp2_fast(sm[k][c16] - cm));
+        x += so[k][c16][dim];
+        y += so[k][c16][dim + 1];
+      }
+      if (sp.parts == 1) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        *(uint32_t*)((uint16_t*)a.out + at * D + dim) = T::pack(x * inv, y * inv);
+        if (dim == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (cm + __log2f(sum)) * kLn2;
+      } else {
+        const int64_t pi = at * p.most + part;
+        *(float2*)(p.part_out + pi * D + dim) = float2{x, y};
+        if (dim == 0) p.part_stat[pi] = float2{cm, sum};
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over a row's
+// parts, M the largest m_i.  One wavefront for each (row, head), D / 64 dims a
+// lane; rows of one part were finished by the attention kernel.  Reads the
+// parts once, from L2: a few microseconds at most, mostly the launch.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(kAttnBlock) join_kernel(AttnParams p) {
+  constexpr int E = D / 64;
+  const paged_attention_args& a = p.a;
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * (kAttnBlock / 64) + (threadIdx.x >> 6);
+  if (at >= (int64_t)a.num_rows * a.num_heads) return;
+  const int32_t row = (int32_t)(at / a.num_heads);
+  const int32_t n = a.chosen != nullptr
+                        ? a.num_chosen
+                        : group_length(p, row / p.group_rows * p.group_rows, table_tokens(a.table_width, a.page_size), lane);
+  const Split sp = split_of(n, p.most, p.least, p.unit);
+  if (sp.parts == 1) return;
+  const float2* stat = p.part_stat + at * p.most;
+  float m0 = -INFINITY, l0 = 0.0f, m1 = -INFINITY, l1 = 0.0f;  // at most 128 parts
+  if (lane < sp.parts) m0 = stat[lane].x, l0 = stat[lane].y;
+  if (lane + 64 < sp.parts) m1 = stat[lane + 64].x, l1 = stat[lane + 64].y;
+  const float top = wave_max(fmaxf(m0, m1));
+  const float w0 = m0 == top ? 1.0f : exp2_fast(m0 - top), w1 = m1 == top ? 1.0f : exp2_fast(m1 - top);
+  float sum = l0 * w0 + l1 * w1;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+  const float* po = p.part_out + at * p.most * D + lane * E;
+  float o[E] = {};
+#pragma unroll 4
+  for (int32_t i = 0; i < sp.parts; ++i) {
+    const float by = __shfl(i < 64 ? w0 : w1, i & 63);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += by * po[(int64_t)i * D + e];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* out = (uint16_t*)a.out + at * D + lane * E;
+  if constexpr (E == 1) {
+    *out = (uint16_t)T::pack(o[0] * inv, 0.0f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *(uint32_t*)(out + e) = T::pack(o[e] * inv, o[e + 1] * inv);
+  }
+  if (lane == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+}
+
+namespace {
+
+template <typename T, bool F8, int D, bool CHOSEN>
+const void* attn_tiles(int tiles) {
+  return tiles == 2 ? (const void*)&attn_kernel<T, F8, D, CHOSEN, 2> : (const void*)&attn_kernel<T, F8, D, CHOSEN, 1>;
+}
+template <typename T, bool F8>
+const void* attn_dims(int head_dim, bool chosen, int tiles) {
+  if (head_dim == 64) return chosen ? attn_tiles<T, F8, 64, true>(tiles) : attn_tiles<T, F8, 64, false>(tiles);
+  if (head_dim == 128) return chosen ? attn_tiles<T, F8, 128, true>(tiles) : attn_tiles<T, F8, 128, false>(tiles);
+  return nullptr;
+}
+template <typename T>
+const void* join_dims(int head_dim) {
+  switch (head_dim) {
+    case 64: return (const void*)&join_kernel<T, 64>;
+    case 128: return (const void*)&join_kernel<T, 128>;
+    case 256: return (const void*)&join_kernel<T, 256>;
+    case 512: return (const void*)&join_kernel<T, 512>;
+    default: return nullptr;
+  }
+}
+
+}  // namespace
+
+const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int tiles) {
+  if (dtype == PAGED_BF16)
+    return store == PAGED_E4M3 ? attn_dims<Bf16, true>(head_dim, chosen, tiles)
+                               : attn_dims<Bf16, false>(head_dim, chosen, tiles);
+  return store == PAGED_E4M3 ? attn_dims<Fp16, true>(head_dim, chosen, tiles)
+                             : attn_dims<Fp16, false>(head_dim, chosen, tiles);
+}
+
+const void* join_kernel_ptr(int dtype, int head_dim) {
+  return dtype == PAGED_BF16 ? join_dims<Bf16>(head_dim) : join_dims<Fp16>(head_dim);
+}
+
+}  // namespace rrt

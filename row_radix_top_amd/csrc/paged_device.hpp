@@ -1,0 +1,77 @@
+// Device helpers of the paged-cache kernels: 16-bit types and their matrix
+// instructions, e4m3 conversions, lane exchanges.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "paged_internal.h"
+
+namespace rrt {
+
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
+
+// The two 16-bit types.  pack: two fp32 values to a pair, each rounded to
+// nearest even; from_e4m3: two of the four 8-bit values of a word, exactly;
+// mfma16: D[16][16] += A[16][32] B[32][16], lane l holding A's row l % 16 and
+// B's column l % 16 for the 8 values k = l / 16 * 8 .. + 8, and D's column
+// l % 16 for the rows l / 16 * 4 .. + 4.
+struct Bf16 {
+  using elem = __bf16;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  template <bool HI>
+  static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+  }
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+};
+
+struct Fp16 {
+  using elem = _Float16;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    f16x2 v = {(_Float16)lo, (_Float16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
+  static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
+  template <bool HI>
+  static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+  }
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+};
+
+// Eight e4m3 values (two words) to eight 16-bit ones (four words).
+template <typename T>
+__device__ __forceinline__ u32x4 widen(u32x2 w) {
+  return u32x4{T::template from_e4m3<false>(w[0]), T::template from_e4m3<true>(w[0]),
+               T::template from_e4m3<false>(w[1]), T::template from_e4m3<true>(w[1])};
+}
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+  const int lo = __shfl((int)(uint32_t)v, lane), hi = __shfl((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+}  // namespace rrt

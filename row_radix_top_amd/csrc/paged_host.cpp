@@ -1,0 +1,258 @@
+// Host side of the paged-cache entry points: argument checks, how rows are
+// split, and the launches.  No allocation, no memset and no synchronisation.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "paged_internal.h"
+#include "topk_internal.h"
+
+namespace {
+
+using rrt::set_error;
+
+// Every check that fails names the argument; nothing has been launched then.
+#define REQUIRE(cond, text) \
+  do {                      \
+    if (!(cond)) return set_error(TOPK_EINVAL, text); \
+  } while (0)
+
+bool aligned(const void* p, uintptr_t by) { return reinterpret_cast<uintptr_t>(p) % by == 0; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int launch(const void* fn, int64_t grid, int block, void* params, hipStream_t stream, const char* what) {
+  char buf[192];
+  if (fn == nullptr) {
+    std::snprintf(buf, sizeof(buf), "%s: no kernel instance for these arguments", what);
+    return set_error(TOPK_EINVAL, buf);
+  }
+  if (grid > INT32_MAX) {
+    std::snprintf(buf, sizeof(buf), "%s: %lld workgroups are more than one launch takes", what, (long long)grid);
+    return set_error(TOPK_EINVAL, buf);
+  }
+  void* args[] = {params};
+  hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)block), args, 0, stream);
+  if (e == hipSuccess) e = hipGetLastError();
+  if (e != hipSuccess) {
+    std::snprintf(buf, sizeof(buf), "%s: launch failed: %s", what, hipGetErrorString(e));
+    return set_error(TOPK_ELAUNCH, buf);
+  }
+  return TOPK_OK;
+}
+
+int check_types(paged_dtype dtype, paged_dtype store) {
+  REQUIRE(dtype == PAGED_BF16 || dtype == PAGED_FP16, "dtype must be PAGED_BF16 or PAGED_FP16");
+  REQUIRE(store == dtype || store == PAGED_E4M3, "store must be dtype or PAGED_E4M3");
+  return TOPK_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+
+// A part's fewest positions and the unit its length is rounded to: four
+// wavefronts take 32 tokens each.
+constexpr int32_t kUnit = 128;
+constexpr int32_t kLeast = 256;
+constexpr int32_t kMostParts = 128;
+constexpr int64_t kPartsPerCu = 4;  // workgroups per CU that a launch is split into
+
+int check_attention(const paged_attention_args* a, bool latent) {
+  REQUIRE(a != nullptr, "null args");
+  if (int rc = check_types(a->dtype, a->store)) return rc;
+  REQUIRE(a->num_rows >= 0, "num_rows must be >= 0");
+  REQUIRE(a->next_n >= 1 && a->num_rows % a->next_n == 0, "next_n must be >= 1 and divide num_rows");
+  REQUIRE(a->num_heads >= 1, "num_heads must be >= 1");
+  if (latent) {
+    REQUIRE(a->head_dim == 256 || a->head_dim == 512, "head_dim of the latent vector must be 256 or 512");
+  } else {
+    REQUIRE(a->head_dim == 64 || a->head_dim == 128, "head_dim must be 64 or 128");
+    REQUIRE(a->num_kv_heads >= 1 && a->num_heads % a->num_kv_heads == 0, "num_kv_heads must be >= 1 and divide num_heads");
+  }
+  REQUIRE(a->page_size >= 1, "page_size must be >= 1");
+  REQUIRE(a->table_width >= 1, "table_width must be >= 1");
+  REQUIRE(a->max_splits >= 0 && a->max_splits <= kMostParts, "max_splits must be in [0, 128]");
+  REQUIRE(a->chosen == nullptr || (a->num_chosen >= 1 && a->num_chosen <= rrt::kMostTokens),
+          "num_chosen must be in [1, 2^30]");
+  REQUIRE(std::isfinite(a->softmax_scale), "softmax_scale must be finite");
+  if (a->num_rows == 0) return TOPK_OK;
+  REQUIRE(a->num_pages >= 1, "num_pages must be >= 1");
+  REQUIRE((int64_t)a->num_rows * a->num_heads <= INT32_MAX, "num_rows * num_heads must be below 2^31");
+  REQUIRE(a->q != nullptr && a->k != nullptr && a->block_table != nullptr && a->lengths != nullptr && a->out != nullptr,
+          "null q, k, block_table, lengths or out");
+  REQUIRE(latent || a->v != nullptr, "null v");
+  const int64_t sz = a->store == PAGED_E4M3 ? 1 : 2;
+  REQUIRE(a->q_row_stride >= 0 && a->q_head_stride >= 0 && a->page_stride >= 0 && a->token_stride >= 0 &&
+              a->head_stride >= 0 && a->table_stride >= 0 && a->chosen_stride >= 0,
+          "strides must be >= 0");
+  REQUIRE(aligned(a->q, 16) && a->q_row_stride % 8 == 0 && a->q_head_stride % 8 == 0,
+          "q and its strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->k, 16) && (latent || aligned(a->v, 16)) && a->page_stride * sz % 16 == 0 &&
+              a->token_stride * sz % 16 == 0 && (latent || a->head_stride * sz % 16 == 0),
+          "the cache and its strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->out, 4), "out must be 4-byte aligned");
+  REQUIRE(aligned(a->block_table, 4) && aligned(a->lengths, 4) && aligned(a->chosen, 4) && aligned(a->lse, 4) &&
+              aligned(a->k_scales, 4) && aligned(a->v_scales, 4),
+          "block_table, lengths, chosen, lse and scales must be 4-byte aligned");
+  REQUIRE(a->store == PAGED_E4M3 || (a->k_scales == nullptr && a->v_scales == nullptr),
+          "scales belong to an e4m3 cache");
+  return TOPK_OK;
+}
+
+struct AttnPlan {
+  rrt::AttnParams p;
+  const void* fn;
+  int64_t grid;
+  size_t bytes;
+};
+
+int plan_attention(const paged_attention_args* a, bool latent, hipStream_t stream, AttnPlan* out) {
+  if (int rc = check_attention(a, latent)) return rc;
+  std::memset(out, 0, sizeof(*out));
+  if (a->num_rows == 0) return TOPK_OK;
+  int dev = 0, cus = 0;
+  if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
+  rrt::AttnParams& p = out->p;
+  p.a = *a;
+  p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
+  p.unit = kUnit;
+  p.least = kLeast;
+  const bool chosen = a->chosen != nullptr;
+  int64_t units = 0;
+  // Rows of a sequence read its cache together unless each has its own
+  // chosen positions.
+  p.group_rows = chosen ? 1 : a->next_n;
+  const int64_t columns = (int64_t)p.group_rows * (a->num_heads / a->num_kv_heads);
+  const int tiles = columns > 16 ? 2 : 1;
+  p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
+  p.groups = a->num_rows / p.group_rows;
+  units = (int64_t)p.groups * a->num_kv_heads * p.col_tiles;
+  out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, tiles);
+  const int64_t longest = chosen ? a->num_chosen : rrt::table_tokens(a->table_width, a->page_size);
+  int64_t most = a->max_splits > 0 ? a->max_splits : ceil_div(kPartsPerCu * cus, units);
+  most = std::max<int64_t>(1, std::min<int64_t>({most, (int64_t)kMostParts, longest / p.least}));
+  p.most = (int32_t)most;
+  out->grid = units * most;
+  out->bytes = most == 1 ? 0 : (size_t)a->num_rows * a->num_heads * most * (a->head_dim * sizeof(float) + sizeof(float2));
+  return TOPK_OK;
+}
+
+int run_attention(const paged_attention_args* a, bool latent, void* workspace, hipStream_t stream) {
+  AttnPlan plan;
+  if (int rc = plan_attention(a, latent, stream, &plan)) return rc;
+  if (a->num_rows == 0) return TOPK_OK;
+  if (plan.bytes > 0) {
+    if (workspace == nullptr) {
+      char buf[96];
+      std::snprintf(buf, sizeof(buf), "this launch needs a workspace of %zu bytes", plan.bytes);
+      return set_error(TOPK_EWORKSPACE, buf);
+    }
+    REQUIRE(aligned(workspace, 16), "workspace must be 16-byte aligned");
+    plan.p.part_out = static_cast<float*>(workspace);
+    plan.p.part_stat =
+        reinterpret_cast<float2*>(plan.p.part_out + (int64_t)a->num_rows * a->num_heads * plan.p.most * a->head_dim);
+  }
+  const char* name = latent ? "latent_attention" : "paged_attention";
+  if (int rc = launch(plan.fn, plan.grid, 256, &plan.p, stream, name)) return rc;
+  if (plan.p.most == 1) return TOPK_OK;
+  return launch(rrt::join_kernel_ptr(a->dtype, a->head_dim), ceil_div((int64_t)a->num_rows * a->num_heads, 4), 256,
+                &plan.p, stream, "join of split rows");
+}
+
+}  // namespace
+
+extern "C" {
+
+int paged_layout(const int32_t* lengths, const int32_t* new_tokens, int32_t num_seqs, const int32_t* free_pages,
+                 int32_t num_free, int32_t* block_table, int64_t table_stride, int32_t table_width,
+                 int32_t page_size, int32_t capacity, int32_t* starts, int32_t* slots, int32_t* row_lengths,
+                 int32_t* row_seqs, int32_t* pages, hipStream_t stream) {
+  REQUIRE(num_seqs >= 0, "num_seqs must be >= 0");
+  REQUIRE(num_free >= 0, "num_free must be >= 0");
+  REQUIRE(capacity >= 0, "capacity must be >= 0");
+  REQUIRE(page_size >= 1, "page_size must be >= 1");
+  REQUIRE(table_width >= 1, "table_width must be >= 1");
+  REQUIRE(num_seqs <= 1 || table_stride >= table_width, "table_stride must be >= table_width");
+  REQUIRE(num_seqs == 0 || (lengths != nullptr && new_tokens != nullptr && block_table != nullptr),
+          "null lengths, new_tokens or block_table");
+  REQUIRE(num_free == 0 || free_pages != nullptr, "null free_pages");
+  REQUIRE(starts != nullptr && pages != nullptr, "null starts or pages");
+  REQUIRE(capacity == 0 || (slots != nullptr && row_lengths != nullptr && row_seqs != nullptr),
+          "null slots, row_lengths or row_seqs");
+  for (const void* p : {(const void*)lengths, (const void*)new_tokens, (const void*)free_pages,
+                        (const void*)block_table, (const void*)starts, (const void*)slots, (const void*)row_lengths,
+                        (const void*)row_seqs, (const void*)pages})
+    REQUIRE(aligned(p, 4), "all arrays must be 4-byte aligned");
+  rrt::LayoutParams p{lengths, new_tokens, free_pages, block_table, starts, slots, row_lengths, row_seqs, pages,
+                      table_stride, num_seqs, num_free, table_width, page_size, capacity};
+  const int64_t grid = std::min<int64_t>(std::max<int64_t>(1, ceil_div(capacity, 256)), 512);
+  return launch(rrt::layout_kernel_ptr(), grid, 256, &p, stream, "paged_layout");
+}
+
+int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* parts, int32_t num_parts,
+                 int32_t page_size, int32_t num_pages, paged_dtype dtype, paged_dtype store, hipStream_t stream) {
+  if (int rc = check_types(dtype, store)) return rc;
+  REQUIRE(num_tokens >= 0, "num_tokens must be >= 0");
+  REQUIRE(num_parts == 1 || num_parts == 2, "num_parts must be 1 or 2");
+  REQUIRE(parts != nullptr, "null parts");
+  REQUIRE(page_size >= 1 && num_pages >= 0, "page_size must be >= 1 and num_pages >= 0");
+  rrt::AppendParams p{};
+  const int64_t sz = store == PAGED_E4M3 ? 1 : 2;
+  bool wide = true;
+  for (int i = 0; i < num_parts; ++i) {
+    const paged_part& q = parts[i];
+    REQUIRE(q.width >= 1 && q.head_width >= 1 && q.width % q.head_width == 0,
+            "a part's head_width must divide its width, both >= 1");
+    REQUIRE(q.src_stride >= 0 && q.dst_page_stride >= 0 && q.dst_token_stride >= 0 && q.dst_head_stride >= 0,
+            "strides must be >= 0");
+    REQUIRE(store == PAGED_E4M3 || q.scales == nullptr, "scales belong to an e4m3 cache");
+    REQUIRE(aligned(q.src, 2) && aligned(q.dst, (uintptr_t)sz) && aligned(q.scales, 4),
+            "a part's pointers must be aligned to their elements");
+    if (num_tokens > 0 && num_pages > 0) REQUIRE(q.src != nullptr && q.dst != nullptr, "null src or dst of a part");
+    // 16-byte loads, and stores of as many elements.
+    wide = wide && aligned(q.src, 16) && q.src_stride % 8 == 0 && aligned(q.dst, 8 * sz) && q.head_width % 8 == 0 &&
+           q.dst_page_stride % 8 == 0 && q.dst_token_stride % 8 == 0 && q.dst_head_stride % 8 == 0;
+    p.part[i] = q;
+  }
+  if (num_tokens == 0 || num_pages == 0) return TOPK_OK;
+  REQUIRE(slots != nullptr && aligned(slots, 4), "slots must be 4-byte aligned and not null");
+  for (int i = 0; i < num_parts; ++i) p.chunks[i] = wide ? parts[i].width / 8 : parts[i].width;
+  REQUIRE((int64_t)p.chunks[0] + p.chunks[1] <= INT32_MAX, "a token's parts are too wide");
+  p.slots = slots;
+  p.num_tokens = num_tokens;
+  p.page_size = page_size;
+  p.num_slots = (int64_t)num_pages * page_size;
+  const int64_t items = (int64_t)num_tokens * (p.chunks[0] + p.chunks[1]);
+  const int64_t grid = std::min<int64_t>(ceil_div(items, 256), 1 << 16);
+  return launch(rrt::append_kernel_ptr(dtype, store, wide), grid, 256, &p, stream, "paged_append");
+}
+
+int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes) {
+  REQUIRE(bytes != nullptr, "null bytes");
+  AttnPlan plan;
+  if (int rc = plan_attention(args, false, stream, &plan)) return rc;
+  *bytes = plan.bytes;
+  return TOPK_OK;
+}
+
+int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream) {
+  return run_attention(args, false, workspace, stream);
+}
+
+int64_t paged_debug_place(const int32_t* table_row, int32_t page_size, int32_t num_pages, int64_t page_stride,
+                          int64_t token_stride, int32_t pos) {
+  return rrt::locate(table_row, page_size, num_pages, page_stride, token_stride, pos);
+}
+
+void paged_debug_split(int32_t n, int32_t most, int32_t least, int32_t unit, int32_t out[2]) {
+  const rrt::Split s = rrt::split_of(n, most, least, unit);
+  out[0] = s.parts;
+  out[1] = s.chunk;
+}
+
+}  // extern "C"

@@ -1,0 +1,109 @@
+// Launch parameters shared by the host side and the kernels of the paged
+// cache (layout, append, attention, latent attention, latent prefill).  Not
+// part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+#include "paged_attention.h"
+
+namespace rrt {
+
+// Defined beside topk_ragged's host code: sets the thread's error text and
+// returns code; the stream's device with its CU count.
+int set_error(int code, const char* msg);
+int device_of_stream(hipStream_t stream, int* dev, int* num_cus);
+
+// ---------------------------------------------------------------------------
+// Arithmetic that host and kernels must agree on
+// ---------------------------------------------------------------------------
+
+#define RRT_HD __host__ __device__ __forceinline__
+
+RRT_HD int32_t clamp_to(int32_t x, int64_t most) {
+  return x < 0 ? 0 : (int64_t)x > most ? (int32_t)most : x;
+}
+
+// Longest context a table row can hold; at most 2^30 positions, so that sums
+// of a position and a tile stay in int32.
+constexpr int32_t kMostTokens = 1 << 30;
+RRT_HD int64_t table_tokens(int32_t width, int32_t page_size) {
+  const int64_t n = (int64_t)width * page_size;
+  return n > kMostTokens ? kMostTokens : n;
+}
+
+// Place of position pos in the pool, in elements, or -1 where the table holds
+// no page of it.  The caller keeps 0 <= pos < table_width * page_size.
+RRT_HD int64_t locate(const int32_t* table_row, int32_t page_size, int32_t num_pages, int64_t page_stride,
+                      int64_t token_stride, int32_t pos) {
+  const uint32_t j = (uint32_t)pos / (uint32_t)page_size;
+  const int32_t page = table_row[j];
+  if ((uint32_t)page >= (uint32_t)num_pages) return -1;
+  return (int64_t)page * page_stride + (int64_t)((uint32_t)pos - j * (uint32_t)page_size) * token_stride;
+}
+
+// How a row of n positions is split: `parts` parts of `chunk` positions (the
+// last one shorter), chunk a multiple of `unit`, parts <= most and no part
+// shorter than `least` positions except where n itself is (n = 0: one empty
+// part).  A function of the row's own length, so a ragged batch's short rows
+// are not cut into parts that are too small to be worth a join.  n is at most
+// kMostTokens.
+struct Split {
+  int32_t parts, chunk;
+};
+RRT_HD Split split_of(int32_t n, int32_t most, int32_t least, int32_t unit) {
+  int32_t parts = n / least;
+  if (parts > most) parts = most;
+  if (parts < 1) parts = 1;
+  const int64_t per = ((int64_t)n + parts - 1) / parts;
+  int64_t chunk = (per + unit - 1) / unit * unit;
+  if (chunk < unit) chunk = unit;
+  parts = (int32_t)(((int64_t)n + chunk - 1) / chunk);
+  return {parts < 1 ? 1 : parts, (int32_t)chunk};
+}
+
+// ---------------------------------------------------------------------------
+// Kernel parameters
+// ---------------------------------------------------------------------------
+
+struct LayoutParams {
+  const int32_t* lengths;
+  const int32_t* new_tokens;
+  const int32_t* free_pages;
+  int32_t* table;
+  int32_t *starts, *slots, *row_lengths, *row_seqs, *pages;
+  int64_t table_stride;
+  int32_t num_seqs, num_free, table_width, page_size, capacity;
+};
+
+struct AppendParams {
+  const int32_t* slots;
+  paged_part part[2];
+  int32_t chunks[2];  // work items per token of each part
+  int32_t num_tokens, page_size;
+  int64_t num_slots;
+};
+
+struct AttnParams {
+  paged_attention_args a;
+  float* part_out;     // [rows, heads, most, head_dim], unnormalised
+  float2* part_stat;   // [rows, heads, most]: maximum (base-2 logarithm) and sum
+  float scale_log2;    // softmax_scale * log2(e)
+  int32_t most;        // parts a row is split into, at most
+  int32_t least;       // fewest positions of a part
+  int32_t unit;        // a part's positions are a multiple of this
+  int32_t groups;      // units of work along the rows: sequences, or rows
+  int32_t group_rows;  // rows of a group: next_n, or 1
+  int32_t col_tiles;   // column tiles of a key-value head
+};
+
+// Kernel lookup: nullptr if there is no such instance.
+const void* layout_kernel_ptr();
+const void* append_kernel_ptr(int dtype, int store, bool wide);
+const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int tiles);
+const void* join_kernel_ptr(int dtype, int head_dim);
+
+}  // namespace rrt

@@ -11,6 +11,7 @@
 #include <atomic>
 #include <string>
 
+#include "paged_internal.h"
 #include "topk_internal.h"
 #include "topk_ragged.h"
 
@@ -558,6 +559,20 @@ int launch(const void* scores, int64_t row_stride, const int32_t* lengths, const
 }
 
 }  // namespace
+
+namespace rrt {
+
+int set_error(int code, const char* msg) { return fail(code, msg); }
+
+int device_of_stream(hipStream_t stream, int* dev, int* num_cus) {
+  if (int rc = stream_device(stream, dev)) return rc;
+  DevCache* d = nullptr;
+  if (int rc = device_info(*dev, &d)) return rc;
+  *num_cus = d->num_cus.load(std::memory_order_relaxed);
+  return TOPK_OK;
+}
+
+}  // namespace rrt
 
 extern "C" {
 
