@@ -3,9 +3,10 @@
  * attention over it, on AMD Instinct MI355X (gfx950).
  *
  * One serving step of sparse attention: paged_layout gives new tokens their
- * pages and slots, paged_append writes them, topk_ragged
- * chooses positions from the indexer's scores, and paged_attention reads the
- * chosen positions (or all of them).
+ * pages and slots, paged_append / latent_append write them, topk_ragged
+ * chooses positions from the indexer's scores, and paged_attention /
+ * latent_attention read the chosen positions (or all of them).
+ * latent_prefill attends a chunk of new tokens over its context.
  *
  * Conventions, as in topk_ragged.h:
  *   - All data pointers are DEVICE pointers owned by the caller.  The library
@@ -161,6 +162,61 @@ typedef struct {
 
 int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes);
 int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream);
+
+/*
+ * latent_attention -- the absorbed form: every head reads one shared latent
+ * vector a token, keys c[0 .. head_dim + 64), values c[0 .. head_dim):
+ * out = softmax(softmax_scale * q c^T) c.  Arguments as for paged_attention
+ * with k the cache [num_pages, page_size, head_dim + 64], v, v_scales and
+ * num_kv_heads ignored, q [num_rows, num_heads, head_dim + 64] and out
+ * [num_rows, num_heads, head_dim].  head_dim is 256 or 512.
+ */
+int latent_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes);
+int latent_attention(const paged_attention_args* args, void* workspace, hipStream_t stream);
+
+/*
+ * latent_prefill -- the expanded form for chunks of new tokens: head h has
+ * the keys [w_k[h] c, c_rope] and the values w_v[h] c, c the latent vectors of
+ * the sequence's whole context in the paged cache (the new tokens' included).
+ *
+ *   q              [num_tokens, num_heads, 192]: 128 for w_k c, 64 rope.
+ *   starts         int32 [num_seqs + 1]: sequence s owns tokens
+ *                  [starts[s], starts[s + 1]), starts[0] >= 0, ascending.
+ *                  Tokens outside every sequence are left as they were.
+ *   lengths        int32 [num_seqs], the context after the chunk: token j of
+ *                  a chunk of n sees positions [0, length - n + j].
+ *   w_k, w_v       [num_heads, 128, latent_dim] contiguous, of q's type.
+ *   context_tokens the most that the lengths add up to (each clamped to
+ *                  [0, table_width * page_size]).  A sequence that does not
+ *                  fit gets NaN in out and lse.
+ *   out, lse       [num_tokens, num_heads, 128] and [num_tokens, num_heads].
+ *   workspace      latent_prefill_workspace_size() bytes: the expanded keys
+ *                  and values, 512 bytes a token and head.
+ */
+typedef struct {
+  const void* q;
+  const void* cache;
+  const float* scale;        /* fp32 [1] or NULL; only with PAGED_E4M3 */
+  const void* w_k;
+  const void* w_v;
+  const int32_t* block_table;
+  const int32_t* starts;
+  const int32_t* lengths;
+  void* out;
+  float* lse;
+  int64_t q_row_stride, q_head_stride;
+  int64_t page_stride, token_stride;
+  int64_t table_stride;
+  int64_t context_tokens;
+  int32_t num_tokens, num_seqs, num_heads;
+  int32_t latent_dim;        /* 256 or 512 */
+  int32_t page_size, num_pages, table_width;
+  float softmax_scale;
+  paged_dtype dtype, store;
+} latent_prefill_args;
+
+int latent_prefill_workspace_size(const latent_prefill_args* args, hipStream_t stream, size_t* bytes);
+int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t stream);
 
 /* Arithmetic that the kernels share with the host (testing only; host
  * pointers).  paged_debug_place: the element offset of position pos in the

@@ -33,6 +33,8 @@ from .binding import (  # noqa: F401
 from .attention import (  # noqa: F401
     Layout,
     latent_append,
+    latent_attention,
+    latent_prefill,
     paged_append,
     paged_attention,
     paged_layout,

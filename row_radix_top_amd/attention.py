@@ -23,7 +23,8 @@ MAX_SPLITS = 128
 
 # Every symbol include/paged_attention.h declares.
 EXPORTED = (
-    "paged_layout", "paged_append", "paged_attention", "paged_attention_workspace_size",
+    "paged_layout", "paged_append", "paged_attention", "paged_attention_workspace_size", "latent_attention",
+    "latent_attention_workspace_size", "latent_prefill", "latent_prefill_workspace_size",
     "paged_debug_place", "paged_debug_split",
 )
 
@@ -43,6 +44,15 @@ class AttentionArgs(ctypes.Structure):
                 ("num_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32),
                 ("num_pages", _i32), ("table_width", _i32), ("num_chosen", _i32), ("softmax_scale", _f32),
                 ("dtype", _i32), ("store", _i32), ("max_splits", _i32)]
+
+
+class PrefillArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("cache", _vp), ("scale", _vp), ("w_k", _vp), ("w_v", _vp), ("block_table", _vp),
+                ("starts", _vp), ("lengths", _vp), ("out", _vp), ("lse", _vp), ("q_row_stride", _i64),
+                ("q_head_stride", _i64), ("page_stride", _i64), ("token_stride", _i64), ("table_stride", _i64),
+                ("context_tokens", _i64), ("num_tokens", _i32), ("num_seqs", _i32), ("num_heads", _i32),
+                ("latent_dim", _i32), ("page_size", _i32), ("num_pages", _i32), ("table_width", _i32),
+                ("softmax_scale", _f32), ("dtype", _i32), ("store", _i32)]
 
 
 class Layout(NamedTuple):
@@ -66,7 +76,8 @@ def load() -> ctypes.CDLL:
         lib.paged_layout.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                      _vp]
         lib.paged_append.argtypes = [_vp, _i32, ctypes.POINTER(Part), _i32, _i32, _i32, _i32, _i32, _vp]
-        for name, args in (("paged_attention", AttentionArgs),):
+        for name, args in (("paged_attention", AttentionArgs), ("latent_attention", AttentionArgs),
+                           ("latent_prefill", PrefillArgs)):
             if not hasattr(lib, name):
                 continue
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp, _vp]
@@ -366,3 +377,72 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, s
         _check(lib.paged_attention(ctypes.byref(a), ws, sp), "paged_attention")
     return out, lse
 
+
+def latent_attention(q, cache, block_table, lengths, *, softmax_scale: float, chosen=None, scale=None,
+                     next_n: int | None = None, out=None, lse=None, workspace=None, max_splits: int = 0, stream=None):
+    """The absorbed form of latent attention: every head of q [num_rows,
+    num_heads, latent_dim + 64] reads the shared vectors of cache [num_pages,
+    page_size, latent_dim + 64] as keys and their first latent_dim values as
+    values; latent_dim 256 or 512.  Returns (out [num_rows, num_heads,
+    latent_dim], lse).  Other arguments as for paged_attention; scale:
+    float32 [1] of a float8_e4m3fn cache."""
+    device = q.device
+    with _on(stream, device):
+        if cache.dim() != 3:
+            raise ValueError("cache must be [num_pages, page_size, latent_dim + 64]")
+        dim = cache.shape[2]
+        a, out, lse = _attention_args(q, cache, lengths, block_table, chosen, next_n, softmax_scale, dim,
+                                      dim - ROPE_DIM, out, lse, max_splits)
+        a.k_scales = _scales(scale, "scale", device, 1, a.store)
+        lib, sp = load(), _stream(device)
+        ws, _keep = _workspace(lib.latent_attention_workspace_size, a, workspace, device, "latent_attention", sp)
+        _check(lib.latent_attention(ctypes.byref(a), ws, sp), "latent_attention")
+    return out, lse
+
+
+def latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, *, context_tokens: int, softmax_scale: float,
+                   scale=None, out=None, lse=None, workspace=None, stream=None):
+    """The expanded form for chunks of new tokens: causal attention of q
+    [num_tokens, num_heads, 192] over each sequence's whole context, whose
+    keys [w_k c, rope] and values w_v c are formed from the latent vectors in
+    the paged cache.  starts: int32 [num_seqs + 1], lengths: int32 [num_seqs],
+    both as paged_layout gives and takes them; w_k, w_v: [num_heads, 128,
+    latent_dim]; context_tokens: at least the sum of the lengths.  Returns
+    (out [num_tokens, num_heads, 128], lse).  See paged_attention.h."""
+    import torch
+    device = q.device
+    with _on(stream, device):
+        code, store = _code(q, "q"), _code(cache, "cache", True)
+        if store != 2 and cache.dtype != q.dtype:
+            raise TypeError("cache must have q's type or float8_e4m3fn")
+        if q.dim() != 3 or q.shape[2] != HEAD_DIM + ROPE_DIM or q.stride(2) != 1:
+            raise ValueError(f"q must be [num_tokens, num_heads, {HEAD_DIM + ROPE_DIM}], its last stride 1")
+        if cache.dim() != 3 or cache.stride(2) != 1 or cache.device != device:
+            raise ValueError("cache must be [num_pages, page_size, latent_dim + 64] on q's device, its last stride 1")
+        tokens, heads, dim = q.shape[0], q.shape[1], cache.shape[2] - ROPE_DIM
+        for w, name in ((w_k, "w_k"), (w_v, "w_v")):
+            _like(w, name, device, q.dtype, (heads, HEAD_DIM, dim))
+        n = lengths.numel()
+        a = PrefillArgs()
+        a.q, a.cache, a.w_k, a.w_v = q.data_ptr(), cache.data_ptr(), w_k.data_ptr(), w_v.data_ptr()
+        a.lengths, a.starts = _ints(lengths, "lengths", device), _ints(starts, "starts", device, (n + 1,))
+        a.block_table = _matrix(block_table, "block_table", device, n)
+        a.scale = _scales(scale, "scale", device, 1, store)
+        if out is None:
+            out = torch.empty((tokens, heads, HEAD_DIM), dtype=q.dtype, device=device)
+        else:
+            _like(out, "out", device, q.dtype, (tokens, heads, HEAD_DIM))
+        if lse is None:
+            lse = torch.empty((tokens, heads), dtype=torch.float32, device=device)
+        else:
+            _like(lse, "lse", device, torch.float32, (tokens, heads))
+        a.out, a.lse = out.data_ptr(), lse.data_ptr()
+        a.q_row_stride, a.q_head_stride = q.stride(0), q.stride(1)
+        a.page_stride, a.token_stride, a.table_stride = cache.stride(0), cache.stride(1), block_table.stride(0)
+        a.context_tokens, a.num_tokens, a.num_seqs, a.num_heads, a.latent_dim = context_tokens, tokens, n, heads, dim
+        a.num_pages, a.page_size, a.table_width = cache.shape[0], cache.shape[1], block_table.shape[1]
+        a.softmax_scale, a.dtype, a.store = softmax_scale, code, store
+        lib, sp = load(), _stream(device)
+        ws, _keep = _workspace(lib.latent_prefill_workspace_size, a, workspace, device, "latent_prefill", sp)
+        _check(lib.latent_prefill(ctypes.byref(a), ws, sp), "latent_prefill")
+    return out, lse

@@ -38,6 +38,13 @@ HIP_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
+# Files of matrix kernels: accumulators in the general half of the register
+# file, which leaves the other half to operands that only matrix instructions
+# read.  Without it, rescaling an accumulator anywhere in a loop moves all of
+# them between the halves on every pass.
+MATRIX_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+MATRIX_FILES = ("paged_attention.hip", "latent_attention.hip", "latent_prefill.hip")
+
 
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
@@ -48,6 +55,8 @@ def hipcc() -> str:
 
 def _compile(src: str, extra: list[str], verbose: bool) -> tuple[str, float]:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
+    if os.path.basename(src) in MATRIX_FILES:
+        extra = [*MATRIX_FLAGS, *extra]
     cmd = [hipcc(), *HIP_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", src, "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)

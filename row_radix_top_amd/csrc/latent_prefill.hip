@@ -1,0 +1,482 @@
+// The expanded form of latent attention: keys and values of every head formed
+// from the latent vectors of the context, then causal attention over them.
+
+#include "paged_device.hpp"
+
+namespace rrt {
+
+// ---------------------------------------------------------------------------
+// Two kernels.  `expand` forms k_h = W_k,h c and v_h = W_v,h c for every
+// context token and head (2 DC 256 flop each) and leaves them in the workspace
+// in fragment order: 1 KB blocks that are, lane by lane, the operands that the
+// attention's matrix instructions take.  `prefill` streams them through LDS
+// with plain linear copies, and no operand needs a shuffle, a transpose or a
+// swizzle there.
+//
+// A context tile is 64 tokens.  With tb = token / 32, half = lane / 32:
+//   key block (tb, s):   lane holds token tb*32 + lane % 32, dims s*16 + half*8 .. +8
+//   value block (tb, ks, db): lane holds dim db*32 + lane % 32, tokens
+//     tb*32 + ks*16 + half*4 + {0..3, 8..11}: the tokens whose weights the lane
+//     holds after S^T = K Q^T, so the weights go from one product into the
+//     next without leaving the lane.
+// The expanded keys and values are rounded to the 16-bit type, as a program
+// that keeps them would; that is the operator's own rounding beside those of
+// the weights and the output.
+// ---------------------------------------------------------------------------
+constexpr int kExpandBlock = 256;
+constexpr int kHead = PAGED_HEAD_DIM;
+constexpr int kRopeDim = PAGED_ROPE_DIM;
+constexpr int kBlock16 = 1024;                              // bytes of a block
+constexpr int kKeyTile = 16 * kBlock16, kRopeTile = 8 * kBlock16, kValueTile = 16 * kBlock16;
+
+using lds_u32x4 = __attribute__((address_space(3))) u32x4;
+
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) { return *(lds_u32x4*)at; }
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
+                                   (__attribute__((address_space(3))) uint32_t*)(uintptr_t)to, 16, 0, 0);
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ int32_t context_of(const PrefillParams& p, int32_t s) {
+  return clamp_to(p.a.lengths[s], table_tokens(p.a.table_width, p.a.page_size));
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t per) { return (int32_t)(((int64_t)n + per - 1) / per); }
+
+__device__ __forceinline__ int32_t scan_up(int32_t x, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int32_t y = __shfl_up(x, off);
+    if (lane >= off) x += y;
+  }
+  return x;
+}
+
+// The sequence that context tile `tile` belongs to and the tiles before that
+// sequence; -1 if the tile lies past the last sequence.  All lanes take part.
+__device__ __forceinline__ int32_t sequence_of_tile(const PrefillParams& p, int32_t tile, int lane, int32_t* before) {
+  int32_t base = 0;
+  for (int32_t s0 = 0; s0 < p.a.num_seqs; s0 += 64) {
+    const int32_t mine = s0 + lane < p.a.num_seqs ? tiles_of(context_of(p, s0 + lane), kCtxTile) : 0;
+    const int32_t upto = base + scan_up(mine, lane);
+    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > tile);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      *before = __builtin_amdgcn_readlane(upto - mine, l);
+      return s0 + l;
+    }
+    base = __builtin_amdgcn_readlane(upto, 63);
+  }
+  return -1;
+}
+
+// ---------------------------------------------------------------------------
+// Expansion: one head's 128 keys and 128 values for two context tiles a
+// workgroup.  Wavefronts 0 and 1 form the keys of a tile each, 2 and 3 the
+// values.  Latent vectors and weights pass through LDS in slices of 64 of the
+// summed dims, two slices deep, 16-byte chunks at c ^ (row / 2 % 8).
+// ---------------------------------------------------------------------------
+template <typename T, bool F8, int DC>
+__global__ void __launch_bounds__(kExpandBlock, 1) expand_kernel(PrefillParams p) {
+  constexpr int SL = 64;             // dims of a slice
+  constexpr int NS = DC / SL;
+  constexpr int TOK = 2 * kCtxTile;  // tokens of a workgroup
+  __shared__ __align__(1024) uint16_t sx[2][TOK * SL];
+  __shared__ __align__(1024) uint16_t sw[2][2 * kHead * SL];
+  __shared__ int64_t splace[TOK];
+  const latent_prefill_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t head = (int32_t)(blockIdx.x % (uint32_t)a.num_heads);
+  const int32_t tile0 = (int32_t)(blockIdx.x / (uint32_t)a.num_heads) * 2;
+
+  // Places of the tokens: wavefronts 0 and 1 find a tile's each.
+  if (w < 2) {
+    int64_t off = -1;
+    int32_t before = 0;
+    const int32_t tile = tile0 + w;
+    const int32_t s = tile < p.capacity ? sequence_of_tile(p, tile, lane, &before) : -1;
+    if (s >= 0) {
+      const int32_t pos = (tile - before) * kCtxTile + lane;
+      if (pos < context_of(p, s))
+        off = locate(a.block_table + (int64_t)s * a.table_stride, a.page_size, a.num_pages, a.page_stride,
+                     a.token_stride, pos);
+      const uint64_t bits = __builtin_amdgcn_ballot_w64(off >= 0);
+      if (head == 0 && lane == 0) p.valid[tile] = bits;
+    }
+    splace[w * 64 + lane] = s < 0 ? -2 : off;
+  }
+  __syncthreads();
+  const bool real[2] = {splace[0] != -2, splace[64] != -2};
+  if (!real[0] && !real[1]) return;
+
+  // Slice k of the weights (256 rows) and of the latent vectors (128 rows).
+  constexpr int SZ = F8 ? 1 : 2;
+  const char* cache = (const char*)a.cache;
+  const char* wk = (const char*)a.w_k + (int64_t)head * kHead * DC * 2;
+  const char* wv = (const char*)a.w_v + (int64_t)head * kHead * DC * 2;
+  u32x2 stage[4];
+  auto issue = [&](int k, int b) {
+    const int r8 = lane >> 3, c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // 32 blocks of 8 weight rows
+      const int row = (w * 8 + i) * 8 + r8;
+      const char* from = (row < kHead ? wk + row * (DC * 2) : wv + (row - kHead) * (DC * 2)) + k * (SL * 2);
+      load_to_lds(from + ((c ^ ((row >> 1) & 7)) * 16), lds_at(&sw[b][(w * 8 + i) * 8 * SL]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 16 blocks of 8 tokens
+      const int row = (w * 4 + i) * 8 + r8;
+      const int64_t off = splace[row];
+      const char* from = cache + (off < 0 ? 0 : off) * SZ + k * (SL * SZ);
+      if constexpr (F8) {
+        stage[i] = *(const u32x2*)(from + c * 8);
+      } else {
+        load_to_lds(from + ((c ^ ((row >> 1) & 7)) * 16), lds_at(&sx[b][(w * 4 + i) * 8 * SL]));
+      }
+    }
+  };
+  auto store = [&](int b) {
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (w * 4 + i) * 8 + (lane >> 3), c = lane & 7;
+        ((u32x4*)&sx[b][row * SL])[c ^ ((row >> 1) & 7)] = widen<T>(stage[i]);
+      }
+    }
+  };
+  // Tokens that are not there count as zeros.
+  auto clear = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (w * 4 + i) * 8 + (lane >> 3);
+      if (splace[row] < 0) ((u32x4*)&sx[b][row * SL])[lane & 7] = u32x4{0, 0, 0, 0};
+    }
+  };
+
+  f32x16 acc[2][4];  // [block of 32 tokens][block of 32 dims]
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) acc[t][d] = f32x16{};
+  const bool keys = w < 2;
+  const int tile_in = w & 1;
+  issue(0, 0);
+  store(0);
+  for (int k = 0; k < NS; ++k) {
+    const int b = k & 1;
+    wait_loads();
+    clear(b);
+    __syncthreads();
+    if (k + 1 < NS) issue(k + 1, b ^ 1);
+    const uint32_t xrow = lds_at(&sx[b][0]) + (uint32_t)(tile_in * 64 + (lane & 31)) * (SL * 2);
+    const uint32_t wrow = lds_at(&sw[b][0]) + (uint32_t)((keys ? 0 : kHead) + (lane & 31)) * (SL * 2);
+#pragma unroll
+    for (int s = 0; s < SL / 16; ++s) {
+      const uint32_t c = (uint32_t)((s * 2 + half) ^ ((lane >> 1) & 7)) * 16;
+      u32x4 x[2], y[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) x[t] = lds_read16(xrow + t * (32 * SL * 2) + c);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) y[d] = lds_read16(wrow + d * (32 * SL * 2) + c);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[t][d] = keys ? T::mfma32(y[d], x[t], acc[t][d]) : T::mfma32(x[t], y[d], acc[t][d]);
+    }
+    if (k + 1 < NS) store(b ^ 1);
+  }
+
+  const float by = F8 && a.scale != nullptr ? a.scale[0] : 1.0f;
+  const int32_t tile = tile0 + tile_in;
+  if (real[tile_in]) {
+    if (keys) {
+      char* to = p.keys + ((int64_t)head * p.capacity + tile) * kKeyTile + (lane & 31) * 16 + half * 8;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // dims d*32 + j*8 + half*4 .. +4 of the lane's token
+            const f32x16& x = acc[t][d];
+            *(u32x2*)(to + (t * 8 + d * 2 + (j >> 1)) * kBlock16 + (j & 1) * 512) =
+                u32x2{T::pack(x[j * 4] * by, x[j * 4 + 1] * by), T::pack(x[j * 4 + 2] * by, x[j * 4 + 3] * by)};
+          }
+    } else {
+      char* to = p.values + ((int64_t)head * p.capacity + tile) * kValueTile + lane * 16;
+      bool bad = false;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              x[e] = acc[t][d][ks * 8 + e] * by;
+              bad = bad || !(fabsf(x[e]) <= T::kLargest);
+            }
+            *(u32x4*)(to + ((t * 2 + ks) * 4 + d) * kBlock16) =
+                u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
+          }
+      const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
+      if (lane == 0) p.flags[(int64_t)head * p.capacity + tile] = any != 0 ? 1u : 0u;
+    }
+  }
+  // Rope parts, copied once for all heads: wavefront w takes 32 tokens.
+  if (head == 0) {
+    const int32_t rtile = tile0 + (w >> 1);
+    if (real[w >> 1]) {
+      const int64_t off = splace[w * 32 + (lane & 31)];
+      const char* from = cache + (off < 0 ? 0 : off) * SZ + DC * SZ;
+      char* to = p.ropes + (int64_t)rtile * kRopeTile + (w & 1) * (4 * kBlock16) + lane * 16;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u32x4 x;
+        if constexpr (F8) {
+          x = widen<T>(*(const u32x2*)(from + s * 16 + half * 8));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = T::pack(T::lo(x[i]) * by, T::hi(x[i]) * by);
+        } else {
+          x = *(const u32x4*)(from + s * 32 + half * 16);
+        }
+        *(u32x4*)(to + s * kBlock16) = off < 0 ? u32x4{0, 0, 0, 0} : x;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention of 128 query rows of one head a workgroup, 32 a wavefront, over
+// the context's tiles in order; two tiles in LDS, one being loaded and one in
+// use.  S^T and O^T keep a query row in a lane (and the lane 32 further), so
+// the maximum takes one exchange and everything else none.  The reference of
+// the weights moves only when a score passes it by 2^8 (see the absorbed
+// form); keys past a row's end are masked in the tiles that cross it.
+// ---------------------------------------------------------------------------
+constexpr int kRows = 128;
+constexpr float kLazyStep = 8.0f;
+constexpr int kAheadBlocks = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
+  constexpr int TILE = kKeyTile + kRopeTile + kValueTile;  // 40 KB
+  __shared__ __align__(1024) char sm[2][TILE];
+  const latent_prefill_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t head = (int32_t)(blockIdx.x % (uint32_t)a.num_heads);
+  const int32_t want = (int32_t)(blockIdx.x / (uint32_t)a.num_heads);
+
+  // The sequence of this query tile, its tile within the sequence (the last
+  // one first: it has the most work) and the context tiles before it.
+  int32_t seq = -1, local = 0, tile0 = 0, start = 0, count = 0;
+  {
+    int32_t rows_base = 0, ctx_base = 0;
+    for (int32_t s0 = 0; s0 < a.num_seqs; s0 += 64) {
+      const int32_t s = s0 + lane;
+      int32_t from = 0, n = 0, ctx = 0;
+      if (s < a.num_seqs) {
+        from = clamp_to(a.starts[s], a.num_tokens);
+        n = clamp_to(a.starts[s + 1], a.num_tokens) - from;
+        n = n < 0 ? 0 : n;
+        ctx = tiles_of(context_of(p, s), kCtxTile);
+      }
+      const int32_t mine = tiles_of(n, kRows);
+      const int32_t upto = rows_base + scan_up(mine, lane), cupto = ctx_base + scan_up(ctx, lane);
+      const uint64_t past = __builtin_amdgcn_ballot_w64(upto > want);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        seq = s0 + l;
+        local = __builtin_amdgcn_readlane(upto, l) - 1 - want;
+        tile0 = __builtin_amdgcn_readlane(cupto - ctx, l);
+        start = __builtin_amdgcn_readlane(from, l);
+        count = __builtin_amdgcn_readlane(n, l);
+        break;
+      }
+      rows_base = __builtin_amdgcn_readlane(upto, 63);
+      ctx_base = __builtin_amdgcn_readlane(cupto, 63);
+    }
+  }
+  if (seq < 0) return;
+  const int32_t ctx = context_of(p, seq);
+  const int32_t row0 = local * kRows;  // first row of the tile, within the chunk
+  const bool fits = (int64_t)tile0 + tiles_of(ctx, kCtxTile) <= p.capacity;
+
+  // Row of this lane; how many positions it sees (0 for rows past the chunk).
+  const int32_t j = row0 + w * 32 + (lane & 31);
+  const bool real = j < count;
+  const int32_t sees = real ? (ctx - count + j + 1 < 0 ? 0 : ctx - count + j + 1) : 0;
+  const int32_t last = row0 + kRows < count ? row0 + kRows : count;  // rows of the tile end here
+  const int32_t longest = ctx - count + last;                        // positions its last row sees
+  const int32_t tiles = longest > 0 && fits ? tiles_of(longest, kCtxTile) : 0;
+  // Positions that all rows of the wavefront see, and that any of them does.
+  const int32_t wfirst = row0 + w * 32, wlast = wfirst + 31 < count - 1 ? wfirst + 31 : count - 1;
+  const int32_t all_see = wfirst < count ? ctx - count + wfirst + 1 : 0;
+  const int32_t any_see = wfirst < count ? ctx - count + wlast + 1 : 0;
+
+  u32x4 q[12];
+  {
+    const char* qp = (const char*)a.q + 2 * ((int64_t)(start + (real ? j : row0)) * a.q_row_stride + (int64_t)head * a.q_head_stride);
+#pragma unroll
+    for (int s = 0; s < 12; ++s) q[s] = *(const u32x4*)(qp + s * 32 + half * 16);
+  }
+
+  const char* kp = p.keys + ((int64_t)head * p.capacity + tile0) * kKeyTile;
+  const char* rp = p.ropes + (int64_t)tile0 * kRopeTile;
+  const char* vp = p.values + ((int64_t)head * p.capacity + tile0) * kValueTile;
+  auto issue = [&](int32_t i, int b) {
+    // 40 blocks, ten a wavefront: keys, rope parts, values as they lie.
+#pragma unroll
+    for (int k = 0; k < 10; ++k) {
+      const int blk = k * 4 + w;
+      const char* from = k < 4 ? kp + (int64_t)i * kKeyTile + blk * kBlock16
+                       : k < 6 ? rp + (int64_t)i * kRopeTile + (blk - 16) * kBlock16
+                               : vp + (int64_t)i * kValueTile + (blk - 24) * kBlock16;
+      load_to_lds(from + lane * 16, lds_at(&sm[b][blk * kBlock16]));
+    }
+  };
+
+  float ref = -INFINITY, sum = 0.0f;
+  f32x16 o[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = f32x16{};
+  if (tiles > 0) issue(0, 0);
+
+  for (int32_t i = 0; i < tiles; ++i) {
+    const int b = i & 1;
+    wait_loads();
+    __syncthreads();
+    if (i + 1 < tiles) issue(i + 1, b ^ 1);
+    const int32_t t0 = i * kCtxTile;
+    if (t0 >= any_see) continue;  // nothing here for this wavefront
+    const uint32_t base = lds_at(&sm[b][0]) + (uint32_t)lane * 16;
+    auto key = [&](int n) {  // n: token block * 12 + step
+      const int tb = n / 12, s = n % 12;
+      return lds_read16(base + (s < 8 ? (tb * 8 + s) * kBlock16 : kKeyTile + (tb * 4 + s - 8) * kBlock16));
+    };
+    f32x16 s[2] = {f32x16{}, f32x16{}};
+    u32x4 kk[kAheadBlocks];
+#pragma unroll
+    for (int n = 0; n < kAheadBlocks - 1; ++n) kk[n] = key(n);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 24; ++n) {
+      if (n + kAheadBlocks - 1 < 24) kk[(n + kAheadBlocks - 1) % kAheadBlocks] = key(n + kAheadBlocks - 1);
+      s[n / 12] = T::mfma32(kk[n % kAheadBlocks], q[n % 12], s[n / 12]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const uint64_t valid = p.valid[tile0 + i];
+    const bool masked = t0 + kCtxTile > all_see || valid != ~0ull;
+    float top = -INFINITY;
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+      s[tb] *= p.scale_log2;
+      if (masked) {
+        const uint32_t bits = (uint32_t)(valid >> (tb * 32)) >> (half * 4);
+        const int32_t left = sees - t0 - tb * 32 - half * 4;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int t = (e >> 2) * 8 + (e & 3);
+          s[tb][e] = t < left && ((bits >> t) & 1u) != 0 ? s[tb][e] : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[tb][e]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__builtin_amdgcn_ballot_w64(top > ref + kLazyStep) != 0) {
+      const float m = fmaxf(ref, top);
+      const float by = m == ref ? 1.0f : exp2_fast(ref - m);
+      ref = m;
+      sum *= by;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= by;
+    }
+    const float r = ref == -INFINITY ? 0.0f : ref;
+    u32x4 pw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = exp2_fast(s[k >> 1][(k & 1) * 8 + e] - r);
+        sum += x[e];
+      }
+      pw[k] = u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
+    }
+    const uint32_t vbase = base + kKeyTile + kRopeTile;
+    if (masked && p.flags[(int64_t)head * p.capacity + tile0 + i] != 0) {
+      // Values that are not finite in a tile that not every row sees whole: one
+      // token at a time, into the rows that see it.
+      for (int32_t t = 0; t < kCtxTile; ++t) {
+        const int k = t >> 4, in = t & 15;  // block of 16 tokens; the token's half and element there
+        const bool mine = half == ((in >> 2) & 1);
+        const int e = (in >> 3) * 4 + (in & 3);
+        u32x4 keep = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (mine && (e >> 1) == c) keep[c] = (e & 1) ? 0xffff0000u : 0x0000ffffu;
+        u32x4 weight = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) weight = k == c ? pw[c] : weight;
+        weight &= keep;
+        const bool here = t0 + t < sees && ((valid >> t) & 1u) != 0;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const f32x16 x = T::mfma32(lds_read16(vbase + (k * 4 + d) * kBlock16) & keep, weight, o[d]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) o[d][c] = here ? x[c] : o[d][c];
+        }
+      }
+      continue;
+    }
+    u32x4 v[kAheadBlocks];
+    auto value = [&](int n) { return lds_read16(vbase + n * kBlock16); };
+#pragma unroll
+    for (int n = 0; n < kAheadBlocks - 1; ++n) v[n] = value(n);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      if (n + kAheadBlocks - 1 < 16) v[(n + kAheadBlocks - 1) % kAheadBlocks] = value(n + kAheadBlocks - 1);
+      o[n & 3] = T::mfma32(v[n % kAheadBlocks], pw[n >> 2], o[n & 3]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  sum += __shfl_xor(sum, 32);
+  if (!real) return;
+  const int64_t at = (int64_t)(start + j) * a.num_heads + head;
+  const float by = !fits ? NAN : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *(u32x2*)((uint16_t*)a.out + at * kHead + d * 32 + k * 8 + half * 4) =
+          u32x2{T::pack(o[d][k * 4] * by, o[d][k * 4 + 1] * by), T::pack(o[d][k * 4 + 2] * by, o[d][k * 4 + 3] * by)};
+  if (half == 0 && a.lse != nullptr)
+    a.lse[at] = !fits ? NAN : sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
+}
+
+namespace {
+template <typename T>
+const void* expand_dims(int store, int dim) {
+  if (dim == 256) return store == PAGED_E4M3 ? (const void*)&expand_kernel<T, true, 256> : (const void*)&expand_kernel<T, false, 256>;
+  if (dim == 512) return store == PAGED_E4M3 ? (const void*)&expand_kernel<T, true, 512> : (const void*)&expand_kernel<T, false, 512>;
+  return nullptr;
+}
+}  // namespace
+
+const void* expand_kernel_ptr(int dtype, int store, int latent_dim) {
+  return dtype == PAGED_BF16 ? expand_dims<Bf16>(store, latent_dim) : expand_dims<Fp16>(store, latent_dim);
+}
+const void* prefill_kernel_ptr(int dtype) {
+  return dtype == PAGED_BF16 ? (const void*)&prefill_kernel<Bf16> : (const void*)&prefill_kernel<Fp16>;
+}
+int prefill_rows() { return kRows; }
+
+}  // namespace rrt

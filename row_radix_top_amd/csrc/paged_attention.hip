@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
   __shared__ float so[4][16][LD];
   __shared__ float sm[4][16], sl[4][16];
   const paged_attention_args& a = p.a;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, col16 = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 
   const int32_t units = p.groups * a.num_kv_heads * p.col_tiles;
   const int32_t part = (int32_t)(blockIdx.x / (uint32_t)units);
@@ -133,13 +134,14 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
       jlo = j < jlo ? j : jlo;
       jhi = j > jhi ? j : jhi;
     }
-    const int32_t head = kvh * heads_per + (c - j * heads_per);
+    // Columns past the last one compute with the first head and see nothing.
+    const int32_t head = kvh * heads_per + (real ? c - j * heads_per : 0);
     const char* qp = (const char*)a.q + 2 * ((int64_t)(r0 + j) * a.q_row_stride + (int64_t)head * a.q_head_stride);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       // The dims that the lane's key words hold at matrix step i.
       const int dim = F8 ? (i >> 1) * 64 + g * 16 + (i & 1) * 8 : i * 32 + g * 8;
-      q[t][i] = real ? *(const u32x4*)(qp + 2 * dim) : u32x4{0, 0, 0, 0};
+      q[t][i] = *(const u32x4*)(qp + 2 * dim);
     }
   }
 #pragma unroll
@@ -160,14 +162,10 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
   const int32_t* chosen = CHOSEN ? a.chosen + (int64_t)r0 * a.chosen_stride : nullptr;
   const int32_t seen = CHOSEN ? clamp_to(a.lengths[r0], most) : 0;
 
-  // Place of the lane's token (both halves of the wavefront hold the same 32).
-  auto place = [&](int32_t t) -> int64_t {
-    const int32_t i = t + (lane & 31);
-    if (i >= end) return -1;
-    const int32_t pos = CHOSEN ? chosen[i] : i;
-    if (CHOSEN && (uint32_t)pos >= (uint32_t)seen) return -1;
-    return locate(table, a.page_size, a.num_pages, a.page_stride, a.token_stride, pos);
-  };
+  // Places of the lane's tokens (both halves of the wavefront hold the same
+  // 32); a part is never empty unless its row is.
+  constexpr int kStep = 4 * kTok;
+  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, a.page_size, a.num_pages, seen, end, kStep};
 
   float m[NT], l[NT];
   f32x4 o[NT][VD];
@@ -309,21 +307,17 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
   };
 
   // Two tiles in flight: one being read, one being used.
-  constexpr int kStep = 4 * kTok;
   KvTile<F8, D> b0, b1;
   int32_t t = begin + w * kTok;
-  int64_t next = t < end ? place(t) : -1;
   if (t < end) {
-    load_tile<F8, D>(b0, kbase, vbase, next, lane);
-    next = place(t + kStep);
+    places.start(t + (lane & 31));
+    load_tile<F8, D>(b0, kbase, vbase, places.take(), lane);
     while (true) {
-      if (t + kStep < end) load_tile<F8, D>(b1, kbase, vbase, next, lane);
-      next = place(t + 2 * kStep);
+      if (t + kStep < end) load_tile<F8, D>(b1, kbase, vbase, places.take(), lane);
       compute(b0, t);
       t += kStep;
       if (t >= end) break;
-      if (t + kStep < end) load_tile<F8, D>(b0, kbase, vbase, next, lane);
-      next = place(t + 2 * kStep);
+      if (t + kStep < end) load_tile<F8, D>(b0, kbase, vbase, places.take(), lane);
       compute(b1, t);
       t += kStep;
       if (t >= end) break;

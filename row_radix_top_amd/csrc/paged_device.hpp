@@ -8,6 +8,7 @@
 
 namespace rrt {
 
+using f32x16 = float __attribute__((ext_vector_type(16)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
@@ -20,7 +21,9 @@ using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 // nearest even; from_e4m3: two of the four 8-bit values of a word, exactly;
 // mfma16: D[16][16] += A[16][32] B[32][16], lane l holding A's row l % 16 and
 // B's column l % 16 for the 8 values k = l / 16 * 8 .. + 8, and D's column
-// l % 16 for the rows l / 16 * 4 .. + 4.
+// l % 16 for the rows l / 16 * 4 .. + 4; mfma32: D[32][32] += A[32][16]
+// B[16][32], A's row and B's column l % 32 for k = l / 32 * 8 .. + 8, D's column
+// l % 32 for the rows 8 j + l / 32 * 4 + i as value 4 j + i.
 struct Bf16 {
   using elem = __bf16;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -37,6 +40,11 @@ struct Bf16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
   }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  static constexpr float kLargest = 3.3895313892515355e38f;
 };
 
 struct Fp16 {
@@ -55,6 +63,11 @@ struct Fp16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
   }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+  static constexpr float kLargest = 65504.0f;
 };
 
 // Eight e4m3 values (two words) to eight 16-bit ones (four words).
@@ -68,6 +81,53 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
   const int lo = __shfl((int)(uint32_t)v, lane), hi = __shfl((int)(v >> 32), lane);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
+
+__device__ __forceinline__ int64_t readlane64(int64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Places of a lane's tokens, one a tile, `step` positions of the row apart.
+// A place takes up to two dependent reads (the chosen position, its page);
+// memory reads return in order, so each is issued one tile before it is
+// needed and ahead of that tile's data, and nothing waits for it alone:
+//   start(i); loop { off = take(); ... issue the data loads at off ... }
+// take() returns the place of the next tile (in elements, -1: nothing there)
+// and issues the reads for the two after it.
+template <bool CHOSEN>
+struct Places {
+  const int32_t* table;
+  const int32_t* chosen;
+  int64_t page_stride, token_stride;
+  int32_t page_size, num_pages, seen, end, step;
+  int32_t at;          // row index of the entry in `ahead`
+  int32_t ahead;       // the chosen position there
+  int32_t pos, page;   // the next tile's position (-1: none) and its page
+
+  __device__ __forceinline__ int32_t read(int32_t i) const {
+    if constexpr (CHOSEN) return chosen[i < end ? i : end - 1];
+    return i;
+  }
+  __device__ __forceinline__ void look_up() {
+    pos = at < end && (!CHOSEN || (uint32_t)ahead < (uint32_t)seen) ? ahead : -1;
+    page = table[pos < 0 ? 0u : (uint32_t)pos / (uint32_t)page_size];
+    at += step;
+    ahead = read(at);
+  }
+  __device__ __forceinline__ void start(int32_t i) {
+    at = i;
+    ahead = read(i);
+    look_up();
+  }
+  __device__ __forceinline__ int64_t take() {
+    const int64_t off = pos < 0 || (uint32_t)page >= (uint32_t)num_pages
+                            ? -1
+                            : (int64_t)page * page_stride + (int64_t)((uint32_t)pos % (uint32_t)page_size) * token_stride;
+    look_up();
+    return off;
+  }
+};
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -61,6 +61,10 @@ constexpr int32_t kUnit = 128;
 constexpr int32_t kLeast = 256;
 constexpr int32_t kMostParts = 128;
 constexpr int64_t kPartsPerCu = 4;  // workgroups per CU that a launch is split into
+// The latent kernel's: tiles of 32 or 64 tokens, one workgroup on a CU.
+constexpr int32_t kLatentUnit = 64;
+constexpr int32_t kLatentLeast = 128;
+constexpr int64_t kLatentPartsPerCu = 1;
 
 int check_attention(const paged_attention_args* a, bool latent) {
   REQUIRE(a != nullptr, "null args");
@@ -120,21 +124,32 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   rrt::AttnParams& p = out->p;
   p.a = *a;
   p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
-  p.unit = kUnit;
-  p.least = kLeast;
   const bool chosen = a->chosen != nullptr;
   int64_t units = 0;
-  // Rows of a sequence read its cache together unless each has its own
-  // chosen positions.
-  p.group_rows = chosen ? 1 : a->next_n;
-  const int64_t columns = (int64_t)p.group_rows * (a->num_heads / a->num_kv_heads);
-  const int tiles = columns > 16 ? 2 : 1;
-  p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
-  p.groups = a->num_rows / p.group_rows;
-  units = (int64_t)p.groups * a->num_kv_heads * p.col_tiles;
-  out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, tiles);
+  if (latent) {
+    const int heads = a->num_heads <= 16 ? 16 : a->num_heads <= 32 ? 32 : a->num_heads <= 64 || (a->store == PAGED_E4M3 && a->head_dim == 512) ? 64 : 128;
+    p.unit = kLatentUnit;
+    p.least = kLatentLeast;
+    p.group_rows = 1;
+    p.col_tiles = (int32_t)ceil_div(a->num_heads, heads);
+    p.groups = a->num_rows;
+    units = (int64_t)p.groups * p.col_tiles;
+    out->fn = rrt::latent_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, heads);
+  } else {
+    p.unit = kUnit;
+    p.least = kLeast;
+    // Rows of a sequence read its cache together unless each has its own
+    // chosen positions.
+    p.group_rows = chosen ? 1 : a->next_n;
+    const int64_t columns = (int64_t)p.group_rows * (a->num_heads / a->num_kv_heads);
+    const int tiles = columns > 16 ? 2 : 1;
+    p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
+    p.groups = a->num_rows / p.group_rows;
+    units = (int64_t)p.groups * a->num_kv_heads * p.col_tiles;
+    out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, tiles);
+  }
   const int64_t longest = chosen ? a->num_chosen : rrt::table_tokens(a->table_width, a->page_size);
-  int64_t most = a->max_splits > 0 ? a->max_splits : ceil_div(kPartsPerCu * cus, units);
+  int64_t most = a->max_splits > 0 ? a->max_splits : ceil_div((latent ? kLatentPartsPerCu : kPartsPerCu) * cus, units);
   most = std::max<int64_t>(1, std::min<int64_t>({most, (int64_t)kMostParts, longest / p.least}));
   p.most = (int32_t)most;
   out->grid = units * most;
@@ -162,6 +177,71 @@ int run_attention(const paged_attention_args* a, bool latent, void* workspace, h
   if (plan.p.most == 1) return TOPK_OK;
   return launch(rrt::join_kernel_ptr(a->dtype, a->head_dim), ceil_div((int64_t)a->num_rows * a->num_heads, 4), 256,
                 &plan.p, stream, "join of split rows");
+}
+
+// ---------------------------------------------------------------------------
+// Latent prefill
+// ---------------------------------------------------------------------------
+
+int check_prefill(const latent_prefill_args* a) {
+  REQUIRE(a != nullptr, "null args");
+  if (int rc = check_types(a->dtype, a->store)) return rc;
+  REQUIRE(a->num_tokens >= 0, "num_tokens must be >= 0");
+  REQUIRE(a->num_seqs >= 0, "num_seqs must be >= 0");
+  REQUIRE(a->num_heads >= 1, "num_heads must be >= 1");
+  REQUIRE(a->latent_dim == 256 || a->latent_dim == 512, "latent_dim must be 256 or 512");
+  REQUIRE(a->page_size >= 1, "page_size must be >= 1");
+  REQUIRE(a->table_width >= 1, "table_width must be >= 1");
+  REQUIRE(a->context_tokens >= 0 && a->context_tokens <= rrt::kMostTokens, "context_tokens must be in [0, 2^30]");
+  REQUIRE(std::isfinite(a->softmax_scale), "softmax_scale must be finite");
+  if (a->num_tokens == 0 || a->num_seqs == 0) return TOPK_OK;
+  REQUIRE(a->num_pages >= 1, "num_pages must be >= 1");
+  REQUIRE(a->q != nullptr && a->cache != nullptr && a->w_k != nullptr && a->w_v != nullptr &&
+              a->block_table != nullptr && a->starts != nullptr && a->lengths != nullptr && a->out != nullptr,
+          "null q, cache, w_k, w_v, block_table, starts, lengths or out");
+  const int64_t sz = a->store == PAGED_E4M3 ? 1 : 2;
+  REQUIRE(a->q_row_stride >= 0 && a->q_head_stride >= 0 && a->page_stride >= 0 && a->token_stride >= 0 &&
+              a->table_stride >= 0,
+          "strides must be >= 0");
+  REQUIRE(aligned(a->q, 16) && a->q_row_stride % 8 == 0 && a->q_head_stride % 8 == 0,
+          "q and its strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->cache, 16) && a->page_stride * sz % 16 == 0 && a->token_stride * sz % 16 == 0,
+          "the cache and its strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->w_k, 16) && aligned(a->w_v, 16), "w_k and w_v must be aligned to 16 bytes");
+  REQUIRE(aligned(a->out, 16), "out must be 16-byte aligned");
+  REQUIRE(aligned(a->block_table, 4) && aligned(a->starts, 4) && aligned(a->lengths, 4) && aligned(a->lse, 4) &&
+              aligned(a->scale, 4),
+          "block_table, starts, lengths, lse and scale must be 4-byte aligned");
+  REQUIRE(a->store == PAGED_E4M3 || a->scale == nullptr, "scale belongs to an e4m3 cache");
+  return TOPK_OK;
+}
+
+struct PrefillPlan {
+  rrt::PrefillParams p;
+  size_t rope_at, value_at, valid_at, flag_at, bytes;
+};
+
+int plan_prefill(const latent_prefill_args* a, PrefillPlan* out) {
+  if (int rc = check_prefill(a)) return rc;
+  std::memset(out, 0, sizeof(*out));
+  if (a->num_tokens == 0 || a->num_seqs == 0) return TOPK_OK;
+  rrt::PrefillParams& p = out->p;
+  p.a = *a;
+  p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
+  // Each sequence rounds up to whole tiles.
+  const int64_t capacity = a->context_tokens / rrt::kCtxTile + a->num_seqs;
+  const int64_t row_tiles = a->num_tokens / rrt::prefill_rows() + a->num_seqs;
+  REQUIRE(capacity <= INT32_MAX && row_tiles <= INT32_MAX, "too many tokens and sequences for one launch");
+  p.capacity = (int32_t)capacity;
+  p.row_tiles = (int32_t)row_tiles;
+  const size_t tiles = (size_t)capacity, heads = (size_t)a->num_heads;
+  const size_t tile_bytes = (size_t)rrt::kCtxTile * PAGED_HEAD_DIM * 2;
+  out->rope_at = heads * tiles * tile_bytes;
+  out->value_at = out->rope_at + tiles * rrt::kCtxTile * PAGED_ROPE_DIM * 2;
+  out->valid_at = out->value_at + heads * tiles * tile_bytes;
+  out->flag_at = out->valid_at + tiles * sizeof(uint64_t);
+  out->bytes = out->flag_at + heads * tiles * sizeof(uint32_t);
+  return TOPK_OK;
 }
 
 }  // namespace
@@ -242,6 +322,51 @@ int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t
 
 int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream) {
   return run_attention(args, false, workspace, stream);
+}
+
+int latent_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes) {
+  REQUIRE(bytes != nullptr, "null bytes");
+  AttnPlan plan;
+  if (int rc = plan_attention(args, true, stream, &plan)) return rc;
+  *bytes = plan.bytes;
+  return TOPK_OK;
+}
+
+int latent_attention(const paged_attention_args* args, void* workspace, hipStream_t stream) {
+  return run_attention(args, true, workspace, stream);
+}
+
+int latent_prefill_workspace_size(const latent_prefill_args* args, hipStream_t stream, size_t* bytes) {
+  (void)stream;
+  REQUIRE(bytes != nullptr, "null bytes");
+  PrefillPlan plan;
+  if (int rc = plan_prefill(args, &plan)) return rc;
+  *bytes = plan.bytes;
+  return TOPK_OK;
+}
+
+int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t stream) {
+  PrefillPlan plan;
+  if (int rc = plan_prefill(args, &plan)) return rc;
+  if (plan.bytes == 0) return TOPK_OK;
+  if (workspace == nullptr) {
+    char buf[96];
+    std::snprintf(buf, sizeof(buf), "this launch needs a workspace of %zu bytes", plan.bytes);
+    return set_error(TOPK_EWORKSPACE, buf);
+  }
+  REQUIRE(aligned(workspace, 16), "workspace must be 16-byte aligned");
+  rrt::PrefillParams& p = plan.p;
+  char* ws = static_cast<char*>(workspace);
+  p.keys = ws;
+  p.ropes = ws + plan.rope_at;
+  p.values = ws + plan.value_at;
+  p.valid = reinterpret_cast<uint64_t*>(ws + plan.valid_at);
+  p.flags = reinterpret_cast<uint32_t*>(ws + plan.flag_at);
+  if (int rc = launch(rrt::expand_kernel_ptr(args->dtype, args->store, args->latent_dim),
+                      ceil_div(p.capacity, 2) * args->num_heads, 256, &p, stream, "expansion of latent vectors"))
+    return rc;
+  return launch(rrt::prefill_kernel_ptr(args->dtype), (int64_t)p.row_tiles * args->num_heads, 256, &p, stream,
+                "latent_prefill");
 }
 
 int64_t paged_debug_place(const int32_t* table_row, int32_t page_size, int32_t num_pages, int64_t page_stride,

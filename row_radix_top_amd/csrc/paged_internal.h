@@ -100,10 +100,30 @@ struct AttnParams {
   int32_t col_tiles;   // column tiles of a key-value head
 };
 
+// The expanded form works on tiles of kCtxTile context tokens; a sequence
+// has ceil(length / kCtxTile) of them, after those of the sequences before it.
+constexpr int32_t kCtxTile = 64;
+
+struct PrefillParams {
+  latent_prefill_args a;
+  char* keys;       // [heads][capacity] key tiles, fragment order (128 dims, 16 KB)
+  char* ropes;      // [capacity] rope tiles, fragment order (8 KB)
+  char* values;     // [heads][capacity] value tiles, fragment order (16 KB)
+  uint64_t* valid;  // [capacity]: which of a tile's tokens are in the cache
+  uint32_t* flags;  // [heads][capacity]: 1 where a value is not finite
+  float scale_log2;
+  int32_t capacity;   // tiles of the workspace
+  int32_t row_tiles;  // query tiles of a head that the grid covers
+};
+
 // Kernel lookup: nullptr if there is no such instance.
 const void* layout_kernel_ptr();
 const void* append_kernel_ptr(int dtype, int store, bool wide);
 const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int tiles);
+const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads);
 const void* join_kernel_ptr(int dtype, int head_dim);
+const void* expand_kernel_ptr(int dtype, int store, int latent_dim);
+const void* prefill_kernel_ptr(int dtype);
+int prefill_rows();  // query rows of a workgroup
 
 }  // namespace rrt

@@ -28,7 +28,8 @@ def test_library_exports_every_declared_symbol():
         assert hasattr(binding.load(), n), n
 
 
-@pytest.mark.parametrize("struct,name", [(pa.Part, "paged_part"), (pa.AttentionArgs, "paged_attention_args")])
+@pytest.mark.parametrize("struct,name", [(pa.Part, "paged_part"), (pa.AttentionArgs, "paged_attention_args"),
+                                         (pa.PrefillArgs, "latent_prefill_args")])
 def test_ctypes_mirrors_follow_the_header(struct, name):
     body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", _header()).group(1)
     fields = []
@@ -73,10 +74,10 @@ ATTENTION = [
 
 
 @pytest.mark.parametrize("changes,text", ATTENTION, ids=[str(sorted(c.items())) for c, _ in ATTENTION])
-@pytest.mark.parametrize("latent", [False], ids=["paged"])
+@pytest.mark.parametrize("latent", [False, True], ids=["paged", "latent"])
 def test_attention_refuses(latent, changes, text):
     a = _attention(latent, **changes)
-    fn = pa.load().paged_attention
+    fn = pa.load().latent_attention if latent else pa.load().paged_attention
     assert fn(ctypes.byref(a), None, None) == EINVAL
     assert text in binding.last_error()
 
@@ -90,9 +91,46 @@ def test_paged_attention_refuses(changes, text):
 
 
 def test_no_rows_is_no_work():
-    for fn in (pa.load().paged_attention,):
-        a = _attention(num_rows=0, q=None, k=None, out=None)
+    for fn in (pa.load().paged_attention, pa.load().latent_attention):
+        a = _attention(fn is pa.load().latent_attention, num_rows=0, q=None, k=None, out=None)
         assert fn(ctypes.byref(a), None, None) == 0
+
+
+def _prefill(**changes):
+    a = pa.PrefillArgs()
+    for k, v in dict(q=256, cache=512, w_k=256, w_v=256, block_table=256, starts=256, lengths=256, out=256, lse=256,
+                     q_row_stride=8 * 192, q_head_stride=192, page_stride=16 * 576, token_stride=576, table_stride=4,
+                     context_tokens=100, num_tokens=10, num_seqs=2, num_heads=8, latent_dim=512, page_size=16,
+                     num_pages=4, table_width=4, softmax_scale=0.1, dtype=0, store=0).items():
+        setattr(a, k, changes.pop(k, v))
+    for k, v in changes.items():
+        setattr(a, k, v)
+    return a
+
+
+PREFILL = [
+    (dict(dtype=2), "dtype"), (dict(store=1), "store"), (dict(num_tokens=-1), "num_tokens"),
+    (dict(num_seqs=-1), "num_seqs"), (dict(num_heads=0), "num_heads"), (dict(latent_dim=128), "latent_dim"),
+    (dict(page_size=0), "page_size"), (dict(table_width=0), "table_width"), (dict(context_tokens=-1), "context_tokens"),
+    (dict(softmax_scale=float("nan")), "softmax_scale"), (dict(num_pages=0), "num_pages"), (dict(q=None), "null"),
+    (dict(cache=None), "null"), (dict(w_k=None), "null"), (dict(w_v=None), "null"), (dict(starts=None), "null"),
+    (dict(lengths=None), "null"), (dict(block_table=None), "null"), (dict(out=None), "null"), (dict(q=264), "16 bytes"),
+    (dict(cache=520), "16 bytes"), (dict(w_k=264), "16 bytes"), (dict(token_stride=577), "16 bytes"),
+    (dict(q_head_stride=193), "16 bytes"), (dict(out=264), "16-byte"), (dict(lse=257), "4-byte"),
+    (dict(scale=256), "e4m3"), (dict(page_stride=-16), "strides"),
+]
+
+
+@pytest.mark.parametrize("changes,text", PREFILL, ids=[str(sorted(c.items())) for c, _ in PREFILL])
+def test_prefill_refuses(changes, text):
+    assert pa.load().latent_prefill(ctypes.byref(_prefill(**changes)), None, None) == EINVAL
+    assert text in binding.last_error()
+
+
+def test_prefill_needs_its_workspace():
+    assert pa.load().latent_prefill(ctypes.byref(_prefill()), None, None) == -3
+    assert "workspace" in binding.last_error()
+    assert pa.load().latent_prefill(ctypes.byref(_prefill(num_tokens=0, q=None)), None, None) == 0
 
 
 def _layout(**changes):
