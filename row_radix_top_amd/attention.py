@@ -66,26 +66,27 @@ class Layout(NamedTuple):
 
 
 _lib = None
+torch = None  # imported with the library, on the first call
 
 
 def load() -> ctypes.CDLL:
     """The built library with these entry points' signatures set."""
-    global _lib
+    global _lib, torch, _CODES
     if _lib is None:
+        import torch as _torch
+        torch = _torch
+        _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: _E4M3}
         lib = binding.load()
         lib.paged_layout.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                      _vp]
         lib.paged_append.argtypes = [_vp, _i32, ctypes.POINTER(Part), _i32, _i32, _i32, _i32, _i32, _vp]
         for name, args in (("paged_attention", AttentionArgs), ("latent_attention", AttentionArgs),
                            ("latent_prefill", PrefillArgs)):
-            if not hasattr(lib, name):
-                continue
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp, _vp]
             getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args), _vp,
                                                                ctypes.POINTER(ctypes.c_size_t)]
         for name in EXPORTED:
-            if hasattr(lib, name):
-                getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).restype = ctypes.c_int
         lib.paged_debug_place.argtypes = [_vp, _i32, _i32, _i64, _i64, _i32]
         lib.paged_debug_place.restype = _i64
         lib.paged_debug_split.argtypes = [_i32, _i32, _i32, _i32, _vp]
@@ -95,101 +96,102 @@ def load() -> ctypes.CDLL:
 
 
 # ---------------------------------------------------------------------------
-# Argument checks
+# Argument checks.  A decode step makes these calls once a layer, so what a
+# call costs on the host counts: devices are compared by index, no context is
+# entered for the usual call, and outputs that the call itself allocates are
+# not checked.
 # ---------------------------------------------------------------------------
-
-def _dtypes():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_E4M3 = 2
+_CODES: dict = {}
 
 
-_codes = None
+def _elsewhere(x, stream) -> bool:
+    """Whether the call has to enter another device or stream first."""
+    return stream is not None or x.get_device() != torch._C._cuda_getDevice()
+
+
+def _on(stream, x):
+    """The call's stream made current (and its device), so that what torch
+    allocates for the call belongs to it."""
+    device = x.device
+    if device.type != "cuda":
+        raise TypeError("tensors must be on a GPU")
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream and tensors must be on the same device")
+    return torch.cuda.stream(stream)
 
 
 def _code(x, name: str, cache: bool = False) -> int:
-    global _codes
-    if _codes is None:
-        _codes = _dtypes()
-    code = _codes.get(x.dtype)
-    if code is None or (code == 2 and not cache):
+    code = _CODES.get(x.dtype)
+    if code is None or (code == _E4M3 and not cache):
         raise TypeError(f"{name} must be bfloat16 or float16" + (" or float8_e4m3fn" if cache else ""))
     return code
 
 
-def _ints(x, name: str, device, shape=None):
-    import torch
-    if x.dtype != torch.int32 or x.device != device:
-        raise TypeError(f"{name} must be an int32 tensor on {device}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(x.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}")
+def _ints(x, name: str, dev: int, n: int) -> int:
+    """Pointer of a contiguous int32 tensor of n entries."""
+    if x.dtype is not torch.int32 or x.get_device() != dev:
+        raise TypeError(f"{name} must be an int32 tensor on cuda:{dev}")
+    if x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} entries")
     return x.data_ptr()
 
 
-def _matrix(x, name: str, device, rows: int):
-    """An int32 [rows, n >= 1] tensor whose rows may be strided."""
-    import torch
-    if x.dtype != torch.int32 or x.device != device or x.dim() != 2:
-        raise TypeError(f"{name} must be a 2-D int32 tensor on {device}")
+def _matrix(x, name: str, dev: int, rows: int) -> int:
+    """Pointer of an int32 [rows, n >= 1] tensor whose rows may be strided."""
+    if x.dtype is not torch.int32 or x.get_device() != dev or x.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D int32 tensor on cuda:{dev}")
     if x.shape[0] != rows or x.shape[1] < 1 or (x.stride(1) != 1 and x.shape[1] > 1):
         raise ValueError(f"{name} must be [{rows}, n] with n >= 1 and unit column stride")
     return x.data_ptr()
 
 
-def _scales(x, name: str, device, n: int, code: int):
-    import torch
+def _scales(x, name: str, dev: int, n: int, code: int):
     if x is None:
         return None
-    if code != 2:
+    if code != _E4M3:
         raise ValueError(f"{name} belongs to a float8_e4m3fn cache")
-    if x.dtype != torch.float32 or x.device != device or x.numel() != n or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} on {device}")
+    if x.dtype is not torch.float32 or x.get_device() != dev or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} on cuda:{dev}")
     return x.data_ptr()
 
 
-def _like(x, name: str, device, dtype, shape):
-    if x.dtype != dtype or x.device != device or tuple(x.shape) != shape or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _output(x, name: str, dtype, shape, like):
+    """x if it is given (and fits), else a new tensor."""
+    if x is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if x.dtype is not dtype or x.get_device() != like.get_device() or tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {like.device}")
     return x
 
 
-_null = contextlib.nullcontext()
+def _launch(name: str, args, workspace, key, like) -> None:
+    """Calls entry point `name` with a workspace large enough: `workspace`, or
+    a new one.  key: what its size depends on."""
+    dev = like.get_device()
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    need = _sizes.get((name, dev, key))
+    if need is None:
+        size = ctypes.c_size_t(0)
+        _check(getattr(_lib, name + "_workspace_size")(args, stream, size), name)
+        need = size.value
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        _sizes[name, dev, key] = need
+    ptr = None
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        elif (workspace.get_device() != dev or not workspace.is_contiguous()
+              or workspace.numel() * workspace.element_size() < need):
+            raise ValueError(f"workspace must be a contiguous tensor of {need} bytes or more on {like.device}")
+        ptr = workspace.data_ptr()
+    _check(getattr(_lib, name)(args, ptr, stream), name)
 
 
-def _on(stream, device):
-    """The call's stream made current (and its device), so that what torch
-    allocates for the call belongs to it."""
-    import torch
-    if device.type != "cuda":
-        raise TypeError("tensors must be on a GPU")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream and tensors must be on the same device")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return _null
-
-
-def _stream(device) -> int:
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _workspace(fn, args, workspace, device, name: str, sp: int):
-    """Pointer of a workspace large enough (and the tensor, to keep it)."""
-    import torch
-    need = ctypes.c_size_t(0)
-    _check(fn(ctypes.byref(args), sp, ctypes.byref(need)), name)
-    if need.value == 0:
-        return None, None
-    if workspace is None:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-    elif (workspace.device != device or not workspace.is_contiguous()
-          or workspace.numel() * workspace.element_size() < need.value):
-        raise ValueError(f"workspace must be a contiguous tensor of {need.value} bytes or more on {device}")
-    return workspace.data_ptr(), workspace
+_sizes: dict = {}  # workspace bytes by shape: a pure function of it
 
 
 # ---------------------------------------------------------------------------
@@ -206,45 +208,50 @@ def paged_layout(lengths, new_tokens, free_pages, block_table, *, page_size: int
     free_pages (int32) in order.  Returns a Layout of `capacity` rows; tokens
     past it are not written.  See paged_layout in paged_attention.h.
     """
-    import torch
-    device = lengths.device
-    with _on(stream, device):
-        n = lengths.numel()
-        args = (_ints(lengths, "lengths", device), _ints(new_tokens, "new_tokens", device, (n,)), n,
-                _ints(free_pages, "free_pages", device), free_pages.numel(),
-                _matrix(block_table, "block_table", device, n), block_table.stride(0) if n > 1 else block_table.shape[1],
-                block_table.shape[1], page_size, capacity)
-        if capacity < 0:
-            raise ValueError("capacity must be >= 0")
-        if out is None:
-            rows = torch.empty((3, capacity), dtype=torch.int32, device=device)
-            ends = torch.empty(n + 2, dtype=torch.int32, device=device)
-            out = Layout(rows[0], rows[1], rows[2], ends[:n + 1], ends[n + 1:])
-        ptrs = [_ints(x, f"out.{name}", device, (size,)) for x, name, size in
-                ((out.starts, "starts", n + 1), (out.slots, "slots", capacity),
-                 (out.row_lengths, "row_lengths", capacity), (out.row_seqs, "row_seqs", capacity),
-                 (out.pages, "pages", 1))]
-        _check(load().paged_layout(*args, *ptrs, _stream(device)), "paged_layout")
+    lib = load()
+    if _elsewhere(lengths, stream):
+        with _on(stream, lengths):
+            return paged_layout(lengths, new_tokens, free_pages, block_table, page_size=page_size, capacity=capacity,
+                                out=out)
+    if capacity < 0:
+        raise ValueError("capacity must be >= 0")
+    dev, n = lengths.get_device(), lengths.numel()
+    width = block_table.shape[-1]
+    if out is None:
+        whole = torch.empty(3 * capacity + n + 2, dtype=torch.int32, device=lengths.device)
+        out = Layout(*whole.split_with_sizes([capacity, capacity, capacity, n + 1, 1]))
+        at = whole.data_ptr()
+        slots, rows, seqs, starts = at, at + 4 * capacity, at + 8 * capacity, at + 12 * capacity
+        pages = starts + 4 * (n + 1)
+    else:
+        slots, rows, seqs = (_ints(x, name, dev, capacity) for x, name in
+                             ((out.slots, "out.slots"), (out.row_lengths, "out.row_lengths"),
+                              (out.row_seqs, "out.row_seqs")))
+        starts, pages = _ints(out.starts, "out.starts", dev, n + 1), _ints(out.pages, "out.pages", dev, 1)
+    _check(lib.paged_layout(_ints(lengths, "lengths", dev, n), _ints(new_tokens, "new_tokens", dev, n), n,
+                            _ints(free_pages, "free_pages", dev, free_pages.numel()), free_pages.numel(),
+                            _matrix(block_table, "block_table", dev, n), block_table.stride(0) if n > 1 else width,
+                            width, page_size, capacity, starts, slots, rows, seqs, pages,
+                            torch._C._cuda_getCurrentRawStream(dev)), "paged_layout")
     return out
 
 
-def _part(x, name: str, cache, cache_name: str, column: int, heads: int, dim: int, tokens: int, scales) -> Part:
+def _part(x, name: str, cache, column: int, heads: int, dim: int, scales) -> Part:
     """x [tokens, heads, dim] (inner dims contiguous) into columns of cache
     [pages, page_size, heads, dim] or [pages, page_size, width]."""
-    if x.device != cache.device:
-        raise ValueError(f"{name} and {cache_name} must be on the same device")
-    if x.shape[0] != tokens or (x.numel() > 0 and not x[0].is_contiguous()):
-        raise ValueError(f"{name} must have one contiguous row for each slot")
-    if cache.stride(-1) != 1:
-        raise ValueError(f"{cache_name} must have unit stride in its last dimension")
-    return Part(x.data_ptr(), cache.data_ptr() + column * cache.element_size(), scales, x.stride(0), cache.stride(0),
-                cache.stride(1), cache.stride(2) if cache.dim() == 4 else 0, heads * dim, dim)
+    stride = x.stride()
+    if stride[-1] != 1 or (len(stride) == 3 and stride[1] != dim and heads > 1):
+        raise ValueError(f"{name}'s rows must be contiguous")
+    to = cache.stride()
+    return Part(x.data_ptr(), cache.data_ptr() + column * cache.element_size(), scales, stride[0], to[0], to[1],
+                to[2] if len(to) == 4 else 0, heads * dim, dim)
 
 
-def _append(slots, parts, cache, code: int, store: int, stream) -> None:
-    array = (Part * len(parts))(*parts)
-    _check(load().paged_append(_ints(slots, "slots", cache.device), slots.numel(), array, len(parts), cache.shape[1],
-                               cache.shape[0], code, store, stream), "paged_append")
+def _append(slots, one: Part, two: Part, cache, tokens: int, code: int, store: int) -> None:
+    dev = cache.get_device()
+    shape = cache.shape
+    _check(_lib.paged_append(_ints(slots, "slots", dev, tokens), tokens, (Part * 2)(one, two), 2, shape[1], shape[0],
+                             code, store, torch._C._cuda_getCurrentRawStream(dev)), "paged_append")
 
 
 def paged_append(slots, k, v, k_cache, v_cache, *, k_scale=None, v_scale=None, stream=None) -> None:
@@ -253,94 +260,94 @@ def paged_append(slots, k, v, k_cache, v_cache, *, k_scale=None, v_scale=None, s
     drop a token) of the caches [num_pages, page_size, num_kv_heads, head_dim]
     of the same type or float8_e4m3fn, then as x / scale with float32
     [num_kv_heads] scales (None: 1).  No slot may occur twice."""
-    device = k_cache.device
-    with _on(stream, device):
-        code, store = _code(k, "k"), _code(k_cache, "k_cache", True)
-        if v.dtype != k.dtype or v_cache.dtype != k_cache.dtype:
-            raise TypeError("k and v, and k_cache and v_cache, must have the same type")
-        if k.dim() != 3 or k_cache.dim() != 4 or k.shape != v.shape or k_cache.shape != v_cache.shape:
-            raise ValueError("k and v must be [num_tokens, heads, dim], the caches [num_pages, page_size, heads, dim]")
-        tokens, heads, dim = k.shape
-        if tuple(k_cache.shape[2:]) != (heads, dim) or v_cache.device != device:
-            raise ValueError("the caches must have k's heads and dim and be on one device")
-        if slots.numel() != tokens:
-            raise ValueError("slots must hold one entry for each token")
-        _append(slots, [_part(k, "k", k_cache, "k_cache", 0, heads, dim, tokens,
-                              _scales(k_scale, "k_scale", device, heads, store)),
-                        _part(v, "v", v_cache, "v_cache", 0, heads, dim, tokens,
-                              _scales(v_scale, "v_scale", device, heads, store))],
-                k_cache, code, store, _stream(device))
+    load()
+    if _elsewhere(k_cache, stream):
+        with _on(stream, k_cache):
+            return paged_append(slots, k, v, k_cache, v_cache, k_scale=k_scale, v_scale=v_scale)
+    dev = k_cache.get_device()
+    code, store = _code(k, "k"), _code(k_cache, "k_cache", True)
+    if v.dtype is not k.dtype or v_cache.dtype is not k_cache.dtype:
+        raise TypeError("k and v, and k_cache and v_cache, must have the same type")
+    if k.get_device() != dev or v.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("k, v and the caches must be on one device")
+    shape = k_cache.shape
+    if k.dim() != 3 or len(shape) != 4 or k.shape != v.shape or shape != v_cache.shape:
+        raise ValueError("k and v must be [num_tokens, heads, dim], the caches [num_pages, page_size, heads, dim]")
+    tokens, heads, dim = k.shape
+    if shape[2] != heads or shape[3] != dim or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise ValueError("the caches must have k's heads and dim and unit stride in their last dimension")
+    _append(slots, _part(k, "k", k_cache, 0, heads, dim, _scales(k_scale, "k_scale", dev, heads, store)),
+            _part(v, "v", v_cache, 0, heads, dim, _scales(v_scale, "v_scale", dev, heads, store)), k_cache, tokens,
+            code, store)
 
 
 def latent_append(slots, latent, rope, cache, *, scale=None, stream=None) -> None:
     """Writes latent vectors [num_tokens, latent_dim] and their rope parts
     [num_tokens, 64] to their slots of cache [num_pages, page_size, latent_dim
     + 64], as paged_append does; scale: float32 [1]."""
-    device = cache.device
-    with _on(stream, device):
-        code, store = _code(latent, "latent"), _code(cache, "cache", True)
-        if rope.dtype != latent.dtype:
-            raise TypeError("latent and rope must have the same type")
-        if latent.dim() != 2 or rope.dim() != 2 or cache.dim() != 3:
-            raise ValueError("latent and rope must be 2-D and cache 3-D")
-        tokens, dim = latent.shape
-        if rope.shape[1] != ROPE_DIM or cache.shape[2] != dim + ROPE_DIM:
-            raise ValueError(f"rope must have {ROPE_DIM} columns and cache latent's and rope's together")
-        if slots.numel() != tokens:
-            raise ValueError("slots must hold one entry for each token")
-        by = _scales(scale, "scale", device, 1, store)
-        _append(slots, [_part(latent, "latent", cache, "cache", 0, 1, dim, tokens, by),
-                        _part(rope, "rope", cache, "cache", dim, 1, ROPE_DIM, tokens, by)],
-                cache, code, store, _stream(device))
+    load()
+    if _elsewhere(cache, stream):
+        with _on(stream, cache):
+            return latent_append(slots, latent, rope, cache, scale=scale)
+    dev = cache.get_device()
+    code, store = _code(latent, "latent"), _code(cache, "cache", True)
+    if rope.dtype is not latent.dtype:
+        raise TypeError("latent and rope must have the same type")
+    if latent.get_device() != dev or rope.get_device() != dev:
+        raise ValueError("latent, rope and cache must be on one device")
+    if latent.dim() != 2 or rope.dim() != 2 or cache.dim() != 3 or cache.stride(2) != 1:
+        raise ValueError("latent and rope must be 2-D and cache 3-D with unit stride in its last dimension")
+    tokens, dim = latent.shape
+    if rope.shape[0] != tokens or rope.shape[1] != ROPE_DIM or cache.shape[2] != dim + ROPE_DIM:
+        raise ValueError(f"rope must have {ROPE_DIM} columns and cache latent's and rope's together")
+    by = _scales(scale, "scale", dev, 1, store)
+    _append(slots, _part(latent, "latent", cache, 0, 1, dim, by), _part(rope, "rope", cache, dim, 1, ROPE_DIM, by),
+            cache, tokens, code, store)
 
 
 # ---------------------------------------------------------------------------
 # Attention
 # ---------------------------------------------------------------------------
 
-def _attention_args(q, k, lengths, block_table, chosen, next_n, softmax_scale, dim: int, value_dim: int, out, lse,
-                    max_splits: int):
-    import torch
-    device = q.device
+def _attend(entry: str, q, k, v, scales, lengths, block_table, chosen, next_n, softmax_scale, kv: int, value_dim: int,
+            out, lse, workspace, max_splits: int):
+    """paged_attention and latent_attention after what differs between them:
+    k (and v) a cache [num_pages, page_size, ..., dim], scales (name, tensor,
+    size) of each."""
+    dev = q.get_device()
     code, store = _code(q, "q"), _code(k, "the cache", True)
-    if store != 2 and k.dtype != q.dtype:
+    if store != _E4M3 and store != code:
         raise TypeError("the cache must have q's type or float8_e4m3fn")
-    if k.device != device:
+    if k.get_device() != dev:
         raise ValueError("q and the cache must be on the same device")
-    if q.dim() != 3 or q.shape[2] != dim or q.stride(2) != 1:
+    kshape, kstride, qstride = k.shape, k.stride(), q.stride()
+    dim = kshape[-1]
+    if q.dim() != 3 or q.shape[2] != dim or qstride[2] != 1:
         raise ValueError(f"q must be [num_rows, num_heads, {dim}] with unit stride in its last dimension")
-    if k.stride(-1) != 1:
+    if kstride[-1] != 1:
         raise ValueError("the cache must have unit stride in its last dimension")
-    rows, heads = q.shape[0], q.shape[1]
+    rows, heads, _ = q.shape
     if next_n is None:
         next_n = int(lengths.shape[1]) if lengths.dim() == 2 else 1
-    if lengths.numel() != rows:
-        raise ValueError("lengths must hold one entry for each row of q")
     if next_n < 1 or rows % next_n != 0:
         raise ValueError("next_n must be >= 1 and divide the rows")
-    a = AttentionArgs()
-    a.q, a.k = q.data_ptr(), k.data_ptr()
-    a.lengths = _ints(lengths, "lengths", device)
-    a.block_table = _matrix(block_table, "block_table", device, rows // next_n)
-    a.table_stride, a.table_width = block_table.stride(0), block_table.shape[1]
+    lengths_at = _ints(lengths, "lengths", dev, rows)
+    table_at = _matrix(block_table, "block_table", dev, rows // next_n)
+    width = block_table.shape[1]
+    chosen_at, chosen_stride, num_chosen = None, 0, 0
     if chosen is not None:
-        a.chosen = _matrix(chosen, "chosen", device, rows)
-        a.chosen_stride, a.num_chosen = chosen.stride(0), chosen.shape[1]
-    if out is None:
-        out = torch.empty((rows, heads, value_dim), dtype=q.dtype, device=device)
-    else:
-        _like(out, "out", device, q.dtype, (rows, heads, value_dim))
-    if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
-    else:
-        _like(lse, "lse", device, torch.float32, (rows, heads))
-    a.out, a.lse = out.data_ptr(), lse.data_ptr()
-    a.q_row_stride, a.q_head_stride = q.stride(0), q.stride(1)
-    a.page_stride, a.token_stride = k.stride(0), k.stride(1)
-    a.num_rows, a.next_n, a.num_heads, a.num_kv_heads, a.head_dim = rows, next_n, heads, 1, value_dim
-    a.num_pages, a.page_size = k.shape[0], k.shape[1]
-    a.softmax_scale, a.dtype, a.store, a.max_splits = softmax_scale, code, store, max_splits
-    return a, out, lse
+        chosen_at = _matrix(chosen, "chosen", dev, rows)
+        chosen_stride, num_chosen = chosen.stride(0), chosen.shape[1]
+    by = [_scales(x, name, dev, n, store) for name, x, n in scales]
+    out = _output(out, "out", q.dtype, (rows, heads, value_dim), q)
+    lse = _output(lse, "lse", torch.float32, (rows, heads), q)
+    args = AttentionArgs(q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), by[0],
+                         by[1] if len(by) > 1 else None, table_at, lengths_at, chosen_at, out.data_ptr(),
+                         lse.data_ptr(), qstride[0], qstride[1], kstride[0], kstride[1],
+                         kstride[2] if v is not None else 0, block_table.stride(0), chosen_stride, rows, next_n, heads,
+                         kv, value_dim, kshape[1], kshape[0], width, num_chosen, softmax_scale, code, store, max_splits)
+    _launch(entry, args, workspace, (rows, next_n, heads, kv, value_dim, kshape[1], width, num_chosen, max_splits), q)
+    return out, lse
 
 
 def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, softmax_scale: float | None = None,
@@ -357,25 +364,22 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, s
     next_n].  softmax_scale: head_dim ** -0.5 if None.  Rows that see nothing
     get zeros and -inf.
     """
-    device = q.device
-    with _on(stream, device):
-        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-            raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
-        if v_cache.dtype != k_cache.dtype or v_cache.device != device:
-            raise TypeError("k_cache and v_cache must have the same type and device")
-        kv, dim = k_cache.shape[2], k_cache.shape[3]
-        if kv < 1 or q.dim() != 3 or q.shape[1] % kv != 0:
-            raise ValueError("q's heads must be a multiple of the cache's")
-        a, out, lse = _attention_args(q, k_cache, lengths, block_table, chosen, next_n,
-                                      dim ** -0.5 if softmax_scale is None else softmax_scale, dim, dim, out, lse,
-                                      max_splits)
-        a.v, a.num_kv_heads, a.head_stride = v_cache.data_ptr(), kv, k_cache.stride(2)
-        a.k_scales = _scales(k_scale, "k_scale", device, kv, a.store)
-        a.v_scales = _scales(v_scale, "v_scale", device, kv, a.store)
-        lib, sp = load(), _stream(device)
-        ws, _keep = _workspace(lib.paged_attention_workspace_size, a, workspace, device, "paged_attention", sp)
-        _check(lib.paged_attention(ctypes.byref(a), ws, sp), "paged_attention")
-    return out, lse
+    load()
+    if _elsewhere(q, stream):
+        with _on(stream, q):
+            return paged_attention(q, k_cache, v_cache, block_table, lengths, chosen=chosen,
+                                   softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale, next_n=next_n,
+                                   out=out, lse=lse, workspace=workspace, max_splits=max_splits)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
+    if v_cache.dtype is not k_cache.dtype or v_cache.get_device() != q.get_device():
+        raise TypeError("k_cache and v_cache must have the same type and device")
+    kv, dim = k_cache.shape[2], k_cache.shape[3]
+    if kv < 1 or q.dim() != 3 or q.shape[1] % kv != 0:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    return _attend("paged_attention", q, k_cache, v_cache, (("k_scale", k_scale, kv), ("v_scale", v_scale, kv)),
+                   lengths, block_table, chosen, next_n, dim ** -0.5 if softmax_scale is None else softmax_scale, kv,
+                   dim, out, lse, workspace, max_splits)
 
 
 def latent_attention(q, cache, block_table, lengths, *, softmax_scale: float, chosen=None, scale=None,
@@ -386,18 +390,16 @@ def latent_attention(q, cache, block_table, lengths, *, softmax_scale: float, ch
     values; latent_dim 256 or 512.  Returns (out [num_rows, num_heads,
     latent_dim], lse).  Other arguments as for paged_attention; scale:
     float32 [1] of a float8_e4m3fn cache."""
-    device = q.device
-    with _on(stream, device):
-        if cache.dim() != 3:
-            raise ValueError("cache must be [num_pages, page_size, latent_dim + 64]")
-        dim = cache.shape[2]
-        a, out, lse = _attention_args(q, cache, lengths, block_table, chosen, next_n, softmax_scale, dim,
-                                      dim - ROPE_DIM, out, lse, max_splits)
-        a.k_scales = _scales(scale, "scale", device, 1, a.store)
-        lib, sp = load(), _stream(device)
-        ws, _keep = _workspace(lib.latent_attention_workspace_size, a, workspace, device, "latent_attention", sp)
-        _check(lib.latent_attention(ctypes.byref(a), ws, sp), "latent_attention")
-    return out, lse
+    load()
+    if _elsewhere(q, stream):
+        with _on(stream, q):
+            return latent_attention(q, cache, block_table, lengths, softmax_scale=softmax_scale, chosen=chosen,
+                                    scale=scale, next_n=next_n, out=out, lse=lse, workspace=workspace,
+                                    max_splits=max_splits)
+    if cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, page_size, latent_dim + 64]")
+    return _attend("latent_attention", q, cache, None, (("scale", scale, 1),), lengths, block_table, chosen, next_n,
+                   softmax_scale, 1, cache.shape[2] - ROPE_DIM, out, lse, workspace, max_splits)
 
 
 def latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, *, context_tokens: int, softmax_scale: float,
@@ -409,40 +411,31 @@ def latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, *, context_
     both as paged_layout gives and takes them; w_k, w_v: [num_heads, 128,
     latent_dim]; context_tokens: at least the sum of the lengths.  Returns
     (out [num_tokens, num_heads, 128], lse).  See paged_attention.h."""
-    import torch
-    device = q.device
-    with _on(stream, device):
-        code, store = _code(q, "q"), _code(cache, "cache", True)
-        if store != 2 and cache.dtype != q.dtype:
-            raise TypeError("cache must have q's type or float8_e4m3fn")
-        if q.dim() != 3 or q.shape[2] != HEAD_DIM + ROPE_DIM or q.stride(2) != 1:
-            raise ValueError(f"q must be [num_tokens, num_heads, {HEAD_DIM + ROPE_DIM}], its last stride 1")
-        if cache.dim() != 3 or cache.stride(2) != 1 or cache.device != device:
-            raise ValueError("cache must be [num_pages, page_size, latent_dim + 64] on q's device, its last stride 1")
-        tokens, heads, dim = q.shape[0], q.shape[1], cache.shape[2] - ROPE_DIM
-        for w, name in ((w_k, "w_k"), (w_v, "w_v")):
-            _like(w, name, device, q.dtype, (heads, HEAD_DIM, dim))
-        n = lengths.numel()
-        a = PrefillArgs()
-        a.q, a.cache, a.w_k, a.w_v = q.data_ptr(), cache.data_ptr(), w_k.data_ptr(), w_v.data_ptr()
-        a.lengths, a.starts = _ints(lengths, "lengths", device), _ints(starts, "starts", device, (n + 1,))
-        a.block_table = _matrix(block_table, "block_table", device, n)
-        a.scale = _scales(scale, "scale", device, 1, store)
-        if out is None:
-            out = torch.empty((tokens, heads, HEAD_DIM), dtype=q.dtype, device=device)
-        else:
-            _like(out, "out", device, q.dtype, (tokens, heads, HEAD_DIM))
-        if lse is None:
-            lse = torch.empty((tokens, heads), dtype=torch.float32, device=device)
-        else:
-            _like(lse, "lse", device, torch.float32, (tokens, heads))
-        a.out, a.lse = out.data_ptr(), lse.data_ptr()
-        a.q_row_stride, a.q_head_stride = q.stride(0), q.stride(1)
-        a.page_stride, a.token_stride, a.table_stride = cache.stride(0), cache.stride(1), block_table.stride(0)
-        a.context_tokens, a.num_tokens, a.num_seqs, a.num_heads, a.latent_dim = context_tokens, tokens, n, heads, dim
-        a.num_pages, a.page_size, a.table_width = cache.shape[0], cache.shape[1], block_table.shape[1]
-        a.softmax_scale, a.dtype, a.store = softmax_scale, code, store
-        lib, sp = load(), _stream(device)
-        ws, _keep = _workspace(lib.latent_prefill_workspace_size, a, workspace, device, "latent_prefill", sp)
-        _check(lib.latent_prefill(ctypes.byref(a), ws, sp), "latent_prefill")
+    load()
+    if _elsewhere(q, stream):
+        with _on(stream, q):
+            return latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, context_tokens=context_tokens,
+                                  softmax_scale=softmax_scale, scale=scale, out=out, lse=lse, workspace=workspace)
+    dev = q.get_device()
+    code, store = _code(q, "q"), _code(cache, "cache", True)
+    if store != _E4M3 and store != code:
+        raise TypeError("cache must have q's type or float8_e4m3fn")
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM + ROPE_DIM or q.stride(2) != 1:
+        raise ValueError(f"q must be [num_tokens, num_heads, {HEAD_DIM + ROPE_DIM}], its last stride 1")
+    if cache.dim() != 3 or cache.stride(2) != 1 or cache.get_device() != dev:
+        raise ValueError("cache must be [num_pages, page_size, latent_dim + 64] on q's device, its last stride 1")
+    tokens, heads, dim = q.shape[0], q.shape[1], cache.shape[2] - ROPE_DIM
+    for w, name in ((w_k, "w_k"), (w_v, "w_v")):
+        _output(w, name, q.dtype, (heads, HEAD_DIM, dim), q)
+    n = lengths.numel()
+    table_at = _matrix(block_table, "block_table", dev, n)
+    by = _scales(scale, "scale", dev, 1, store)
+    starts_at, lengths_at = _ints(starts, "starts", dev, n + 1), _ints(lengths, "lengths", dev, n)
+    out = _output(out, "out", q.dtype, (tokens, heads, HEAD_DIM), q)
+    lse = _output(lse, "lse", torch.float32, (tokens, heads), q)
+    args = PrefillArgs(q.data_ptr(), cache.data_ptr(), by, w_k.data_ptr(), w_v.data_ptr(), table_at, starts_at,
+                       lengths_at, out.data_ptr(), lse.data_ptr(), q.stride(0), q.stride(1), cache.stride(0),
+                       cache.stride(1), block_table.stride(0), context_tokens, tokens, n, heads, dim, cache.shape[1],
+                       cache.shape[0], block_table.shape[1], softmax_scale, code, store)
+    _launch("latent_prefill", args, workspace, (context_tokens, tokens, n, heads, dim), q)
     return out, lse

@@ -32,7 +32,6 @@ namespace rrt {
 // is kept at c ^ swizzle(t), which spreads both the 16 tokens of a key operand
 // and the 4 tokens x 2 chunks of a transposed read over the banks.
 // ---------------------------------------------------------------------------
-constexpr int kLatentBlock = 256;
 constexpr int kRope = PAGED_ROPE_DIM;
 constexpr float kLazy = 8.0f;
 constexpr int kAhead = 4;  // operands in flight from LDS
@@ -58,20 +57,32 @@ __device__ __forceinline__ uint32_t fresh(uint32_t x) {
   return x;
 }
 
+constexpr int latent_waves(int heads) { return heads == 32 ? 8 : 4; }
+
 template <int DC, int HT>
 struct LatentShape {
-  static constexpr int TT = HT == 128 ? 32 : 64;            // tokens of a tile
-  static constexpr int WH = HT == 128 ? 4 : HT == 64 ? 2 : 1;  // wavefronts along the heads
-  static constexpr int WT = 4 / WH;                         // and along the tokens
-  static constexpr int NH = HT / 16 / WH;                   // 16-head columns of a wavefront's scores
-  static constexpr int NU = TT / 16 / WT;                   // 16-token rows of a wavefront's scores
-  static constexpr int KS = (DC + kRope) / 32;              // matrix steps over the key dims
-  static constexpr int ND = DC / 64;                        // 16-dim rows of a wavefront's output
-  static constexpr int NC = HT / 16;                        // 16-head columns of the output
-  static constexpr int PT = TT + 8;                         // pitch of the weights
+  static constexpr int NW = latent_waves(HT);        // wavefronts
+  static constexpr int TT = 64;                     // tokens of a tile
+  static constexpr int WT = HT == 64 ? 2 : 4;                   // wavefronts along the tokens of the scores
+  static constexpr int WH = NW / WT;                // and along the heads
+  static constexpr int NH = HT / 16 / WH;           // 16-head columns of a wavefront's scores
+  static constexpr int NU = TT / 16 / WT;           // 16-token rows of a wavefront's scores
+  static constexpr int KS = (DC + kRope) / 32;      // matrix steps over the key dims
+  static constexpr int ND = DC / 16 / NW;           // 16-dim rows of a wavefront's output
+  static constexpr int NC = HT / 16;                // 16-head columns of the output
+  static constexpr int PT = TT + 16;                // pitch of the weights (rows 40 banks apart)
 };
 
-__device__ __forceinline__ int swz(int t) { return ((t << 1) | ((t >> 3) & 1)) & 15; }
+// Sixteen-byte reads are served in groups of lanes {0-3, 12-15, 20-27} and so
+// on: tokens 0-3 and 12-15 of one lane group with 4-11 of the next, whose
+// chunk is the neighbour.  swz is a permutation of 0..15 that maps {4..11} to
+// whole pairs (2i, 2i+1), so such a group meets every bank once; and its upper
+// three bits differ over tokens {0-3, 8-11} and over {4-7, 12-15}, which are
+// the rows that a transposed read touches together.  (A rotation of t, without
+// the second lane group in mind, spent 42% of the LDS cycles in conflicts.)
+__device__ __forceinline__ int swz(int t) {
+  return ((t & 3) << 1) | ((t >> 2) & 1) | ((((t >> 2) ^ (t >> 3)) & 1) << 3);
+}
 __device__ __forceinline__ int swz_rope(int t) { return (t >> 1) & 7; }
 
 // 64 lanes x 16 bytes from the lanes' addresses to 1 KB of LDS at `to` (wave
@@ -83,16 +94,16 @@ __device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <typename T, bool F8, int DC, bool CHOSEN, int HT>
-__global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
+__global__ void __launch_bounds__(latent_waves(HT) * 64, latent_waves(HT) / 4) latent_kernel(AttnParams p) {
   using S = LatentShape<DC, HT>;
-  constexpr int TT = S::TT, NH = S::NH, NU = S::NU, KS = S::KS, ND = S::ND, NC = S::NC, PT = S::PT, WT = S::WT;
-  constexpr int TW = TT / 4;  // tokens that a wavefront loads
+  constexpr int TT = S::TT, NH = S::NH, NU = S::NU, KS = S::KS, ND = S::ND, NC = S::NC, PT = S::PT, WT = S::WT, NW = S::NW;
+  constexpr int TW = TT / NW;  // tokens that a wavefront loads
   constexpr int SZ = F8 ? 1 : 2;
   __shared__ __align__(1024) uint16_t sc[2][TT * DC];
   __shared__ __align__(1024) uint16_t sr[2][TT * kRope];
   __shared__ __align__(16) uint16_t sp_[HT * PT];
   __shared__ float smax[WT][HT], ssum[WT][HT], salpha[HT];
-  __shared__ uint32_t svalid[2][4];
+  __shared__ uint32_t svalid[2][NW];
   __shared__ uint32_t sflag[2];
   const paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
@@ -118,7 +129,7 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
   const char* cache = (const char*)a.k;
 
   // Places of the wavefront's token `lane % TW` of each tile.
-  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, a.page_size, a.num_pages, seen, end, TT};
+  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, p.page, a.num_pages, seen, end, TT};
 
   // --- loads of a tile -----------------------------------------------------
   constexpr int LT = F8 ? DC / 16 : DC / 8;      // lanes (16 bytes each) of a token's latent part
@@ -148,7 +159,7 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
         stage[i] = *(const u32x4*)(from + c * 16);
       } else {
         const int tt = w * TW + t;
-        load_to_lds(from + ((c ^ swz(tt)) * 16), lds_at(&sc[b][(w * TW + i * PER) * DC]));
+        load_to_lds(from + (uint32_t)((c ^ swz(tt)) * 16), lds_at(&sc[b][(w * TW + i * PER) * DC]));
       }
     }
 #pragma unroll
@@ -160,7 +171,7 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
         stage_r[i] = *(const u32x4*)(from + c * 16);
       } else {
         const int tt = w * TW + t;
-        load_to_lds(from + ((c ^ swz_rope(tt)) * 16), lds_at(&sr[b][(w * TW + i * 8) * kRope]));
+        load_to_lds(from + ((c ^ swz_rope(tt)) * 16), lds_at(&sr[b][(w * TW + i * (64 / RT)) * kRope]));
       }
     }
   };
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
     float top[NH];
     uint64_t valid = 0;
 #pragma unroll
-    for (int k = 3; k >= 0; --k) valid = (valid << TW) | __builtin_amdgcn_readfirstlane(svalid[b][k]);
+    for (int k = NW - 1; k >= 0; --k) valid = (valid << TW) | __builtin_amdgcn_readfirstlane(svalid[b][k]);
     constexpr uint64_t every = TT == 64 ? ~0ull : (1ull << (TT & 63)) - 1ull;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const uint32_t tt = k * 32 + lg * 8 + half * 4 + (lcol >> 2);
-        const uint32_t chunk = (uint32_t)w * (DC / 32) + ((lcol & 3) >> 1);
+        const uint32_t chunk = (uint32_t)w * (DC / 8 / NW) + ((lcol & 3) >> 1);
         vrow[half] = buf + tt * (DC * 2) + ((chunk ^ (uint32_t)swz((int)tt)) << 4) + (lcol & 1) * 8;
       }
       auto value = [&](int d) {
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
       };
       u32x4 v[kAhead];
 #pragma unroll
-      for (int d = 0; d < kAhead - 1; ++d) v[d] = value(d);
+      for (int d = 0; d < kAhead - 1 && d < ND; ++d) v[d] = value(d);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
@@ -411,14 +422,14 @@ __global__ void __launch_bounds__(kLatentBlock, 1) latent_kernel(AttnParams p) {
       const float by = total == 0.0f ? 0.0f : by_cache / total;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        *(u32x2*)((uint16_t*)a.out + at * DC + w * (DC / 4) + d * 16 + g * 4) =
+        *(u32x2*)((uint16_t*)a.out + at * DC + w * (DC / NW) + d * 16 + g * 4) =
             u32x2{T::pack(o[c][d][0] * by, o[c][d][1] * by), T::pack(o[c][d][2] * by, o[c][d][3] * by)};
       if (w == 0 && lane < 16 && a.lse != nullptr) a.lse[at] = total == 0.0f ? -INFINITY : (m + __log2f(total)) * kLn2;
     } else {
       const int64_t pi = at * p.most + part;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        *(f32x4*)(p.part_out + pi * DC + w * (DC / 4) + d * 16 + g * 4) = o[c][d] * by_cache;
+        *(f32x4*)(p.part_out + pi * DC + w * (DC / NW) + d * 16 + g * 4) = o[c][d] * by_cache;
       if (w == 0 && lane < 16) p.part_stat[pi] = float2{m, total};
     }
   }
@@ -432,9 +443,6 @@ const void* latent_heads(int heads) {
     case 16: return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 16>;
     case 32: return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 32>;
     case 64: return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 64>;
-    case 128:
-      if constexpr (F8 && DC == 512) return nullptr;
-      else return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 128>;
     default: return nullptr;
   }
 }
@@ -448,6 +456,8 @@ const void* latent_dims(int head_dim, bool chosen, int heads) {
 }
 
 }  // namespace
+
+int latent_threads(int heads) { return latent_waves(heads) * 64; }
 
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads) {
   if (dtype == PAGED_BF16)

@@ -75,17 +75,23 @@ __device__ __forceinline__ int32_t sequence_of_tile(const PrefillParams& p, int3
 
 // ---------------------------------------------------------------------------
 // Expansion: one head's 128 keys and 128 values for two context tiles a
-// workgroup.  Wavefronts 0 and 1 form the keys of a tile each, 2 and 3 the
-// values.  Latent vectors and weights pass through LDS in slices of 64 of the
-// summed dims, two slices deep, 16-byte chunks at c ^ (row / 2 % 8).
+// workgroup, a product of [128 tokens x DC] and [DC x 256].  Each wavefront
+// forms 64 x 128 of it: 0 and 1 half of the key dims for all tokens, 2 and 3
+// all value dims for a tile, so that keys come out with consecutive dims in a
+// lane and values with consecutive tokens, as their fragments want them.
+// Latent vectors and weights pass through LDS in slices of 32 of the summed
+// dims, two slices deep (48 KB: two workgroups a CU hide each other's waits),
+// 16-byte chunks at c ^ (row / 4 % 4): a read's 16 rows then meet every bank
+// once.
 // ---------------------------------------------------------------------------
 template <typename T, bool F8, int DC>
-__global__ void __launch_bounds__(kExpandBlock, 1) expand_kernel(PrefillParams p) {
-  constexpr int SL = 64;             // dims of a slice
+__global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p) {
+  constexpr int SL = 32;             // dims of a slice
   constexpr int NS = DC / SL;
   constexpr int TOK = 2 * kCtxTile;  // tokens of a workgroup
-  __shared__ __align__(1024) uint16_t sx[2][TOK * SL];
-  __shared__ __align__(1024) uint16_t sw[2][2 * kHead * SL];
+  constexpr int ROWS = TOK + 2 * kHead;
+  constexpr int PITCH = SL * 2;      // bytes of a slice's row
+  __shared__ __align__(1024) char sm[2][ROWS * PITCH];  // tokens, key weights, value weights
   __shared__ int64_t splace[TOK];
   const latent_prefill_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -113,119 +119,119 @@ __global__ void __launch_bounds__(kExpandBlock, 1) expand_kernel(PrefillParams p
   const bool real[2] = {splace[0] != -2, splace[64] != -2};
   if (!real[0] && !real[1]) return;
 
-  // Slice k of the weights (256 rows) and of the latent vectors (128 rows).
+  // A wavefront loads 64 rows of weights and 32 of tokens of each slice, 16
+  // rows (of four lanes) at a time.
   constexpr int SZ = F8 ? 1 : 2;
+  const int r16 = lane >> 2, c4 = lane & 3;
+  const int swap = c4 ^ ((r16 >> 2) & 3);  // the chunk that lands at the lane's place
   const char* cache = (const char*)a.cache;
-  const char* wk = (const char*)a.w_k + (int64_t)head * kHead * DC * 2;
-  const char* wv = (const char*)a.w_v + (int64_t)head * kHead * DC * 2;
-  u32x2 stage[4];
+  const char* wrow = (w < 2 ? (const char*)a.w_k : (const char*)a.w_v) +
+                     ((int64_t)head * kHead + (w & 1) * 64 + r16) * (DC * 2) + swap * 16;
+  const char* xrow[2];
+  bool gone[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t off = splace[w * 32 + i * 16 + r16];
+    gone[i] = off < 0;
+    xrow[i] = cache + (off < 0 ? 0 : off) * SZ + (F8 ? c4 * 8 : swap * 16);
+  }
+  const bool any_gone = __builtin_amdgcn_ballot_w64(gone[0] || gone[1]) != 0;
+  u32x2 stage[2];
   auto issue = [&](int k, int b) {
-    const int r8 = lane >> 3, c = lane & 7;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // 32 blocks of 8 weight rows
-      const int row = (w * 8 + i) * 8 + r8;
-      const char* from = (row < kHead ? wk + row * (DC * 2) : wv + (row - kHead) * (DC * 2)) + k * (SL * 2);
-      load_to_lds(from + ((c ^ ((row >> 1) & 7)) * 16), lds_at(&sw[b][(w * 8 + i) * 8 * SL]));
-    }
+    for (int i = 0; i < 4; ++i)
+      load_to_lds(wrow + i * (16 * DC * 2) + k * PITCH, lds_at(&sm[b][(TOK + w * 64 + i * 16) * PITCH]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // 16 blocks of 8 tokens
-      const int row = (w * 4 + i) * 8 + r8;
-      const int64_t off = splace[row];
-      const char* from = cache + (off < 0 ? 0 : off) * SZ + k * (SL * SZ);
-      if constexpr (F8) {
-        stage[i] = *(const u32x2*)(from + c * 8);
-      } else {
-        load_to_lds(from + ((c ^ ((row >> 1) & 7)) * 16), lds_at(&sx[b][(w * 4 + i) * 8 * SL]));
-      }
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (F8)
+        stage[i] = *(const u32x2*)(xrow[i] + k * SL);
+      else
+        load_to_lds(xrow[i] + k * PITCH, lds_at(&sm[b][(w * 32 + i * 16) * PITCH]));
     }
   };
+  auto mine = [&](int b, int i) { return (u32x4*)&sm[b][(w * 32 + i * 16 + r16) * PITCH]; };
   auto store = [&](int b) {
     if constexpr (F8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = (w * 4 + i) * 8 + (lane >> 3), c = lane & 7;
-        ((u32x4*)&sx[b][row * SL])[c ^ ((row >> 1) & 7)] = widen<T>(stage[i]);
-      }
-    }
-  };
-  // Tokens that are not there count as zeros.
-  auto clear = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (w * 4 + i) * 8 + (lane >> 3);
-      if (splace[row] < 0) ((u32x4*)&sx[b][row * SL])[lane & 7] = u32x4{0, 0, 0, 0};
+      for (int i = 0; i < 2; ++i) mine(b, i)[swap] = widen<T>(stage[i]);
     }
   };
 
-  f32x16 acc[2][4];  // [block of 32 tokens][block of 32 dims]
+  f32x16 acc[2][4];  // [block of 32 rows][block of 32 columns]
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int d = 0; d < 4; ++d) acc[t][d] = f32x16{};
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+  // Keys: rows are dims, columns tokens.  Values: rows are tokens, columns dims.
   const bool keys = w < 2;
-  const int tile_in = w & 1;
+  const int arow = keys ? TOK + w * 64 : (w & 1) * 64, brow = keys ? 0 : TOK + kHead;
+  const uint32_t lrow = (uint32_t)(lane & 31) * PITCH, lswap = (uint32_t)(lane >> 2) & 3;
   issue(0, 0);
   store(0);
   for (int k = 0; k < NS; ++k) {
     const int b = k & 1;
     wait_loads();
-    clear(b);
+    if (any_gone) {  // tokens that are not there count as zeros
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (gone[i]) mine(b, i)[c4] = u32x4{0, 0, 0, 0};
+    }
     __syncthreads();
     if (k + 1 < NS) issue(k + 1, b ^ 1);
-    const uint32_t xrow = lds_at(&sx[b][0]) + (uint32_t)(tile_in * 64 + (lane & 31)) * (SL * 2);
-    const uint32_t wrow = lds_at(&sw[b][0]) + (uint32_t)((keys ? 0 : kHead) + (lane & 31)) * (SL * 2);
+    const uint32_t abase = lds_at(&sm[b][0]) + (uint32_t)arow * PITCH + lrow;
+    const uint32_t bbase = lds_at(&sm[b][0]) + (uint32_t)brow * PITCH + lrow;
 #pragma unroll
     for (int s = 0; s < SL / 16; ++s) {
-      const uint32_t c = (uint32_t)((s * 2 + half) ^ ((lane >> 1) & 7)) * 16;
+      const uint32_t c = (((uint32_t)(s * 2 + half)) ^ lswap) * 16;
       u32x4 x[2], y[4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) x[t] = lds_read16(xrow + t * (32 * SL * 2) + c);
+      for (int i = 0; i < 2; ++i) x[i] = lds_read16(abase + i * (32 * PITCH) + c);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) y[d] = lds_read16(wrow + d * (32 * SL * 2) + c);
+      for (int j = 0; j < 4; ++j) y[j] = lds_read16(bbase + j * (32 * PITCH) + c);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) acc[t][d] = keys ? T::mfma32(y[d], x[t], acc[t][d]) : T::mfma32(x[t], y[d], acc[t][d]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma32(x[i], y[j], acc[i][j]);
     }
     if (k + 1 < NS) store(b ^ 1);
   }
 
   const float by = F8 && a.scale != nullptr ? a.scale[0] : 1.0f;
-  const int32_t tile = tile0 + tile_in;
-  if (real[tile_in]) {
-    if (keys) {
-      char* to = p.keys + ((int64_t)head * p.capacity + tile) * kKeyTile + (lane & 31) * 16 + half * 8;
+  if (keys) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int j = 0; j < 4; ++j) {  // 32 tokens
+      if (!real[j >> 1]) continue;
+      char* to = p.keys + ((int64_t)head * p.capacity + tile0 + (j >> 1)) * kKeyTile + (lane & 31) * 16 + half * 8;
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // dims d*32 + j*8 + half*4 .. +4 of the lane's token
-            const f32x16& x = acc[t][d];
-            *(u32x2*)(to + (t * 8 + d * 2 + (j >> 1)) * kBlock16 + (j & 1) * 512) =
-                u32x2{T::pack(x[j * 4] * by, x[j * 4 + 1] * by), T::pack(x[j * 4 + 2] * by, x[j * 4 + 3] * by)};
-          }
-    } else {
-      char* to = p.values + ((int64_t)head * p.capacity + tile) * kValueTile + lane * 16;
-      bool bad = false;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] = acc[t][d][ks * 8 + e] * by;
-              bad = bad || !(fabsf(x[e]) <= T::kLargest);
-            }
-            *(u32x4*)(to + ((t * 2 + ks) * 4 + d) * kBlock16) =
-                u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
-          }
-      const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
-      if (lane == 0) p.flags[(int64_t)head * p.capacity + tile] = any != 0 ? 1u : 0u;
+        for (int e = 0; e < 4; ++e) {  // dims w*64 + i*32 + e*8 + half*4 .. +4 of the lane's token
+          const f32x16& x = acc[i][j];
+          *(u32x2*)(to + ((j & 1) * 8 + w * 4 + i * 2 + (e >> 1)) * kBlock16 + (e & 1) * 512) =
+              u32x2{T::pack(x[e * 4] * by, x[e * 4 + 1] * by), T::pack(x[e * 4 + 2] * by, x[e * 4 + 3] * by)};
+        }
     }
+  } else if (real[w & 1]) {
+    const int32_t tile = tile0 + (w & 1);
+    char* to = p.values + ((int64_t)head * p.capacity + tile) * kValueTile + lane * 16;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = acc[i][j][ks * 8 + e] * by;
+            bad = bad || !(fabsf(x[e]) <= T::kLargest);
+          }
+          *(u32x4*)(to + ((i * 2 + ks) * 4 + j) * kBlock16) =
+              u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
+        }
+    const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
+    if (lane == 0) p.flags[(int64_t)head * p.capacity + tile] = any != 0 ? 1u : 0u;
   }
   // Rope parts, copied once for all heads: wavefront w takes 32 tokens.
   if (head == 0) {

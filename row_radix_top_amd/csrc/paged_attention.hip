@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
   // Places of the lane's tokens (both halves of the wavefront hold the same
   // 32); a part is never empty unless its row is.
   constexpr int kStep = 4 * kTok;
-  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, a.page_size, a.num_pages, seen, end, kStep};
+  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, p.page, a.num_pages, seen, end, kStep};
 
   float m[NT], l[NT];
   f32x4 o[NT][VD];
@@ -368,16 +368,26 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
 
 // ---------------------------------------------------------------------------
 // Join: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over a row's
-// parts, M the largest m_i.  One wavefront for each (row, head), D / 64 dims a
-// lane; rows of one part were finished by the attention kernel.  Reads the
-// parts once, from L2: a few microseconds at most, mostly the launch.
+// parts, M the largest m_i; rows of one part were finished by the attention
+// kernel.
+//
+// Many parts (MANY): a workgroup for each (row, head); D / 4 threads cover the
+// dims, the groups of threads beside each other take every G-th part and meet
+// in LDS, so a row of many parts is not a chain of as many reads (20 heads of
+// 512 dims in 64 parts: 5.8 us, 13.7 us with one wavefront each).  Up to four
+// parts: one wavefront for each (row, head) and no LDS (8192 of them, two
+// parts: 9.1 us, 13.7 us with a workgroup each).
 // ---------------------------------------------------------------------------
-template <typename T, int D>
+template <typename T, int D, bool MANY>
 __global__ void __launch_bounds__(kAttnBlock) join_kernel(AttnParams p) {
-  constexpr int E = D / 64;
+  constexpr int TD = MANY ? D / 4 : 64;     // threads of a (row, head) along the dims
+  constexpr int E = D / TD;                 // dims of a thread
+  constexpr int G = MANY ? kAttnBlock / TD : 1;
+  __shared__ float acc[MANY ? G : 1][MANY ? D : 1];
+  __shared__ float weight[MANY ? 128 : 1];
   const paged_attention_args& a = p.a;
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * (kAttnBlock / 64) + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t at = MANY ? blockIdx.x : (int64_t)blockIdx.x * (kAttnBlock / 64) + w;
   if (at >= (int64_t)a.num_rows * a.num_heads) return;
   const int32_t row = (int32_t)(at / a.num_heads);
   const int32_t n = a.chosen != nullptr
@@ -385,32 +395,54 @@ __global__ void __launch_bounds__(kAttnBlock) join_kernel(AttnParams p) {
                         : group_length(p, row / p.group_rows * p.group_rows, table_tokens(a.table_width, a.page_size), lane);
   const Split sp = split_of(n, p.most, p.least, p.unit);
   if (sp.parts == 1) return;
+  // Every wavefront forms the weights: at most 128, two a lane.
   const float2* stat = p.part_stat + at * p.most;
-  float m0 = -INFINITY, l0 = 0.0f, m1 = -INFINITY, l1 = 0.0f;  // at most 128 parts
-  if (lane < sp.parts) m0 = stat[lane].x, l0 = stat[lane].y;
-  if (lane + 64 < sp.parts) m1 = stat[lane + 64].x, l1 = stat[lane + 64].y;
-  const float top = wave_max(fmaxf(m0, m1));
-  const float w0 = m0 == top ? 1.0f : exp2_fast(m0 - top), w1 = m1 == top ? 1.0f : exp2_fast(m1 - top);
-  float sum = l0 * w0 + l1 * w1;
+  const float2 s0 = lane < sp.parts ? stat[lane] : float2{-INFINITY, 0.0f};
+  const float2 s1 = MANY && lane + 64 < sp.parts ? stat[lane + 64] : float2{-INFINITY, 0.0f};
+  const float top = wave_max(fmaxf(s0.x, s1.x));
+  const float w0 = s0.x == top ? 1.0f : exp2_fast(s0.x - top), w1 = s1.x == top ? 1.0f : exp2_fast(s1.x - top);
+  float sum = s0.y * w0 + s1.y * w1;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  const float* po = p.part_out + at * p.most * D + lane * E;
+  const int g = MANY ? (int)threadIdx.x / TD : 0, d = MANY ? (int)threadIdx.x % TD : lane;
+  const float* po = p.part_out + at * p.most * D + d * E;
   float o[E] = {};
-#pragma unroll 4
-  for (int32_t i = 0; i < sp.parts; ++i) {
-    const float by = __shfl(i < 64 ? w0 : w1, i & 63);
+  if constexpr (MANY) {
+    if (w == 0) weight[lane] = w0, weight[lane + 64] = w1;
+    __syncthreads();
+#pragma unroll 8
+    for (int32_t i = g; i < sp.parts; i += G) {
+      const f32x4 x = *(const f32x4*)(po + (int64_t)i * D);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += by * po[(int64_t)i * D + e];
+      for (int e = 0; e < E; ++e) o[e] += weight[i] * x[e];
+    }
+  } else {
+#pragma unroll 4
+    for (int32_t i = 0; i < sp.parts; ++i) {
+      const float by = __shfl(w0, i);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += by * po[(int64_t)i * D + e];
+    }
+  }
+  if constexpr (MANY) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[g][d * E + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x >= TD) return;
+#pragma unroll
+    for (int k = 1; k < G; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += acc[k][d * E + e];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* out = (uint16_t*)a.out + at * D + lane * E;
+  uint16_t* out = (uint16_t*)a.out + at * D + d * E;
   if constexpr (E == 1) {
     *out = (uint16_t)T::pack(o[0] * inv, 0.0f);
   } else {
 #pragma unroll
     for (int e = 0; e < E; e += 2) *(uint32_t*)(out + e) = T::pack(o[e] * inv, o[e + 1] * inv);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+  if (d == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 namespace {
@@ -426,12 +458,12 @@ const void* attn_dims(int head_dim, bool chosen, int tiles) {
   return nullptr;
 }
 template <typename T>
-const void* join_dims(int head_dim) {
+const void* join_dims(int head_dim, bool many) {
   switch (head_dim) {
-    case 64: return (const void*)&join_kernel<T, 64>;
-    case 128: return (const void*)&join_kernel<T, 128>;
-    case 256: return (const void*)&join_kernel<T, 256>;
-    case 512: return (const void*)&join_kernel<T, 512>;
+    case 64: return many ? (const void*)&join_kernel<T, 64, true> : (const void*)&join_kernel<T, 64, false>;
+    case 128: return many ? (const void*)&join_kernel<T, 128, true> : (const void*)&join_kernel<T, 128, false>;
+    case 256: return many ? (const void*)&join_kernel<T, 256, true> : (const void*)&join_kernel<T, 256, false>;
+    case 512: return many ? (const void*)&join_kernel<T, 512, true> : (const void*)&join_kernel<T, 512, false>;
     default: return nullptr;
   }
 }
@@ -446,8 +478,8 @@ const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int
                              : attn_dims<Fp16, false>(head_dim, chosen, tiles);
 }
 
-const void* join_kernel_ptr(int dtype, int head_dim) {
-  return dtype == PAGED_BF16 ? join_dims<Bf16>(head_dim) : join_dims<Fp16>(head_dim);
+const void* join_kernel_ptr(int dtype, int head_dim, bool many) {
+  return dtype == PAGED_BF16 ? join_dims<Bf16>(head_dim, many) : join_dims<Fp16>(head_dim, many);
 }
 
 }  // namespace rrt

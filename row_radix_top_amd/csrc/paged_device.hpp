@@ -100,18 +100,22 @@ struct Places {
   const int32_t* table;
   const int32_t* chosen;
   int64_t page_stride, token_stride;
-  int32_t page_size, num_pages, seen, end, step;
+  Divisor by;          // page size
+  int32_t num_pages, seen, end, step;
   int32_t at;          // row index of the entry in `ahead`
   int32_t ahead;       // the chosen position there
-  int32_t pos, page;   // the next tile's position (-1: none) and its page
+  int32_t page;        // the next tile's page
+  uint32_t in;         // and the offset inside it, all ones where there is no position
 
   __device__ __forceinline__ int32_t read(int32_t i) const {
     if constexpr (CHOSEN) return chosen[i < end ? i : end - 1];
     return i;
   }
   __device__ __forceinline__ void look_up() {
-    pos = at < end && (!CHOSEN || (uint32_t)ahead < (uint32_t)seen) ? ahead : -1;
-    page = table[pos < 0 ? 0u : (uint32_t)pos / (uint32_t)page_size];
+    const bool ok = at < end && (!CHOSEN || (uint32_t)ahead < (uint32_t)seen);
+    const uint32_t pos = ok ? (uint32_t)ahead : 0u, j = divide(pos, by);
+    in = ok ? pos - j * by.by : ~0u;
+    page = table[j];
     at += step;
     ahead = read(at);
   }
@@ -121,9 +125,9 @@ struct Places {
     look_up();
   }
   __device__ __forceinline__ int64_t take() {
-    const int64_t off = pos < 0 || (uint32_t)page >= (uint32_t)num_pages
+    const int64_t off = in == ~0u || (uint32_t)page >= (uint32_t)num_pages
                             ? -1
-                            : (int64_t)page * page_stride + (int64_t)((uint32_t)pos % (uint32_t)page_size) * token_stride;
+                            : (int64_t)page * page_stride + (int64_t)in * token_stride;
     look_up();
     return off;
   }

@@ -99,7 +99,7 @@ int check_attention(const paged_attention_args* a, bool latent) {
   REQUIRE(aligned(a->k, 16) && (latent || aligned(a->v, 16)) && a->page_stride * sz % 16 == 0 &&
               a->token_stride * sz % 16 == 0 && (latent || a->head_stride * sz % 16 == 0),
           "the cache and its strides must be multiples of 16 bytes");
-  REQUIRE(aligned(a->out, 4), "out must be 4-byte aligned");
+  REQUIRE(aligned(a->out, 16), "out must be 16-byte aligned");
   REQUIRE(aligned(a->block_table, 4) && aligned(a->lengths, 4) && aligned(a->chosen, 4) && aligned(a->lse, 4) &&
               aligned(a->k_scales, 4) && aligned(a->v_scales, 4),
           "block_table, lengths, chosen, lse and scales must be 4-byte aligned");
@@ -110,6 +110,7 @@ int check_attention(const paged_attention_args* a, bool latent) {
 
 struct AttnPlan {
   rrt::AttnParams p;
+  int threads;
   const void* fn;
   int64_t grid;
   size_t bytes;
@@ -124,10 +125,12 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   rrt::AttnParams& p = out->p;
   p.a = *a;
   p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
+  p.page = rrt::divisor_of(a->page_size);
   const bool chosen = a->chosen != nullptr;
   int64_t units = 0;
   if (latent) {
-    const int heads = a->num_heads <= 16 ? 16 : a->num_heads <= 32 ? 32 : a->num_heads <= 64 || (a->store == PAGED_E4M3 && a->head_dim == 512) ? 64 : 128;
+    const int heads = a->num_heads <= 16 ? 16 : a->num_heads <= 32 ? 32 : 64;
+    out->threads = rrt::latent_threads(heads);
     p.unit = kLatentUnit;
     p.least = kLatentLeast;
     p.group_rows = 1;
@@ -138,6 +141,7 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   } else {
     p.unit = kUnit;
     p.least = kLeast;
+    out->threads = 256;
     // Rows of a sequence read its cache together unless each has its own
     // chosen positions.
     p.group_rows = chosen ? 1 : a->next_n;
@@ -173,10 +177,12 @@ int run_attention(const paged_attention_args* a, bool latent, void* workspace, h
         reinterpret_cast<float2*>(plan.p.part_out + (int64_t)a->num_rows * a->num_heads * plan.p.most * a->head_dim);
   }
   const char* name = latent ? "latent_attention" : "paged_attention";
-  if (int rc = launch(plan.fn, plan.grid, 256, &plan.p, stream, name)) return rc;
+  if (int rc = launch(plan.fn, plan.grid, plan.threads, &plan.p, stream, name)) return rc;
   if (plan.p.most == 1) return TOPK_OK;
-  return launch(rrt::join_kernel_ptr(a->dtype, a->head_dim), ceil_div((int64_t)a->num_rows * a->num_heads, 4), 256,
-                &plan.p, stream, "join of split rows");
+  const bool many = plan.p.most > 4;
+  const int64_t outputs = (int64_t)a->num_rows * a->num_heads;
+  return launch(rrt::join_kernel_ptr(a->dtype, a->head_dim, many), many ? outputs : ceil_div(outputs, 4), 256, &plan.p,
+                stream, "join of split rows");
 }
 
 // ---------------------------------------------------------------------------

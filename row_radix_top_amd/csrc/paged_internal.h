@@ -35,6 +35,19 @@ RRT_HD int64_t table_tokens(int32_t width, int32_t page_size) {
   return n > kMostTokens ? kMostTokens : n;
 }
 
+// x / d for 0 <= x < 2^31 by one multiplication: with s = ceil(log2 d) and
+// m = ceil(2^(31 + s) / d) < 2^32, x m / 2^(31 + s) exceeds x / d by less than
+// x / 2^(31 + s) < 1 / d, so its floor is the quotient's.
+struct Divisor {
+  uint32_t mul, shift, by;
+};
+inline Divisor divisor_of(int32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < (uint64_t)d) ++s;
+  return {(uint32_t)(((1ull << (31 + s)) + (uint64_t)d - 1) / (uint64_t)d), s, (uint32_t)d};
+}
+RRT_HD uint32_t divide(uint32_t x, const Divisor& d) { return (uint32_t)(((uint64_t)x * d.mul) >> 31 >> d.shift); }
+
 // Place of position pos in the pool, in elements, or -1 where the table holds
 // no page of it.  The caller keeps 0 <= pos < table_width * page_size.
 RRT_HD int64_t locate(const int32_t* table_row, int32_t page_size, int32_t num_pages, int64_t page_stride,
@@ -98,6 +111,7 @@ struct AttnParams {
   int32_t groups;      // units of work along the rows: sequences, or rows
   int32_t group_rows;  // rows of a group: next_n, or 1
   int32_t col_tiles;   // column tiles of a key-value head
+  Divisor page;        // by page_size
 };
 
 // The expanded form works on tiles of kCtxTile context tokens; a sequence
@@ -121,8 +135,9 @@ const void* layout_kernel_ptr();
 const void* append_kernel_ptr(int dtype, int store, bool wide);
 const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int tiles);
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads);
-const void* join_kernel_ptr(int dtype, int head_dim);
+const void* join_kernel_ptr(int dtype, int head_dim, bool many);
 const void* expand_kernel_ptr(int dtype, int store, int latent_dim);
+int latent_threads(int heads);  // of a workgroup
 const void* prefill_kernel_ptr(int dtype);
 int prefill_rows();  // query rows of a workgroup
 

@@ -67,7 +67,7 @@ ATTENTION = [
     (dict(num_pages=0), "num_pages"), (dict(q=None), "null"), (dict(k=None), "null"), (dict(lengths=None), "null"),
     (dict(block_table=None), "null"), (dict(out=None), "null"), (dict(q=264), "16 bytes"),
     (dict(q_row_stride=1028), "16 bytes"), (dict(k=520), "16 bytes"), (dict(token_stride=129), "16 bytes"),
-    (dict(page_stride=-128), "strides"), (dict(out=258), "4-byte"), (dict(lse=257), "4-byte"),
+    (dict(page_stride=-128), "strides"), (dict(out=264), "16-byte"), (dict(lse=257), "4-byte"),
     (dict(k_scales=256), "e4m3"), (dict(num_rows=1 << 30, num_heads=8), "2^31"),
     (dict(store=2, token_stride=136), "16 bytes"),
 ]
