@@ -110,11 +110,9 @@ __global__ void __launch_bounds__(latent_waves(HT) * 64, latent_waves(HT) / 4) l
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wh = w % S::WH, wt = w / S::WH;
 
-  const uint32_t units = (uint32_t)(p.groups * p.col_tiles);
-  const int32_t part = (int32_t)(blockIdx.x / units);
-  const uint32_t unit = blockIdx.x - (uint32_t)part * units;
-  const int32_t row = (int32_t)(unit / (uint32_t)p.col_tiles);
-  const int32_t head0 = (int32_t)(unit - (uint32_t)row * (uint32_t)p.col_tiles) * HT;
+  Work work;
+  if (!work_of(blockIdx.x, (uint32_t)p.col_tiles, (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
+  const int32_t part = work.part, row = work.group, head0 = work.unit * HT;
   const int64_t most = table_tokens(a.table_width, a.page_size);
   const int32_t seen = clamp_to(a.lengths[row], most);
   const int32_t n = CHOSEN ? a.num_chosen : seen;

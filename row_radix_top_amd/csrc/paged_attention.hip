@@ -58,25 +58,29 @@ struct KvTile {
   static constexpr int VW = F8 ? D / 64 : D / 32;                // words of a lane's value dims
   u32x4 k[2][KL];
   uint32_t v[8][VW];
-  uint32_t valid;  // bit i: token i of the tile is in the cache and inside the part
 };
 
+// off: place of the tile's token `lane % 32`, in elements (-1: none; the load
+// then takes the pool's first token, and the tile's mask leaves it out).
 template <bool F8, int D>
-__device__ __forceinline__ void load_tile(KvTile<F8, D>& b, const char* k, const char* v, int64_t off, int lane) {
-  using Tile = KvTile<F8, D>;
+__device__ __forceinline__ void load_keys(KvTile<F8, D>& b, const char* k, int64_t off, int lane) {
   constexpr int SZ = F8 ? 1 : 2;
-  const int row = lane & 15, g = lane >> 4;
-  b.valid = (uint32_t)__builtin_amdgcn_ballot_w64(off >= 0);
   const int64_t at = off < 0 ? 0 : off * SZ;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const char* kp = k + shfl64(at, u * 16 + row) + g * 16;
+    const char* kp = k + shfl64(at, u * 16 + (lane & 15)) + (lane >> 4) * 16;
 #pragma unroll
-    for (int i = 0; i < Tile::KL; ++i) b.k[u][i] = *(const u32x4*)(kp + i * 64);
+    for (int i = 0; i < KvTile<F8, D>::KL; ++i) b.k[u][i] = *(const u32x4*)(kp + i * 64);
   }
+}
+template <bool F8, int D>
+__device__ __forceinline__ void load_values(KvTile<F8, D>& b, const char* v, int64_t off, int lane) {
+  using Tile = KvTile<F8, D>;
+  constexpr int SZ = F8 ? 1 : 2;
+  const int64_t at = off < 0 ? 0 : off * SZ;
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    const char* vp = v + shfl64(at, (t >> 2) * 16 + g * 4 + (t & 3)) + row * (Tile::VW * 4);
+    const char* vp = v + shfl64(at, (t >> 2) * 16 + (lane >> 4) * 4 + (t & 3)) + (lane & 15) * (Tile::VW * 4);
     if constexpr (Tile::VW == 4) {
       const u32x4 x = *(const u32x4*)vp;
 #pragma unroll
@@ -90,8 +94,14 @@ __device__ __forceinline__ void load_tile(KvTile<F8, D>& b, const char* k, const
   }
 }
 
-template <typename T, bool F8, int D, bool CHOSEN, int NT>
-__global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnParams p) {
+// What a row reads: all its positions (kOne: a sequence has one row; kRows:
+// several, which share the reads but may end at different places), or chosen
+// ones.
+enum { kOne, kRows, kChosen };
+
+template <typename T, bool F8, int D, int MODE, int NT>
+__global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) attn_kernel(AttnParams p) {
+  constexpr bool CHOSEN = MODE == kChosen;
   constexpr int KS = D / 32;  // matrix steps over the key dims
   constexpr int VD = D / 16;  // value dims of a lane
   constexpr int SZ = F8 ? 1 : 2;
@@ -102,12 +112,10 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
   const int lane = threadIdx.x & 63, col16 = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 
-  const int32_t units = p.groups * a.num_kv_heads * p.col_tiles;
-  const int32_t part = (int32_t)(blockIdx.x / (uint32_t)units);
-  int32_t unit = (int32_t)(blockIdx.x - (uint32_t)part * (uint32_t)units);
-  const int32_t kvh = unit % a.num_kv_heads;
-  unit /= a.num_kv_heads;
-  const int32_t tile = unit % p.col_tiles, group = unit / p.col_tiles;
+  Work work;
+  if (!work_of(blockIdx.x, (uint32_t)(a.num_kv_heads * p.col_tiles), (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
+  const int32_t part = work.part, group = work.group;
+  const int32_t kvh = work.unit % a.num_kv_heads, tile = work.unit / a.num_kv_heads;
   const int32_t r0 = group * p.group_rows;
   const int32_t heads_per = a.num_heads / a.num_kv_heads;
   const int64_t most = table_tokens(a.table_width, a.page_size);
@@ -176,10 +184,11 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
     for (int d = 0; d < VD; ++d) o[t][d] = f32x4{0, 0, 0, 0};
   }
 
-  auto compute = [&](const KvTile<F8, D>& b, int32_t t0) {
-    const bool whole = b.valid == 0xffffffffu;
-    const bool ragged = !CHOSEN && t0 + kTok > shortest;  // some column ends inside the tile, or before it
-    if (b.valid == 0) return;
+  // One tile: `next` is called when its keys are no longer needed.
+  KvTile<F8, D> b;
+  auto compute = [&](uint32_t valid, int32_t t0, auto&& next) {
+    const bool whole = valid == 0xffffffffu;  // bit i: token i is in the cache and inside the part
+    const bool ragged = MODE == kRows && t0 + kTok > shortest;  // some column ends inside the tile, or before it
     f32x4 s[NT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -198,6 +207,11 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
         for (int i = 0; i < KS; ++i) s[t][u] = T::mfma16(kk[i], q[t][i], s[t][u]);
       }
     }
+    // The barriers keep the scheduler from starting the next loads into further
+    // registers before these are free.
+    __builtin_amdgcn_sched_barrier(0);
+    next();
+    __builtin_amdgcn_sched_barrier(0);
     u32x4 pk[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int i = (e >> 2) * 16 + g * 4 + (e & 3);
-          const bool in = ((b.valid >> i) & 1u) != 0 && (CHOSEN || t0 + i < collen[t]);
+          const bool in = ((valid >> i) & 1u) != 0 && (MODE != kRows || t0 + i < collen[t]);
           x[e] = in ? x[e] : -INFINITY;
         }
       }
@@ -249,14 +263,12 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
       }
     // One matrix step for value dim d of each lane's block; the words of
     // `keep` are all ones where the pair's tokens count.
-    auto accumulate = [&](int d, bool masked, u32x4 keep, f32x4(&out)[NT]) {
+    auto accumulate = [&](int d, u32x4 keep, int t) {
       const uint32_t sel = (d & 1) ? 0x07060302u : 0x05040100u;
       const int i = d >> 1;
       u32x4 vt = {__builtin_amdgcn_perm(v[1][i], v[0][i], sel), __builtin_amdgcn_perm(v[3][i], v[2][i], sel),
                   __builtin_amdgcn_perm(v[5][i], v[4][i], sel), __builtin_amdgcn_perm(v[7][i], v[6][i], sel)};
-      if (masked) vt &= keep;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) out[t] = T::mfma16(vt, pk[t], o[t][d]);
+      return T::mfma16(vt & keep, pk[t], o[t][d]);
     };
     auto keep_words = [&](uint32_t bits) {  // bits: the tile's tokens that count
       u32x4 k;
@@ -267,25 +279,13 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
       }
       return k;
     };
-    if (!ragged || p.group_rows == 1) {
-      if (whole) {
+    if (!ragged) {
+      u32x4 keep = {~0u, ~0u, ~0u, ~0u};
+      if (!whole) keep = keep_words(valid);
 #pragma unroll
-        for (int d = 0; d < VD; ++d) {
-          f32x4 out[NT];
-          accumulate(d, false, u32x4{}, out);
+      for (int d = 0; d < VD; ++d)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][d] = out[t];
-        }
-      } else {
-        const u32x4 keep = keep_words(b.valid);
-#pragma unroll
-        for (int d = 0; d < VD; ++d) {
-          f32x4 out[NT];
-          accumulate(d, true, keep, out);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][d] = out[t];
-        }
-      }
+        for (int t = 0; t < NT; ++t) o[t][d] = accumulate(d, keep, t);
       return;
     }
     // Rows of the sequence end at different places in this tile: one row's
@@ -293,34 +293,41 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 ? 2 : 1) attn_kernel(AttnP
     for (int32_t j = jlo; j <= jhi; ++j) {
       const int32_t left = clamp_to(a.lengths[r0 + j], most) - t0;
       if (left <= 0) continue;  // its weights in this tile are zeros
-      const u32x4 keep = keep_words(left >= 32 ? b.valid : b.valid & ((1u << left) - 1u));
+      const u32x4 keep = keep_words(left >= 32 ? valid : valid & ((1u << left) - 1u));
 #pragma unroll
-      for (int d = 0; d < VD; ++d) {
-        f32x4 out[NT];
-        accumulate(d, true, keep, out);
+      for (int d = 0; d < VD; ++d)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+          const f32x4 x = accumulate(d, keep, t);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[t][d][i] = colrow[t] == j ? out[t][i] : o[t][d][i];
-      }
+          for (int i = 0; i < 4; ++i) o[t][d][i] = colrow[t] == j ? x[i] : o[t][d][i];
+        }
     }
   };
 
-  // Two tiles in flight: one being read, one being used.
-  KvTile<F8, D> b0, b1;
+  // The next tile's keys are loaded once this one's scores are formed, its
+  // values once this one's are summed: the registers of one tile, and loads in
+  // flight all the time.  (Two whole tiles in registers left room for two
+  // wavefronts on a SIMD instead of three.)
   int32_t t = begin + w * kTok;
   if (t < end) {
     places.start(t + (lane & 31));
-    load_tile<F8, D>(b0, kbase, vbase, places.take(), lane);
+    int64_t off = places.take();
+    load_keys<F8, D>(b, kbase, off, lane);
+    load_values<F8, D>(b, vbase, off, lane);
     while (true) {
-      if (t + kStep < end) load_tile<F8, D>(b1, kbase, vbase, places.take(), lane);
-      compute(b0, t);
+      const uint32_t valid = (uint32_t)__builtin_amdgcn_ballot_w64(off >= 0);
+      const bool more = t + kStep < end;
+      compute(valid, t, [&] {
+        if (more) {
+          off = places.take();
+          load_keys<F8, D>(b, kbase, off, lane);
+        }
+      });
+      if (!more) break;
+      __builtin_amdgcn_sched_barrier(0);
+      load_values<F8, D>(b, vbase, off, lane);
       t += kStep;
-      if (t >= end) break;
-      if (t + kStep < end) load_tile<F8, D>(b0, kbase, vbase, places.take(), lane);
-      compute(b1, t);
-      t += kStep;
-      if (t >= end) break;
     }
   }
 
@@ -390,9 +397,8 @@ __global__ void __launch_bounds__(kAttnBlock) join_kernel(AttnParams p) {
   const int64_t at = MANY ? blockIdx.x : (int64_t)blockIdx.x * (kAttnBlock / 64) + w;
   if (at >= (int64_t)a.num_rows * a.num_heads) return;
   const int32_t row = (int32_t)(at / a.num_heads);
-  const int32_t n = a.chosen != nullptr
-                        ? a.num_chosen
-                        : group_length(p, row / p.group_rows * p.group_rows, table_tokens(a.table_width, a.page_size), lane);
+  const int64_t most = table_tokens(a.table_width, a.page_size);
+  const int32_t n = a.chosen != nullptr ? a.num_chosen : group_length(p, row / p.group_rows * p.group_rows, most, lane);
   const Split sp = split_of(n, p.most, p.least, p.unit);
   if (sp.parts == 1) return;
   // Every wavefront forms the weights: at most 128, two a lane.
@@ -447,14 +453,19 @@ __global__ void __launch_bounds__(kAttnBlock) join_kernel(AttnParams p) {
 
 namespace {
 
-template <typename T, bool F8, int D, bool CHOSEN>
+template <typename T, bool F8, int D, int MODE>
 const void* attn_tiles(int tiles) {
-  return tiles == 2 ? (const void*)&attn_kernel<T, F8, D, CHOSEN, 2> : (const void*)&attn_kernel<T, F8, D, CHOSEN, 1>;
+  return tiles == 2 ? (const void*)&attn_kernel<T, F8, D, MODE, 2> : (const void*)&attn_kernel<T, F8, D, MODE, 1>;
+}
+template <typename T, bool F8, int D>
+const void* attn_modes(int mode, int tiles) {
+  return mode == kOne ? attn_tiles<T, F8, D, kOne>(tiles)
+       : mode == kRows ? attn_tiles<T, F8, D, kRows>(tiles) : attn_tiles<T, F8, D, kChosen>(tiles);
 }
 template <typename T, bool F8>
-const void* attn_dims(int head_dim, bool chosen, int tiles) {
-  if (head_dim == 64) return chosen ? attn_tiles<T, F8, 64, true>(tiles) : attn_tiles<T, F8, 64, false>(tiles);
-  if (head_dim == 128) return chosen ? attn_tiles<T, F8, 128, true>(tiles) : attn_tiles<T, F8, 128, false>(tiles);
+const void* attn_dims(int head_dim, int mode, int tiles) {
+  if (head_dim == 64) return attn_modes<T, F8, 64>(mode, tiles);
+  if (head_dim == 128) return attn_modes<T, F8, 128>(mode, tiles);
   return nullptr;
 }
 template <typename T>
@@ -470,12 +481,13 @@ const void* join_dims(int head_dim, bool many) {
 
 }  // namespace
 
-const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int tiles) {
+const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int rows, int tiles) {
+  const int mode = chosen ? kChosen : rows > 1 ? kRows : kOne;
   if (dtype == PAGED_BF16)
-    return store == PAGED_E4M3 ? attn_dims<Bf16, true>(head_dim, chosen, tiles)
-                               : attn_dims<Bf16, false>(head_dim, chosen, tiles);
-  return store == PAGED_E4M3 ? attn_dims<Fp16, true>(head_dim, chosen, tiles)
-                             : attn_dims<Fp16, false>(head_dim, chosen, tiles);
+    return store == PAGED_E4M3 ? attn_dims<Bf16, true>(head_dim, mode, tiles)
+                               : attn_dims<Bf16, false>(head_dim, mode, tiles);
+  return store == PAGED_E4M3 ? attn_dims<Fp16, true>(head_dim, mode, tiles)
+                             : attn_dims<Fp16, false>(head_dim, mode, tiles);
 }
 
 const void* join_kernel_ptr(int dtype, int head_dim, bool many) {

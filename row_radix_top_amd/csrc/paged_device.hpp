@@ -135,6 +135,23 @@ struct Places {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Which (group of rows, part) and which of its `inner` units (heads, column
+// tiles) a workgroup takes.  Workgroups go to the eight XCDs in turn; all units
+// of a (group, part) are given to one XCD, one after the other.  They read
+// neighbouring bytes of the same tokens: with head h of every token on XCD
+// h % 8 each XCD's L2 would see one 256-byte column of the cache, a fraction
+// of its channels.  False past the last one.
+struct Work {
+  int32_t group, part, unit;
+};
+__device__ __forceinline__ bool work_of(uint32_t block, uint32_t inner, uint32_t groups, uint32_t most, Work* w) {
+  const uint32_t idx = block >> 3, outer = idx / inner * 8 + (block & 7);
+  w->unit = (int32_t)(idx % inner);
+  w->part = (int32_t)(outer / groups);
+  w->group = (int32_t)(outer - (uint32_t)w->part * groups);
+  return w->part < (int32_t)most;
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 

@@ -60,11 +60,23 @@ int check_types(paged_dtype dtype, paged_dtype store) {
 constexpr int32_t kUnit = 128;
 constexpr int32_t kLeast = 256;
 constexpr int32_t kMostParts = 128;
-constexpr int64_t kPartsPerCu = 4;  // workgroups per CU that a launch is split into
-// The latent kernel's: tiles of 32 or 64 tokens, one workgroup on a CU.
+// The latent kernel's: tiles of 64 tokens, one workgroup on a CU.
 constexpr int32_t kLatentUnit = 64;
 constexpr int32_t kLatentLeast = 128;
-constexpr int64_t kLatentPartsPerCu = 1;
+
+// How many parts the longest row gets, at most; units: workgroups of an
+// unsplit launch.  Times in us for 1, 2, 4, 8 and 16 parts at 256 CUs:
+//   4 x 8 units of 8192 positions        97   57   36   28   29
+//   8 units of 32768                    368  191  102   57   35 (64: 30)
+//   64 x 8 ragged, 1 to 32768           968  877  878  845  856
+//   256 x 8 ragged, 500 to 4096         490  476  480  517  540
+//   64 x 4 of 2048 chosen                31   33   35   38   38
+// So: two workgroups a CU; four parts at least where rows may differ in length
+// (the longest one ends the launch), one a CU is enough where all are alike.
+int64_t parts_for(bool latent, bool chosen, int64_t units, int64_t cus) {
+  if (latent || chosen) return ceil_div(cus, units);
+  return std::max<int64_t>(4, ceil_div(2 * cus, units));
+}
 
 int check_attention(const paged_attention_args* a, bool latent) {
   REQUIRE(a != nullptr, "null args");
@@ -150,13 +162,13 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
     p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
     p.groups = a->num_rows / p.group_rows;
     units = (int64_t)p.groups * a->num_kv_heads * p.col_tiles;
-    out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, tiles);
+    out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, p.group_rows, tiles);
   }
   const int64_t longest = chosen ? a->num_chosen : rrt::table_tokens(a->table_width, a->page_size);
-  int64_t most = a->max_splits > 0 ? a->max_splits : ceil_div((latent ? kLatentPartsPerCu : kPartsPerCu) * cus, units);
+  int64_t most = a->max_splits > 0 ? a->max_splits : parts_for(latent, chosen, units, cus);
   most = std::max<int64_t>(1, std::min<int64_t>({most, (int64_t)kMostParts, longest / p.least}));
   p.most = (int32_t)most;
-  out->grid = units * most;
+  out->grid = ceil_div((int64_t)p.groups * most, 8) * 8 * (units / p.groups);  // see work_of
   out->bytes = most == 1 ? 0 : (size_t)a->num_rows * a->num_heads * most * (a->head_dim * sizeof(float) + sizeof(float2));
   return TOPK_OK;
 }

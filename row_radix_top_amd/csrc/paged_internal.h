@@ -133,7 +133,7 @@ struct PrefillParams {
 // Kernel lookup: nullptr if there is no such instance.
 const void* layout_kernel_ptr();
 const void* append_kernel_ptr(int dtype, int store, bool wide);
-const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int tiles);
+const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int rows, int tiles);
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads);
 const void* join_kernel_ptr(int dtype, int head_dim, bool many);
 const void* expand_kernel_ptr(int dtype, int store, int latent_dim);
