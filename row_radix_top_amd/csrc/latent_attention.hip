@@ -1,6 +1,8 @@
 // The absorbed form of latent attention: all heads of a row read one shared
 // vector a token, as keys whole and as values without its rope part.
 
+#include <type_traits>
+
 #include "paged_device.hpp"
 
 namespace rrt {
@@ -11,22 +13,30 @@ namespace rrt {
 //
 // 2 (2 DC + 64) flop a head and token against 2 (DC + 64) bytes a token: with
 // 128 heads near the card's balance of matrix rate and memory rate, with few
-// heads bound by memory.  Every token's vector is used by all heads and twice
-// (scores, values), so a tile of TT tokens is staged in LDS once, in 16 bits,
-// two buffers deep: the next tile's loads go straight to LDS while this one is
-// used (an e4m3 cache goes through registers, where it is widened).
+// heads bound by memory.  Every token's vector is used by all
+// heads and twice (scores, values), so a tile of 64 tokens is staged in LDS
+// once, in 16 bits, two buffers deep: the next tile's loads go straight to LDS
+// while this one is used.  (An e4m3 cache: the raw bytes go to two buffers of
+// half the size, and each wavefront widens its own tokens into one tile.)
 //
-//   S^T[token][head] = C Q^T: WH x WT wavefronts split heads and tokens; each
+//   S^T[token][head] = C Q^T: 2 x 4 wavefronts split heads and tokens; each
 //     keeps the queries of its heads in registers for the whole part.
-//   O^T[dim][head] += C^T P^T: each wavefront owns a quarter of the value dims
+//   O^T[dim][head] += C^T P^T: each wavefront owns an eighth of the value dims
 //     for all heads, so the values are read from LDS once in all; their
 //     transpose is the LDS read instruction's.  P passes through LDS.
 //
+// Eight wavefronts, two on a SIMD, with 256 registers each: queries 144 (two
+// 16-head columns a wavefront, so a key operand serves two products) and
+// outputs 64 at 512 dims and 64 heads.  One wavefront a SIMD with all 512 was
+// slower however its products were overlapped: loads, addresses, weights and
+// LDS latencies then add up, with no second wavefront to run meanwhile
+// (5300 cycles for 32 tokens of which 1090 on the matrix unit).
+//
 // The weights are relative to a reference that follows the running maximum
 // lazily: only when a score passes it by 2^8 does the workgroup agree on a new
-// one and rescale (P then stays below 2^8, sums below 2^8 n: far inside
-// fp32; relative precision does not depend on the reference).  So most tiles
-// take two barriers and no rescaling.
+// one, form the weights again and rescale (P then stays below 2^8, sums below
+// 2^8 n: far inside fp32; relative precision does not depend on the
+// reference).
 //
 // LDS rows are a multiple of all banks wide; 16-byte chunk c of token t's row
 // is kept at c ^ swizzle(t), which spreads both the 16 tokens of a key operand
@@ -34,11 +44,12 @@ namespace rrt {
 // ---------------------------------------------------------------------------
 constexpr int kRope = PAGED_ROPE_DIM;
 constexpr float kLazy = 8.0f;
-constexpr int kAhead = 4;  // operands in flight from LDS
+constexpr int kAhead = 4;  // key operands in flight from LDS, and one in use
 
 using i16x4 = short __attribute__((ext_vector_type(4)));
 using lds_i16x4 = __attribute__((address_space(3))) i16x4;
 using lds_u32x4 = __attribute__((address_space(3))) u32x4;
+using lds_i32 = __attribute__((address_space(3))) int32_t;
 using lds_u32x2 = __attribute__((address_space(3))) u32x2;
 
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
@@ -57,20 +68,19 @@ __device__ __forceinline__ uint32_t fresh(uint32_t x) {
   return x;
 }
 
-constexpr int latent_waves(int heads) { return heads == 32 ? 8 : 4; }
+constexpr int kLatentBlock = 512;
 
 template <int DC, int HT>
 struct LatentShape {
-  static constexpr int NW = latent_waves(HT);        // wavefronts
-  static constexpr int TT = 64;                     // tokens of a tile
-  static constexpr int WT = HT == 64 ? 2 : 4;                   // wavefronts along the tokens of the scores
-  static constexpr int WH = NW / WT;                // and along the heads
-  static constexpr int NH = HT / 16 / WH;           // 16-head columns of a wavefront's scores
-  static constexpr int NU = TT / 16 / WT;           // 16-token rows of a wavefront's scores
-  static constexpr int KS = (DC + kRope) / 32;      // matrix steps over the key dims
-  static constexpr int ND = DC / 16 / NW;           // 16-dim rows of a wavefront's output
-  static constexpr int NC = HT / 16;                // 16-head columns of the output
-  static constexpr int PT = TT + 16;                // pitch of the weights (rows 40 banks apart)
+  static constexpr int NW = 8;                  // wavefronts
+  static constexpr int TT = 64;                 // tokens of a tile
+  static constexpr int WT = 4;                  // wavefronts along the tokens of the scores, 16 each
+  static constexpr int WH = 2;                  // and along the heads
+  static constexpr int NH = HT / 16 / WH;       // 16-head columns of a wavefront's scores
+  static constexpr int KS = (DC + kRope) / 32;  // matrix steps over the key dims
+  static constexpr int ND = DC / 16 / NW;       // 16-dim rows of a wavefront's output
+  static constexpr int NC = HT / 16;            // 16-head columns of the output
+  static constexpr int PT = TT + 16;            // pitch of the weights (rows 40 banks apart)
 };
 
 // Sixteen-byte reads are served in groups of lanes {0-3, 12-15, 20-27} and so
@@ -85,26 +95,43 @@ __device__ __forceinline__ int swz(int t) {
 }
 __device__ __forceinline__ int swz_rope(int t) { return (t >> 1) & 7; }
 
-// 64 lanes x 16 bytes from the lanes' addresses to 1 KB of LDS at `to` (wave
-// uniform); counted by vmcnt, no registers are written.
+// Loads straight to LDS: 16 (4) bytes from each active lane's address to `to`
+// (wave uniform) + 16 (4) x lane.  No register is written, so nothing but
+// wait_loads() below waits for them; as instructions that the compiler knows
+// to write LDS, they made it wait for all of them before every transposed read.
 __device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
-                                   (__attribute__((address_space(3))) uint32_t*)(uintptr_t)to, 16, 0, 0);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(from) : "memory");
+}
+__device__ __forceinline__ void load4_to_lds(const int32_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
+}
+// Waits until all but the last N loads have arrived.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 template <typename T, bool F8, int DC, bool CHOSEN, int HT>
-__global__ void __launch_bounds__(latent_waves(HT) * 64, latent_waves(HT) / 4) latent_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kLatentBlock, 2) latent_kernel(AttnParams p) {
   using S = LatentShape<DC, HT>;
-  constexpr int TT = S::TT, NH = S::NH, NU = S::NU, KS = S::KS, ND = S::ND, NC = S::NC, PT = S::PT, WT = S::WT, NW = S::NW;
-  constexpr int TW = TT / NW;  // tokens that a wavefront loads
+  constexpr int NW = S::NW, TT = S::TT, NH = S::NH, KS = S::KS, ND = S::ND, NC = S::NC, PT = S::PT, WT = S::WT;
+  constexpr int TW = TT / NW;                 // tokens that a wavefront loads
   constexpr int SZ = F8 ? 1 : 2;
-  __shared__ __align__(1024) uint16_t sc[2][TT * DC];
-  __shared__ __align__(1024) uint16_t sr[2][TT * kRope];
+  constexpr int ROW = (DC + kRope) * SZ;      // bytes of a raw token
+  constexpr uint32_t kTileBytes = TT * DC * 2, kRawBytes = TT * ROW;
+  constexpr int NB = F8 ? 1 : 2;              // tiles in 16 bits
+  __shared__ __align__(1024) uint16_t sc[NB][TT * DC];
+  __shared__ __align__(1024) uint16_t sr[TT * kRope];
+  __shared__ __align__(1024) char sraw[F8 ? kRawBytes : 16];
+  __shared__ __align__(1024) u32x4 sq[S::WH * NH * (kRope / 32)][64];
   __shared__ __align__(16) uint16_t sp_[HT * PT];
   __shared__ float smax[WT][HT], ssum[WT][HT], salpha[HT];
-  __shared__ uint32_t svalid[2][NW];
-  __shared__ uint32_t sflag[2];
+  __shared__ int32_t spos[2][TT], spage[2][TT];
+  __shared__ __align__(8) uint8_t svalid[2][NW];
+  __shared__ int32_t sflag[2];  // the tile (plus one) whose scores pass the reference
   const paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -126,91 +153,178 @@ __global__ void __launch_bounds__(latent_waves(HT) * 64, latent_waves(HT) / 4) l
   const int32_t* chosen = CHOSEN ? a.chosen + (int64_t)row * a.chosen_stride : nullptr;
   const char* cache = (const char*)a.k;
 
-  // Places of the wavefront's token `lane % TW` of each tile.
-  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, p.page, a.num_pages, seen, end, TT};
+  // --- places of a tile's tokens -------------------------------------------
+  // Lane l looks after the wavefront's token l % TW.  The chosen position of a
+  // token of tile t + 2, the page of one of tile t + 1 and tile t's data are
+  // on their way at the same time, all of them straight to LDS, so that the
+  // one wait of a tile covers each and nothing waits for a place alone.
+  const int32_t first = begin + w * TW;
+  constexpr uint32_t kSlot = TT * 4;
+  const uint32_t pos_at = lds_at(&spos[0][0]) + (uint32_t)w * (TW * 4), page_at = lds_at(&spage[0][0]) + (uint32_t)w * (TW * 4);
+  auto fetch_chosen = [&](int32_t t) {
+    if constexpr (CHOSEN) {
+      const uint32_t ln = fresh((uint32_t)lane);
+      const int32_t i = first + t * TT + (int32_t)(ln & (TW - 1));
+      if (ln < TW) load4_to_lds(chosen + (i < end ? i : end - 1), pos_at + ((uint32_t)t & 1) * kSlot);
+    }
+  };
+  // Starts the page's load; returns the token's offset inside it (all ones: no
+  // such token).
+  auto fetch_page = [&](int32_t t) -> uint32_t {
+    const uint32_t slot = ((uint32_t)t & 1) * kSlot;
+    const uint32_t ln = fresh((uint32_t)lane), l8 = ln & (TW - 1);
+    const int32_t i = first + t * TT + (int32_t)l8;
+    int32_t pos = i;
+    if constexpr (CHOSEN) pos = *(lds_i32*)(pos_at + slot + l8 * 4);
+    const bool ok = i < end && (!CHOSEN || (uint32_t)pos < (uint32_t)seen);
+    const uint32_t x = ok ? (uint32_t)pos : 0u, j = divide(x, p.page);
+    if (ln < TW) load4_to_lds(table + j, page_at + slot);
+    return ok ? x - j * p.page.by : ~0u;
+  };
+  auto place = [&](int32_t t, uint32_t in) -> int64_t {
+    const int32_t page = *(lds_i32*)(page_at + ((uint32_t)t & 1) * kSlot + (fresh((uint32_t)lane) & (TW - 1)) * 4);
+    return in == ~0u || (uint32_t)page >= (uint32_t)a.num_pages
+               ? -1
+               : (int64_t)page * a.page_stride + (int64_t)in * a.token_stride;
+  };
 
   // --- loads of a tile -----------------------------------------------------
-  constexpr int LT = F8 ? DC / 16 : DC / 8;      // lanes (16 bytes each) of a token's latent part
-  constexpr int PER = 64 / LT;                   // tokens of one load
-  constexpr int NL = TW / PER;                   // loads
-  constexpr int RT = F8 ? 4 : 8;                 // lanes of a token's rope part
-  constexpr int NR = (TW * RT + 63) / 64;        // loads of the rope parts
-  u32x4 stage[F8 ? NL : 1], stage_r[F8 ? NR : 1];
-
-  auto issue = [&](int64_t off, int b) {
-    const uint32_t valid = (uint32_t)__builtin_amdgcn_ballot_w64(off >= 0) & (TW == 32 ? ~0u : (1u << TW) - 1u);
-    if (lane == 0) svalid[b][w] = valid;
+  // LT lanes of 16 bytes hold a token's latent part, RT its rope part.  swz is
+  // linear over the bits of its argument, so a lane's chunk offset is its own
+  // part, fixed, and a wave-uniform part for each load.  Raw e4m3 rows lie as
+  // they are.
+  constexpr int LT = DC * SZ / 16, PER = 64 / LT, NL = TW / PER;
+  constexpr int RT = kRope * SZ / 16;
+  uint32_t recent = 0;  // which of the wavefront's tokens count, a byte a tile, the last one lowest
+  // Rope parts have one buffer: theirs start when the scores before them are
+  // formed (e4m3: with the rest; the raw bytes are the wavefront's own).
+  const char* rope_from = nullptr;
+  auto issue = [&](int32_t t, uint32_t in) {
+    const uint32_t b = (uint32_t)t & 1;
+    const int64_t off = place(t, in);
+    const uint32_t valid = (uint32_t)__builtin_amdgcn_ballot_w64(off >= 0) & ((1u << TW) - 1u);
+    recent = recent << 8 | valid;
     const int64_t at = (off < 0 ? 0 : off) * SZ;
-    const int lane = (int)fresh((uint32_t)threadIdx.x & 63u);
-    int64_t rope_at[NR];
+    const uint32_t ln = fresh((uint32_t)lane);
+    if (ln == 0) svalid[b][w] = (uint8_t)valid;
+    const uint32_t sub = PER == 1 ? 0u : ln / LT, chunk = ln % LT;
+    const uint32_t lane_chunk = F8 ? chunk * 16 : (chunk ^ (uint32_t)swz((int)sub)) << 4;
+    const uint32_t wave_swz = F8 ? 0u : (uint32_t)swz(w * TW) << 4;
+    const uint32_t to = F8 ? lds_at(&sraw[0]) + (uint32_t)(w * TW) * DC
+                           : lds_at(&sc[0][0]) + b * kTileBytes + (uint32_t)(w * TW) * (DC * 2);
 #pragma unroll
-    for (int i = 0; i < NR; ++i) rope_at[i] = shfl64(at, (i * (64 / RT) + lane / RT) & (TW - 1));
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int t = i * PER + lane / LT;  // of the wavefront's tokens
-      const int c = lane % LT;
-      int64_t place = readlane64(at, i * PER);
-#pragma unroll
-      for (int k = 1; k < PER; ++k) place = lane / LT >= k ? readlane64(at, i * PER + k) : place;
-      const char* from = cache + place;
-      if constexpr (F8) {
-        stage[i] = *(const u32x4*)(from + c * 16);
+    for (int k = 0; k < NL; ++k) {
+      const uint32_t offset = F8 ? lane_chunk : lane_chunk ^ (wave_swz ^ ((uint32_t)swz(k * PER) << 4));
+      if constexpr (PER == 1) {
+        load_to_lds(cache + readlane64(at, k), offset, to + (uint32_t)k * 1024);
       } else {
-        const int tt = w * TW + t;
-        load_to_lds(from + (uint32_t)((c ^ swz(tt)) * 16), lds_at(&sc[b][(w * TW + i * PER) * DC]));
-      }
-    }
+        int64_t where = readlane64(at, k * PER);
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int t = i * (64 / RT) + lane / RT;
-      const int c = lane % RT;
-      const char* from = cache + rope_at[i] + DC * SZ;
-      if constexpr (F8) {
-        stage_r[i] = *(const u32x4*)(from + c * 16);
-      } else {
-        const int tt = w * TW + t;
-        load_to_lds(from + ((c ^ swz_rope(tt)) * 16), lds_at(&sr[b][(w * TW + i * (64 / RT)) * kRope]));
+        for (int j = 1; j < PER; ++j) where = sub >= (uint32_t)j ? readlane64(at, k * PER + j) : where;
+        load_to_lds(cache + where + offset, to + (uint32_t)k * 1024);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  // e4m3: the staged tile, widened, into its buffer.
-  auto store = [&](int b) {
+    const uint32_t tok = (ln / RT) & (TW - 1), rchunk = ln % RT;
+    const char* rope = cache + shfl64(at, (int)tok) + DC * SZ;
     if constexpr (F8) {
-      const int lane = (int)fresh((uint32_t)threadIdx.x & 63u);
+      if (ln < TW * RT)
+        load_to_lds(rope + rchunk * 16, lds_at(&sraw[0]) + TT * DC + (uint32_t)(w * TW) * kRope);
+    } else {
+      rope_from = rope + ((rchunk ^ (uint32_t)swz_rope(w * TW + (int)tok)) << 4);
+    }
+  };
+  auto issue_rope = [&] {
+    if constexpr (!F8) load_to_lds(rope_from, lds_at(&sr[0]) + (uint32_t)(w * TW) * (kRope * 2));
+  };
+  // e4m3: the wavefront's raw tokens of tile t, widened, into the tile.
+  auto widen_tile = [&] {
+    if constexpr (F8) {
+      const uint32_t ln = fresh((uint32_t)lane);
+      const uint32_t raw = lds_at(&sraw[0]) + (uint32_t)(w * TW) * DC + ln * 16;
+      const uint32_t sub = ln / LT;
+      const uint32_t base = lds_at(&sc[0][0]) + ((uint32_t)(w * TW) + sub) * (DC * 2) +
+                            ((((ln % LT) * 2) ^ (uint32_t)swz((int)sub) ^ (uint32_t)swz(w * TW)) << 4);
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int tt = w * TW + i * PER + lane / LT, c = (lane % LT) * 2;
-        u32x4* rowp = (u32x4*)&sc[b][tt * DC];
-        rowp[c ^ swz(tt)] = widen<T>(u32x2{stage[i][0], stage[i][1]});
-        rowp[(c + 1) ^ swz(tt)] = widen<T>(u32x2{stage[i][2], stage[i][3]});
+      for (int k = 0; k < NL; ++k) {
+        const u32x4 x = lds_read16(raw + (uint32_t)k * 1024);
+        const uint32_t to = (base ^ ((uint32_t)swz(k * PER) << 4)) + (uint32_t)(k * PER) * (DC * 2);
+        *(lds_u32x4*)to = widen<T>(u32x2{x[0], x[1]});
+        *(lds_u32x4*)(to ^ 16) = widen<T>(u32x2{x[2], x[3]});
       }
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const int t = i * (64 / RT) + lane / RT, c = (lane % RT) * 2;
-        if (t >= TW) continue;
-        const int tt = w * TW + t;
-        u32x4* rowp = (u32x4*)&sr[b][tt * kRope];
-        rowp[c ^ swz_rope(tt)] = widen<T>(u32x2{stage_r[i][0], stage_r[i][1]});
-        rowp[(c + 1) ^ swz_rope(tt)] = widen<T>(u32x2{stage_r[i][2], stage_r[i][3]});
+      if (ln < TW * RT) {
+        const uint32_t tt = (uint32_t)(w * TW) + ln / RT;
+        const u32x4 x = lds_read16(lds_at(&sraw[0]) + TT * DC + (uint32_t)(w * TW) * kRope + ln * 16);
+        const uint32_t to = lds_at(&sr[0]) + tt * (kRope * 2) + ((((ln % RT) * 2) ^ (uint32_t)swz_rope((int)tt)) << 4);
+        *(lds_u32x4*)to = widen<T>(u32x2{x[0], x[1]});
+        *(lds_u32x4*)(to ^ 16) = widen<T>(u32x2{x[2], x[3]});
       }
     }
   };
+  // Tokens of the wavefront that do not count become zeros: their places may
+  // hold NaN.  Before the barrier that shows the tile.
+  auto clear = [&](uint32_t b, uint32_t valid) {
+    if (valid == (1u << TW) - 1u) return;
+#pragma nounroll
+    for (int t = 0; t < TW; ++t) {
+      if ((valid >> t) & 1u) continue;
+      const uint32_t tt = (uint32_t)(w * TW + t);
+      if (lane < DC / 8) *(lds_u32x4*)(lds_at(&sc[0][0]) + b * kTileBytes + tt * (DC * 2) + (uint32_t)lane * 16) = u32x4{0, 0, 0, 0};
+      if (lane < kRope / 8) *(lds_u32x4*)(lds_at(&sr[0]) + tt * (kRope * 2) + (uint32_t)lane * 16) = u32x4{0, 0, 0, 0};
+    }
+  };
 
+  // Queries of the wavefront's heads, as the scores' second operand.  The
+  // latent part stays in the half of the register file that only matrix
+  // instructions read, and fills it; the rope part lies in LDS.
+  constexpr int KL = DC / 32, KR = kRope / 32;
+  u32x4 q[NH][KL];
+  // They come through LDS, where the tile that is not yet in use takes all
+  // heads' rows once (each wavefront reading its own from memory, in 64-byte
+  // pieces and four times over, took 9 us).
+  auto issue_queries = [&] {
+    constexpr int QL = DC / 8, QPER = 64 / QL, HW = HT / NW;
+    static_assert(S::WH * NH * KR <= NW, "a rope fragment a wavefront");
+    const uint32_t ln = (uint32_t)lane;
+    auto row_of_head = [&](int32_t head) {  // columns past the last head compute a copy of head 0 that is not written
+      return (const char*)a.q + 2 * ((int64_t)row * a.q_row_stride +
+                                     (int64_t)(head < a.num_heads ? head : 0) * a.q_head_stride);
+    };
+#pragma unroll
+    for (int k = 0; k < HW / QPER; ++k) {
+      const int h = w * HW + k * QPER + (int)(ln / QL);
+      load_to_lds(row_of_head(head0 + h) + (((ln % QL) ^ (uint32_t)swz(h)) << 4),
+                  lds_at(&sc[NB - 1][0]) + (uint32_t)(w * HW + k * QPER) * (DC * 2));
+    }
+    if (w < S::WH * NH * KR)
+      load_to_lds(row_of_head(head0 + (w / KR) * 16 + col) + (DC + (w % KR) * 32 + g * 8) * 2, lds_at(&sq[w][0]));
+  };
+  auto rope_query = [&](int h, int i) { return lds_at(&sq[(wh * NH + h) * KR + i][0]) + fresh((uint32_t)lane) * 16; };
+  // The first tile's chain of reads (positions, pages, data) and the queries
+  // are on their way together: one trip to memory after the other is most of a
+  // short part's time.
+  uint32_t in = ~0u;  // of the tile that is issued next
+  uint32_t in0 = ~0u;
+  for (int32_t t = 0; t < 2 && t < tiles; ++t) fetch_chosen(t);
+  issue_queries();
+  wait_loads<HT * DC / 8 / 64 / NW>();  // all but the queries
+  if (tiles > 0) in0 = fetch_page(0);
+  if (tiles > 1) in = fetch_page(1);
+  if (tiles > 2) fetch_chosen(2);  // into the first tile's slot, read by then
+  wait_loads<0>();
   if (tiles > 0) {
-    places.start(begin + w * TW + (lane & (TW - 1)));
-    issue(places.take(), 0);
+    issue(0, in0);
+    issue_rope();
   }
-
-  // Queries of the wavefront's heads, as the scores' second operand.
-  u32x4 q[NH][KS];
+  __syncthreads();
 #pragma unroll
   for (int h = 0; h < NH; ++h) {
-    const int32_t head = head0 + (wh * NH + h) * 16 + col;
-    // Columns past the last head compute a copy of head 0 that is not written.
-    const char* qp = (const char*)a.q + 2 * ((int64_t)row * a.q_row_stride +
-                                             (int64_t)(head < a.num_heads ? head : 0) * a.q_head_stride);
+    const int t = (wh * NH + h) * 16 + col;
+    const uint32_t at = lds_at(&sc[NB - 1][0]) + (uint32_t)t * (DC * 2) + (((uint32_t)g ^ (uint32_t)swz(t)) << 4);
 #pragma unroll
-    for (int i = 0; i < KS; ++i) q[h][i] = *(const u32x4*)(qp + 2 * (i * 32 + g * 8));
+    for (int i = 0; i < KL; ++i) q[h][i] = lds_read16((at ^ ((i & 3) << 6)) + (i >> 2) * 256);
+#pragma unroll
+    for (int i = 0; i < KL; ++i) asm volatile("" : "+a"(q[h][i]));
   }
   const float by_cache = F8 && a.k_scales != nullptr ? a.k_scales[0] : 1.0f;
   const float scale = p.scale_log2 * by_cache;
@@ -224,176 +338,148 @@ __global__ void __launch_bounds__(latent_waves(HT) * 64, latent_waves(HT) / 4) l
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[c][d] = f32x4{0, 0, 0, 0};
   if (tid < 2) sflag[tid] = 0;
-  if (tiles > 0) store(0);
 
   for (int32_t i = 0; i < tiles; ++i) {
-    const int b = i & 1;
-    if constexpr (!F8) wait_loads();
-    // Tokens that do not count become zeros: their places may hold NaN.
-    {
-      const uint32_t mine = __builtin_amdgcn_readfirstlane(svalid[b][w]);
-      constexpr uint32_t all = TW == 32 ? ~0u : (1u << TW) - 1u;
-      if (mine != all) {
-        for (int t = 0; t < TW; ++t) {
-          if ((mine >> t) & 1u) continue;
-          const int tt = w * TW + t;
-          for (int c = lane; c < DC / 8; c += 64) ((u32x4*)&sc[b][tt * DC])[c] = u32x4{0, 0, 0, 0};
-          if (lane < 8) ((u32x4*)&sr[b][tt * kRope])[lane] = u32x4{0, 0, 0, 0};
-        }
-      }
+    const uint32_t b = F8 ? 0u : (uint32_t)i & 1;
+    wait_loads<0>();  // the tile, the next one's pages and the positions after that
+    if constexpr (F8) {
+      __syncthreads();  // the tile before is no longer read
+      widen_tile();
     }
+    clear(b, recent & ((1u << TW) - 1u));
     __syncthreads();
-    if (tid == 0) sflag[b ^ 1] = 0;
-    if (i + 1 < tiles) issue(places.take(), b ^ 1);
-
     // Scores.  Address bits 4..7 of a row's chunk are (4 (k % 4) + g) ^ swz, so
-    // step k is one exclusive-or away from step 0.
+    // step k is one exclusive-or away from step 0.  A ring keeps the reads some
+    // steps ahead; the scheduling barriers keep the compiler from reading all
+    // operands at once into registers that it does not have.
     const uint32_t ln = fresh((uint32_t)lane), lcol = ln & 15, lg = ln >> 4;
-    const uint32_t buf = lds_at(&sc[0][0]) + (uint32_t)b * (TT * DC * 2), bufr = lds_at(&sr[0][0]) + (uint32_t)b * (TT * kRope * 2);
-    uint32_t krow[NU], rrow[NU];
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const uint32_t tt = (uint32_t)(wt * NU + u) * 16 + lcol;
-      krow[u] = buf + tt * (DC * 2) + ((lg ^ (uint32_t)swz((int)tt)) << 4);
-      rrow[u] = bufr + tt * (kRope * 2) + ((lg ^ (uint32_t)swz_rope((int)tt)) << 4);
-    }
-    f32x4 s[NH][NU];
-#pragma unroll
-    for (int h = 0; h < NH; ++h)
-#pragma unroll
-      for (int u = 0; u < NU; ++u) s[h][u] = f32x4{0, 0, 0, 0};
-    // A ring of key operands, so that reads are some steps ahead; the barriers
-    // keep the scheduler from reading all of them at once into registers that
-    // the accumulators need.
-    auto key = [&](int k, int u) {
-      return k < DC / 32 ? lds_read16((krow[u] ^ ((k & 3) << 6)) + (k >> 2) * 256)
-                         : lds_read16(rrow[u] ^ ((k - DC / 32) << 6));
+    const uint32_t ktok = (uint32_t)wt * 16 + lcol;
+    const uint32_t krow = lds_at(&sc[0][0]) + b * kTileBytes + ktok * (DC * 2) + ((lg ^ (uint32_t)swz((int)ktok)) << 4);
+    const uint32_t rrow = lds_at(&sr[0]) + ktok * (kRope * 2) + ((lg ^ (uint32_t)swz_rope((int)ktok)) << 4);
+    auto key = [&](int k) {
+      return k < KL ? lds_read16((krow ^ ((k & 3) << 6)) + (k >> 2) * 256) : lds_read16(rrow ^ ((k - KL) << 6));
     };
-    u32x4 kk[kAhead][NU];
+    // The next tile's loads.  Half the wavefronts, one of the two on each
+    // SIMD, start them before their scores and half behind, so that one's
+    // addresses are formed under the other's matrix products.
+    auto ahead = [&] {
+      if (i + 3 < tiles) fetch_chosen(i + 3);
+      const uint32_t next = i + 2 < tiles ? fetch_page(i + 2) : ~0u;
+      if (i + 1 < tiles) issue(i + 1, in);
+      in = next;
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (w < NW / 2) ahead();
+    const uint32_t shown = *(const uint16_t*)&svalid[i & 1][wt * 2];
+    u32x4 ring[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead - 1; ++k)
+    for (int n = 0; n < kAhead - 1; ++n) ring[n] = key(n);
+    f32x4 s[NH];
 #pragma unroll
-      for (int u = 0; u < NU; ++u) kk[k][u] = key(k, u);
+    for (int h = 0; h < NH; ++h) s[h] = f32x4{0, 0, 0, 0};
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      if (k + kAhead - 1 < KS) {
+    for (int n = 0; n < KS; ++n) {
+      if (n + kAhead - 1 < KS) ring[(n + kAhead - 1) % kAhead] = key(n + kAhead - 1);
 #pragma unroll
-        for (int u = 0; u < NU; ++u) kk[(k + kAhead - 1) % kAhead][u] = key(k + kAhead - 1, u);
-      }
-#pragma unroll
-      for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int h = 0; h < NH; ++h) s[h][u] = T::mfma16(kk[k % kAhead][u], q[h][k], s[h][u]);
+      for (int h = 0; h < NH; ++h)
+        s[h] = T::mfma16(ring[n % kAhead], n < KL ? q[h][n < KL ? n : 0] : lds_read16(rope_query(h, n < KL ? 0 : n - KL)), s[h]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    float top[NH];
-    uint64_t valid = 0;
-#pragma unroll
-    for (int k = NW - 1; k >= 0; --k) valid = (valid << TW) | __builtin_amdgcn_readfirstlane(svalid[b][k]);
-    constexpr uint64_t every = TT == 64 ? ~0ull : (1ull << (TT & 63)) - 1ull;
+    if (w >= NW / 2) ahead();
+    // Scaled and masked, and each head's maximum over the wavefront's tokens.
+    const uint32_t bits = __builtin_amdgcn_readfirstlane(shown);
+    float top[NH], kept[NH];
+    bool past = false;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      top[h] = -INFINITY;
+      s[h] *= scale;
+      if (bits != 0xffffu) {
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        s[h][u] *= scale;
-        if (valid != every) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[h][u][e] = (valid >> ((wt * NU + u) * 16 + g * 4 + e)) & 1u ? s[h][u][e] : -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top[h] = fmaxf(top[h], s[h][u][e]);
+        for (int e = 0; e < 4; ++e) s[h][e] = (bits >> (lg * 4 + e)) & 1u ? s[h][e] : -INFINITY;
       }
-      top[h] = fmaxf(top[h], __shfl_xor(top[h], 16));
-      top[h] = fmaxf(top[h], __shfl_xor(top[h], 32));
+      top[h] = max_xor32(max_xor16(fmaxf(fmaxf(s[h][0], s[h][1]), fmaxf(s[h][2], s[h][3]))));
+      past = past || top[h] > ref[h] + kLazy;
+      kept[h] = sum[h];
     }
-    auto weights = [&]() {
+    if (__builtin_amdgcn_ballot_w64(past) != 0 && ln == 0) sflag[i & 1] = i + 1;
+    // Weights under the present reference.
+    auto weights = [&] {
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         const float r = ref[h] == -INFINITY ? 0.0f : ref[h];
+        float x[4];
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          float x[4];
+        for (int e = 0; e < 4; ++e) x[e] = exp2_fast(s[h][e] - r);
+        sum[h] = kept[h] + ((x[0] + x[1]) + (x[2] + x[3]));
+        *(lds_u32x2*)(lds_at(sp_) + ((((wh * NH + h) * 16 + lcol) * PT + wt * 16 + lg * 4) * 2)) =
+            u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+      }
+    };
+    weights();
+    __syncthreads();
+    if (i + 1 < tiles) issue_rope();
+    const int32_t flag = sflag[i & 1];
+    // Values.  The wavefront's dims are 16 of every 128, so that they are a
+    // fixed distance apart whatever the swizzle.
+    const uint32_t prow = lds_at(sp_) + lcol * (PT * 2) + lg * 16;
+    const uint32_t dims = (uint32_t)w * 2 + ((lcol & 3) >> 1);
+    u32x4 v[ND];
+    auto values = [&](int k) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = exp2_fast(s[h][u][e] - r);
-          sum[h] += (x[0] + x[1]) + (x[2] + x[3]);
-          *(u32x2*)&sp_[((wh * NH + h) * 16 + col) * PT + (wt * NU + u) * 16 + g * 4] =
-              u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t tt = k * 32 + lg * 8 + half * 4 + (lcol >> 2);
+        const uint32_t at = lds_at(&sc[0][0]) + b * kTileBytes + tt * (DC * 2) + ((dims ^ (uint32_t)swz((int)tt)) << 4) + (lcol & 1) * 8;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const u32x2 x = lds_read_tr(at + d * 256);
+          v[d][half * 2] = x[0], v[d][half * 2 + 1] = x[1];
         }
       }
     };
-    bool past = false;
-#pragma unroll
-    for (int h = 0; h < NH; ++h) past = past || top[h] > ref[h] + kLazy;
-    if (__builtin_amdgcn_ballot_w64(past) != 0) {
-      if (lane == 0) sflag[b] = 1;
-    }
-    float kept[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) kept[h] = sum[h];
-    weights();
-    __syncthreads();
-    if (__builtin_amdgcn_readfirstlane(sflag[b]) != 0) {
+    values(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (__builtin_amdgcn_readfirstlane(flag) == i + 1) {
       // A new reference for every head, the maximum so far.
-      if (lane < 16) {
+      if (ln < 16) {
 #pragma unroll
-        for (int h = 0; h < NH; ++h) smax[wt][(wh * NH + h) * 16 + lane] = top[h];
+        for (int h = 0; h < NH; ++h) smax[wt][(wh * NH + h) * 16 + ln] = top[h];
       }
       __syncthreads();
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        const int at = (wh * NH + h) * 16 + col;
+        const int at = (wh * NH + h) * 16 + (int)lcol;
         float m = ref[h];
 #pragma unroll
         for (int k = 0; k < WT; ++k) m = fmaxf(m, smax[k][at]);
         const float by = m == ref[h] ? 1.0f : exp2_fast(ref[h] - m);
         ref[h] = m;
-        sum[h] = kept[h] * by;
-        if (wt == 0 && lane < 16) salpha[at] = by;
+        kept[h] *= by;
+        if (wt == 0 && ln < 16) salpha[at] = by;
       }
       weights();
       __syncthreads();
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const float by = salpha[c * 16 + col];
+        const float by = salpha[c * 16 + lcol];
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[c][d] *= by;
       }
     }
-
-    // Values.  Dims d of the wavefront's quarter: again an exclusive-or away.
-    const uint32_t prow = lds_at(sp_) + lcol * (PT * 2) + lg * 16;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < TT / 32; ++k) {
-      u32x4 pw[NC];
+      u32x4 pw[2];
+      pw[0] = lds_read16(prow + k * 64);
+      if (k > 0) values(k);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) pw[c] = lds_read16(prow + c * (16 * PT * 2) + k * 64);
-      uint32_t vrow[2];
+      for (int c = 0; c < NC; ++c) {
+        if (c + 1 < NC) pw[(c + 1) & 1] = lds_read16(prow + (c + 1) * (16 * PT * 2) + k * 64);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t tt = k * 32 + lg * 8 + half * 4 + (lcol >> 2);
-        const uint32_t chunk = (uint32_t)w * (DC / 8 / NW) + ((lcol & 3) >> 1);
-        vrow[half] = buf + tt * (DC * 2) + ((chunk ^ (uint32_t)swz((int)tt)) << 4) + (lcol & 1) * 8;
+        for (int d = 0; d < ND; ++d) o[c][d] = T::mfma16(v[d], pw[c & 1], o[c][d]);
       }
-      auto value = [&](int d) {
-        const u32x2 x = lds_read_tr(vrow[0] ^ (d << 5)), y = lds_read_tr(vrow[1] ^ (d << 5));
-        return u32x4{x[0], x[1], y[0], y[1]};
-      };
-      u32x4 v[kAhead];
-#pragma unroll
-      for (int d = 0; d < kAhead - 1 && d < ND; ++d) v[d] = value(d);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        if (d + kAhead - 1 < ND) v[(d + kAhead - 1) % kAhead] = value(d + kAhead - 1);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) o[c][d] = T::mfma16(v[d % kAhead], pw[c], o[c][d]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
-    if (i + 1 < tiles) store(b ^ 1);
   }
 
   // Sums over the lanes and wavefronts that share a head.
@@ -420,14 +506,14 @@ __global__ void __launch_bounds__(latent_waves(HT) * 64, latent_waves(HT) / 4) l
       const float by = total == 0.0f ? 0.0f : by_cache / total;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        *(u32x2*)((uint16_t*)a.out + at * DC + w * (DC / NW) + d * 16 + g * 4) =
+        *(u32x2*)((uint16_t*)a.out + at * DC + d * 128 + w * 16 + g * 4) =
             u32x2{T::pack(o[c][d][0] * by, o[c][d][1] * by), T::pack(o[c][d][2] * by, o[c][d][3] * by)};
       if (w == 0 && lane < 16 && a.lse != nullptr) a.lse[at] = total == 0.0f ? -INFINITY : (m + __log2f(total)) * kLn2;
     } else {
       const int64_t pi = at * p.most + part;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        *(f32x4*)(p.part_out + pi * DC + w * (DC / NW) + d * 16 + g * 4) = o[c][d] * by_cache;
+        *(f32x4*)(p.part_out + pi * DC + d * 128 + w * 16 + g * 4) = o[c][d] * by_cache;
       if (w == 0 && lane < 16) p.part_stat[pi] = float2{m, total};
     }
   }
@@ -438,7 +524,6 @@ namespace {
 template <typename T, bool F8, int DC, bool CHOSEN>
 const void* latent_heads(int heads) {
   switch (heads) {
-    case 16: return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 16>;
     case 32: return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 32>;
     case 64: return (const void*)&latent_kernel<T, F8, DC, CHOSEN, 64>;
     default: return nullptr;
@@ -454,8 +539,6 @@ const void* latent_dims(int head_dim, bool chosen, int heads) {
 }
 
 }  // namespace
-
-int latent_threads(int heads) { return latent_waves(heads) * 64; }
 
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads) {
   if (dtype == PAGED_BF16)

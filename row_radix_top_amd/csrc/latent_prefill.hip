@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[tb][e]);
     }
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_xor32(top);
     if (__builtin_amdgcn_ballot_w64(top > ref + kLazyStep) != 0) {
       const float m = fmaxf(ref, top);
       const float by = m == ref ? 1.0f : exp2_fast(ref - m);

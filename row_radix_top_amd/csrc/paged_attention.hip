@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
       float mt = x[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) mt = fmaxf(mt, x[e]);
-      mt = fmaxf(mt, __shfl_xor(mt, 16));
-      mt = fmaxf(mt, __shfl_xor(mt, 32));
+      mt = max_xor32(max_xor16(mt));
       if (__builtin_amdgcn_ballot_w64(mt > m[t]) != 0) {
         const float mn = fmaxf(m[t], mt);
         const float by = mn == m[t] ? 1.0f : exp2_fast(m[t] - mn);

@@ -138,11 +138,11 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   p.a = *a;
   p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
   p.page = rrt::divisor_of(a->page_size);
+  out->threads = latent ? 512 : 256;
   const bool chosen = a->chosen != nullptr;
   int64_t units = 0;
   if (latent) {
-    const int heads = a->num_heads <= 16 ? 16 : a->num_heads <= 32 ? 32 : 64;
-    out->threads = rrt::latent_threads(heads);
+    const int heads = a->num_heads <= 32 ? 32 : 64;
     p.unit = kLatentUnit;
     p.least = kLatentLeast;
     p.group_rows = 1;
@@ -153,7 +153,6 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   } else {
     p.unit = kUnit;
     p.least = kLeast;
-    out->threads = 256;
     // Rows of a sequence read its cache together unless each has its own
     // chosen positions.
     p.group_rows = chosen ? 1 : a->next_n;

@@ -68,14 +68,15 @@ struct Split {
   int32_t parts, chunk;
 };
 RRT_HD Split split_of(int32_t n, int32_t most, int32_t least, int32_t unit) {
-  int32_t parts = n / least;
-  if (parts > most) parts = most;
+  // 32 bits are enough, and a 64-bit division is a hundred instructions.
+  uint32_t parts = (uint32_t)n / (uint32_t)least;
+  if (parts > (uint32_t)most) parts = (uint32_t)most;
   if (parts < 1) parts = 1;
-  const int64_t per = ((int64_t)n + parts - 1) / parts;
-  int64_t chunk = (per + unit - 1) / unit * unit;
-  if (chunk < unit) chunk = unit;
-  parts = (int32_t)(((int64_t)n + chunk - 1) / chunk);
-  return {parts < 1 ? 1 : parts, (int32_t)chunk};
+  const uint32_t per = ((uint32_t)n + parts - 1) / parts;
+  uint32_t chunk = (per + (uint32_t)unit - 1) / (uint32_t)unit * (uint32_t)unit;
+  if (chunk < (uint32_t)unit) chunk = (uint32_t)unit;
+  parts = ((uint32_t)n + chunk - 1) / chunk;
+  return {parts < 1 ? 1 : (int32_t)parts, (int32_t)chunk};
 }
 
 // ---------------------------------------------------------------------------
@@ -137,7 +138,6 @@ const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads);
 const void* join_kernel_ptr(int dtype, int head_dim, bool many);
 const void* expand_kernel_ptr(int dtype, int store, int latent_dim);
-int latent_threads(int heads);  // of a workgroup
 const void* prefill_kernel_ptr(int dtype);
 int prefill_rows();  // query rows of a workgroup
 
