@@ -35,9 +35,13 @@ __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) { return *(lds_u32x4*)at; }
+// 16 bytes from each lane's address to LDS at `to` (wave uniform) + 16 x lane.
+// No register is written: wait_loads() alone waits for it.
 __device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
-                                   (__attribute__((address_space(3))) uint32_t*)(uintptr_t)to, 16, 0, 0);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(from) : "memory");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -262,7 +266,13 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // use.  S^T and O^T keep a query row in a lane (and the lane 32 further), so
 // the maximum takes one exchange and everything else none.  The reference of
 // the weights moves only when a score passes it by 2^8 (see the absorbed
-// form); keys past a row's end are masked in the tiles that cross it.
+// form).
+//
+// The tiles that all rows see come first, in a loop of their own: what the
+// last few need (keys past a row's end masked, values that are not finite kept
+// from rows that do not see them) costs registers, and the copies and spills
+// that came with it cost the loop a wait for memory on every tile (790 us
+// against 690 for 8192 tokens x 32 heads, causal: 1.0 PFLOP/s).
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;
 constexpr float kLazyStep = 8.0f;
@@ -330,71 +340,79 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     const char* qp = (const char*)a.q + 2 * ((int64_t)(start + (real ? j : row0)) * a.q_row_stride + (int64_t)head * a.q_head_stride);
 #pragma unroll
     for (int s = 0; s < 12; ++s) q[s] = *(const u32x4*)(qp + s * 32 + half * 16);
-  }
-
-  const char* kp = p.keys + ((int64_t)head * p.capacity + tile0) * kKeyTile;
-  const char* rp = p.ropes + (int64_t)tile0 * kRopeTile;
-  const char* vp = p.values + ((int64_t)head * p.capacity + tile0) * kValueTile;
-  auto issue = [&](int32_t i, int b) {
-    // 40 blocks, ten a wavefront: keys, rope parts, values as they lie.
+    // The scale's sign goes into the queries, so that the largest product has
+    // the largest score (and products are 0 where the scale is).
+    const float sign = p.scale_log2 > 0.0f ? 1.0f : p.scale_log2 < 0.0f ? -1.0f : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 10; ++k) {
-      const int blk = k * 4 + w;
-      const char* from = k < 4 ? kp + (int64_t)i * kKeyTile + blk * kBlock16
-                       : k < 6 ? rp + (int64_t)i * kRopeTile + (blk - 16) * kBlock16
-                               : vp + (int64_t)i * kValueTile + (blk - 24) * kBlock16;
-      load_to_lds(from + lane * 16, lds_at(&sm[b][blk * kBlock16]));
-    }
-  };
+    for (int s = 0; s < 12; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[s][e] = T::pack(T::lo(q[s][e]) * sign, T::hi(q[s][e]) * sign);
+  }
+  const float scale = p.scale_log2 != 0.0f ? fabsf(p.scale_log2) : 1.0f;
 
-  float ref = -INFINITY, sum = 0.0f;
+  // 40 blocks of a tile, ten a wavefront: keys, rope parts, values as they lie.
+  const char* kp = p.keys + ((int64_t)head * p.capacity + tile0) * kKeyTile + w * kBlock16;
+  const char* rp = p.ropes + (int64_t)tile0 * kRopeTile + w * kBlock16;
+  const char* vp = p.values + ((int64_t)head * p.capacity + tile0) * kValueTile + w * kBlock16;
+  auto issue = [&](int32_t i, int b) {
+    const uint32_t to = lds_at(&sm[b][0]) + (uint32_t)w * kBlock16, at = (uint32_t)lane * 16;
+    const char* kt = kp + (int64_t)i * kKeyTile;
+    const char* rt = rp + (int64_t)i * kRopeTile;
+    const char* vt = vp + (int64_t)i * kValueTile;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_to_lds(kt + k * 4096, at, to + k * 4096);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) load_to_lds(rt + k * 4096, at, to + kKeyTile + k * 4096);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_to_lds(vt + k * 4096, at, to + kKeyTile + kRopeTile + k * 4096);
+  };
+  // Which of a tile's tokens are in the cache; read through the scalar cache
+  // and a tile ahead, so that no wait for vector memory is among the loads.
+  using scalar_u64 = const __attribute__((address_space(4))) uint64_t;
+  scalar_u64* valid_of = (scalar_u64*)(p.valid + tile0);
+
+  float ref = -INFINITY, sum = 0.0f;  // base-2 logarithm; of this lane's tokens
   f32x16 o[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) o[d] = f32x16{};
-  if (tiles > 0) issue(0, 0);
+  f32x16 s[2];
+  u32x4 pw[4];
 
-  for (int32_t i = 0; i < tiles; ++i) {
-    const int b = i & 1;
-    wait_loads();
-    __syncthreads();
-    if (i + 1 < tiles) issue(i + 1, b ^ 1);
-    const int32_t t0 = i * kCtxTile;
-    if (t0 >= any_see) continue;  // nothing here for this wavefront
-    const uint32_t base = lds_at(&sm[b][0]) + (uint32_t)lane * 16;
+  auto scores = [&](uint32_t base) {
     auto key = [&](int n) {  // n: token block * 12 + step
-      const int tb = n / 12, s = n % 12;
-      return lds_read16(base + (s < 8 ? (tb * 8 + s) * kBlock16 : kKeyTile + (tb * 4 + s - 8) * kBlock16));
+      const int tb = n / 12, k = n % 12;
+      return lds_read16(base + (k < 8 ? (tb * 8 + k) * kBlock16 : kKeyTile + (tb * 4 + k - 8) * kBlock16));
     };
-    f32x16 s[2] = {f32x16{}, f32x16{}};
-    u32x4 kk[kAheadBlocks];
+    u32x4 ring[kAheadBlocks];
 #pragma unroll
-    for (int n = 0; n < kAheadBlocks - 1; ++n) kk[n] = key(n);
+    for (int n = 0; n < kAheadBlocks - 1; ++n) ring[n] = key(n);
+    s[0] = f32x16{}, s[1] = f32x16{};
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < 24; ++n) {
-      if (n + kAheadBlocks - 1 < 24) kk[(n + kAheadBlocks - 1) % kAheadBlocks] = key(n + kAheadBlocks - 1);
-      s[n / 12] = T::mfma32(kk[n % kAheadBlocks], q[n % 12], s[n / 12]);
+      if (n + kAheadBlocks - 1 < 24) ring[(n + kAheadBlocks - 1) % kAheadBlocks] = key(n + kAheadBlocks - 1);
+      s[n / 12] = T::mfma32(ring[n % kAheadBlocks], q[n % 12], s[n / 12]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    const uint64_t valid = p.valid[tile0 + i];
-    const bool masked = t0 + kCtxTile > all_see || valid != ~0ull;
-    float top = -INFINITY;
+  };
+  // Leaves out tokens that are not in the cache or past `left` (of the tile).
+  auto mask = [&](uint64_t valid, int32_t left) {
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb) {
-      s[tb] *= p.scale_log2;
-      if (masked) {
-        const uint32_t bits = (uint32_t)(valid >> (tb * 32)) >> (half * 4);
-        const int32_t left = sees - t0 - tb * 32 - half * 4;
+      const uint32_t bits = (uint32_t)(valid >> (tb * 32)) >> (half * 4);
+      const int32_t rest = left - tb * 32 - half * 4;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = (e >> 2) * 8 + (e & 3);
-          s[tb][e] = t < left && ((bits >> t) & 1u) != 0 ? s[tb][e] : -INFINITY;
-        }
+      for (int e = 0; e < 16; ++e) {
+        const int t = (e >> 2) * 8 + (e & 3);
+        s[tb][e] = t < rest && ((bits >> t) & 1u) != 0 ? s[tb][e] : -INFINITY;
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[tb][e]);
     }
-    top = max_xor32(top);
+  };
+  auto weights = [&] {
+    float top = s[0][0];
+#pragma unroll
+    for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+    top = max_xor32(top) * scale;
     if (__builtin_amdgcn_ballot_w64(top > ref + kLazyStep) != 0) {
       const float m = fmaxf(ref, top);
       const float by = m == ref ? 1.0f : exp2_fast(ref - m);
@@ -403,54 +421,92 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= by;
     }
-    const float r = ref == -INFINITY ? 0.0f : ref;
-    u32x4 pw[4];
+    const float r = ref == -INFINITY ? 0.0f : -ref;
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_fast(s[k >> 1][(k & 1) * 8 + e] - r);
-        sum += x[e];
+        x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], scale, r));
+        part[e & 3] += x[e];
       }
       pw[k] = u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
     }
-    const uint32_t vbase = base + kKeyTile + kRopeTile;
-    if (masked && p.flags[(int64_t)head * p.capacity + tile0 + i] != 0) {
-      // Values that are not finite in a tile that not every row sees whole: one
-      // token at a time, into the rows that see it.
-      for (int32_t t = 0; t < kCtxTile; ++t) {
-        const int k = t >> 4, in = t & 15;  // block of 16 tokens; the token's half and element there
-        const bool mine = half == ((in >> 2) & 1);
-        const int e = (in >> 3) * 4 + (in & 3);
-        u32x4 keep = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (mine && (e >> 1) == c) keep[c] = (e & 1) ? 0xffff0000u : 0x0000ffffu;
-        u32x4 weight = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) weight = k == c ? pw[c] : weight;
-        weight &= keep;
-        const bool here = t0 + t < sees && ((valid >> t) & 1u) != 0;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const f32x16 x = T::mfma32(lds_read16(vbase + (k * 4 + d) * kBlock16) & keep, weight, o[d]);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) o[d][c] = here ? x[c] : o[d][c];
-        }
-      }
-      continue;
-    }
-    u32x4 v[kAheadBlocks];
+    sum += (part[0] + part[1]) + (part[2] + part[3]);
+  };
+  auto values = [&](uint32_t vbase) {
     auto value = [&](int n) { return lds_read16(vbase + n * kBlock16); };
+    u32x4 ring[kAheadBlocks];
 #pragma unroll
-    for (int n = 0; n < kAheadBlocks - 1; ++n) v[n] = value(n);
+    for (int n = 0; n < kAheadBlocks - 1; ++n) ring[n] = value(n);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
-      if (n + kAheadBlocks - 1 < 16) v[(n + kAheadBlocks - 1) % kAheadBlocks] = value(n + kAheadBlocks - 1);
-      o[n & 3] = T::mfma32(v[n % kAheadBlocks], pw[n >> 2], o[n & 3]);
+      if (n + kAheadBlocks - 1 < 16) ring[(n + kAheadBlocks - 1) % kAheadBlocks] = value(n + kAheadBlocks - 1);
+      o[n & 3] = T::mfma32(ring[n % kAheadBlocks], pw[n >> 2], o[n & 3]);
       __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // Tiles that every row of the workgroup sees whole.
+  const int32_t first_sees = ctx - count + row0 + 1;
+  const int32_t whole = first_sees > 0 && fits ? first_sees / kCtxTile : 0;
+  uint64_t valid = 0;
+  if (tiles > 0) {
+    issue(0, 0);
+    valid = valid_of[0];
+  }
+  for (int32_t i = 0; i < whole; ++i) {
+    wait_loads();
+    __syncthreads();
+    if (i + 1 < tiles) issue(i + 1, (i + 1) & 1);
+    const uint64_t now = valid;
+    if (i + 1 < tiles) valid = valid_of[i + 1];
+    const uint32_t base = lds_at(&sm[i & 1][0]) + (uint32_t)lane * 16;
+    scores(base);
+    if (now != ~0ull) mask(now, kCtxTile);
+    weights();
+    values(base + kKeyTile + kRopeTile);
+  }
+  // Tiles that some row sees in part or not at all.
+  for (int32_t i = whole; i < tiles; ++i) {
+    wait_loads();
+    __syncthreads();
+    if (i + 1 < tiles) issue(i + 1, (i + 1) & 1);
+    const uint64_t now = valid;
+    if (i + 1 < tiles) valid = valid_of[i + 1];
+    const int32_t t0 = i * kCtxTile;
+    if (t0 >= any_see) continue;  // nothing here for this wavefront
+    const uint32_t base = lds_at(&sm[i & 1][0]) + (uint32_t)lane * 16, vbase = base + kKeyTile + kRopeTile;
+    scores(base);
+    mask(now, sees - t0);
+    weights();
+    if (p.flags[(int64_t)head * p.capacity + tile0 + i] == 0) {
+      values(vbase);
+      continue;
+    }
+    // Values that are not finite: one token at a time, into the rows that see
+    // it.
+    for (int32_t t = 0; t < kCtxTile; ++t) {
+      const int k = t >> 4, in = t & 15;  // block of 16 tokens; the token's half and element there
+      const bool mine = half == ((in >> 2) & 1);
+      const int e = (in >> 3) * 4 + (in & 3);
+      u32x4 keep = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (mine && (e >> 1) == c) keep[c] = (e & 1) ? 0xffff0000u : 0x0000ffffu;
+      u32x4 weight = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) weight = k == c ? pw[c] : weight;
+      weight &= keep;
+      const bool here = t0 + t < sees && ((now >> t) & 1u) != 0;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const f32x16 x = T::mfma32(lds_read16(vbase + (k * 4 + d) * kBlock16) & keep, weight, o[d]);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) o[d][c] = here ? x[c] : o[d][c];
+      }
     }
   }
 
