@@ -287,8 +287,8 @@ int paged_layout(const int32_t* lengths, const int32_t* new_tokens, int32_t num_
     REQUIRE(aligned(p, 4), "all arrays must be 4-byte aligned");
   rrt::LayoutParams p{lengths, new_tokens, free_pages, block_table, starts, slots, row_lengths, row_seqs, pages,
                       table_stride, num_seqs, num_free, table_width, page_size, capacity};
-  const int64_t grid = std::min<int64_t>(std::max<int64_t>(1, ceil_div(capacity, 256)), 512);
-  return launch(rrt::layout_kernel_ptr(), grid, 256, &p, stream, "paged_layout");
+  const int64_t grid = std::min<int64_t>(std::max<int64_t>(1, ceil_div(capacity, rrt::kLayoutBlock)), 512);
+  return launch(rrt::layout_kernel_ptr(), grid, rrt::kLayoutBlock, &p, stream, "paged_layout");
 }
 
 int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* parts, int32_t num_parts,
@@ -325,8 +325,8 @@ int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* par
   p.page_size = page_size;
   p.num_slots = (int64_t)num_pages * page_size;
   const int64_t items = (int64_t)num_tokens * (p.chunks[0] + p.chunks[1]);
-  const int64_t grid = std::min<int64_t>(ceil_div(items, 256), 1 << 16);
-  return launch(rrt::append_kernel_ptr(dtype, store, wide), grid, 256, &p, stream, "paged_append");
+  const int64_t grid = std::min<int64_t>(ceil_div(items, rrt::kAppendBlock), 1 << 16);
+  return launch(rrt::append_kernel_ptr(dtype, store, wide), grid, rrt::kAppendBlock, &p, stream, "paged_append");
 }
 
 int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes) {

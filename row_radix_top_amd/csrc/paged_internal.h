@@ -83,6 +83,9 @@ RRT_HD Split split_of(int32_t n, int32_t most, int32_t least, int32_t unit) {
 // Kernel parameters
 // ---------------------------------------------------------------------------
 
+constexpr int kLayoutBlock = 1024;  // threads of a workgroup of paged_layout
+constexpr int kAppendBlock = 256;   // and of paged_append
+
 struct LayoutParams {
   const int32_t* lengths;
   const int32_t* new_tokens;

@@ -63,6 +63,42 @@ def test_layout_random(n, page_size):
     _layout_case(lengths, new, page_size, width, seed=n)
 
 
+@pytest.mark.parametrize("n", [1023, 2048, 2049, 5000])
+def test_layout_of_many_sequences(n):
+    rng = np.random.default_rng(n)
+    _layout_case(rng.integers(0, 81, size=n), rng.integers(0, 4, size=n), 16, 5, seed=n)
+    _layout_case(rng.integers(0, 81, size=n), np.where(rng.random(n) < 0.01, 80, 0), 16, 5, seed=n)
+
+
+def test_layout_of_more_tokens_than_32_bits_count():
+    """The sum of the lengths stops at 2^31 - 1; the tokens before that are laid out."""
+    import torch
+    n, page, width, capacity = 5, 1 << 20, 1024, 40
+    new = _dev([7] + [1 << 30] * (n - 1), torch.int32)
+    table = torch.full((n, width), -7, dtype=torch.int32, device="cuda")
+    out = rrt.paged_layout(torch.full((n,), 1 << 30, dtype=torch.int32, device="cuda"), new,
+                           _dev(np.arange(100, 600, dtype=np.int32)), table, page_size=page, capacity=capacity)
+    first = (1 << 30) - 7
+    assert out.row_lengths.tolist() == list(range(first + 1, first + 8)) + list(range(1, capacity - 6))
+    assert out.row_seqs.tolist() == [0] * 7 + [1] * (capacity - 7)
+    assert out.slots.tolist() == [-1] * 7 + [100 * page + i for i in range(capacity - 7)]
+    assert out.starts.tolist() == [0, 7, 7 + (1 << 30), (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1]
+    assert int(out.pages) == 4 * width
+    taken = torch.arange(4 * width, dtype=torch.int32, device="cuda") + 100
+    assert bool((table[0] == -7).all())
+    assert torch.equal(table[1:].reshape(-1), torch.where(taken < 600, taken, -1))
+
+
+def test_layout_of_a_page_past_the_slots():
+    """A page whose slots do not fit 32 bits has none."""
+    import torch
+    table = _dev([[1 << 20, 5], [(1 << 31) // 3000, 5]], torch.int32)
+    out = rrt.paged_layout(_dev([8, 8], torch.int32), _dev([1, 1], torch.int32), _dev(np.zeros(0, np.int32)),
+                           table, page_size=3000, capacity=2)
+    last = (1 << 31) // 3000 * 3000 + 7
+    assert out.slots.tolist() == [-1, last if last < 1 << 31 else -1]
+
+
 def test_layout_decode_and_prefill_extremes():
     _layout_case([0, 0, 0], [0, 0, 0], 16, 4)
     _layout_case([0], [5], 16, 4)  # no more new tokens than tokens
