@@ -155,7 +155,7 @@ typedef struct {
   int32_t head_dim;          /* latent: the latent vector without its rope part */
   int32_t page_size, num_pages, table_width;
   int32_t num_chosen;
-  float softmax_scale;
+  float softmax_scale;       /* its product with log2(e) finite */
   paged_dtype dtype, store;
   int32_t max_splits;        /* 0: the library's rule; else at most this many parts a row (1 to 128) */
 } paged_attention_args;
@@ -211,7 +211,7 @@ typedef struct {
   int32_t num_tokens, num_seqs, num_heads;
   int32_t latent_dim;        /* 256 or 512 */
   int32_t page_size, num_pages, table_width;
-  float softmax_scale;
+  float softmax_scale;       /* its product with log2(e) finite */
   paged_dtype dtype, store;
 } latent_prefill_args;
 

@@ -55,6 +55,8 @@ int check_types(paged_dtype dtype, paged_dtype store) {
 // Attention
 // ---------------------------------------------------------------------------
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // A part's fewest positions and the unit its length is rounded to: four
 // wavefronts take 32 tokens each.
 constexpr int32_t kUnit = 128;
@@ -95,7 +97,7 @@ int check_attention(const paged_attention_args* a, bool latent) {
   REQUIRE(a->max_splits >= 0 && a->max_splits <= kMostParts, "max_splits must be in [0, 128]");
   REQUIRE(a->chosen == nullptr || (a->num_chosen >= 1 && a->num_chosen <= rrt::kMostTokens),
           "num_chosen must be in [1, 2^30]");
-  REQUIRE(std::isfinite(a->softmax_scale), "softmax_scale must be finite");
+  REQUIRE(std::isfinite(a->softmax_scale * kLog2e), "softmax_scale times log2(e) must be finite");
   if (a->num_rows == 0) return TOPK_OK;
   REQUIRE(a->num_pages >= 1, "num_pages must be >= 1");
   REQUIRE((int64_t)a->num_rows * a->num_heads <= INT32_MAX, "num_rows * num_heads must be below 2^31");
@@ -136,7 +138,7 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
   rrt::AttnParams& p = out->p;
   p.a = *a;
-  p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
+  p.scale_log2 = a->softmax_scale * kLog2e;
   p.page = rrt::divisor_of(a->page_size);
   out->threads = latent ? 512 : 256;
   const bool chosen = a->chosen != nullptr;
@@ -210,7 +212,7 @@ int check_prefill(const latent_prefill_args* a) {
   REQUIRE(a->page_size >= 1, "page_size must be >= 1");
   REQUIRE(a->table_width >= 1, "table_width must be >= 1");
   REQUIRE(a->context_tokens >= 0 && a->context_tokens <= rrt::kMostTokens, "context_tokens must be in [0, 2^30]");
-  REQUIRE(std::isfinite(a->softmax_scale), "softmax_scale must be finite");
+  REQUIRE(std::isfinite(a->softmax_scale * kLog2e), "softmax_scale times log2(e) must be finite");
   if (a->num_tokens == 0 || a->num_seqs == 0) return TOPK_OK;
   REQUIRE(a->num_pages >= 1, "num_pages must be >= 1");
   REQUIRE(a->q != nullptr && a->cache != nullptr && a->w_k != nullptr && a->w_v != nullptr &&
@@ -244,7 +246,7 @@ int plan_prefill(const latent_prefill_args* a, PrefillPlan* out) {
   if (a->num_tokens == 0 || a->num_seqs == 0) return TOPK_OK;
   rrt::PrefillParams& p = out->p;
   p.a = *a;
-  p.scale_log2 = a->softmax_scale * 1.44269504088896340736f;
+  p.scale_log2 = a->softmax_scale * kLog2e;
   // Each sequence rounds up to whole tiles.
   const int64_t capacity = a->context_tokens / rrt::kCtxTile + a->num_seqs;
   const int64_t row_tiles = a->num_tokens / rrt::prefill_rows() + a->num_seqs;

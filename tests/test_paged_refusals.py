@@ -63,7 +63,7 @@ ATTENTION = [
     (dict(head_dim=96), "head_dim"), (dict(page_size=0), "page_size"), (dict(table_width=0), "table_width"),
     (dict(max_splits=129), "max_splits"), (dict(max_splits=-1), "max_splits"), (dict(chosen=256), "num_chosen"),
     (dict(chosen=256, num_chosen=(1 << 30) + 1), "num_chosen"),
-    (dict(softmax_scale=float("nan")), "softmax_scale"), (dict(softmax_scale=float("inf")), "softmax_scale"),
+    (dict(softmax_scale=float("nan")), "softmax_scale"), (dict(softmax_scale=float("inf")), "softmax_scale"), (dict(softmax_scale=3e38), "softmax_scale"),
     (dict(num_pages=0), "num_pages"), (dict(q=None), "null"), (dict(k=None), "null"), (dict(lengths=None), "null"),
     (dict(block_table=None), "null"), (dict(out=None), "null"), (dict(q=264), "16 bytes"),
     (dict(q_row_stride=1028), "16 bytes"), (dict(k=520), "16 bytes"), (dict(token_stride=129), "16 bytes"),
