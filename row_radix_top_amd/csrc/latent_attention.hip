@@ -138,9 +138,10 @@ __global__ void __launch_bounds__(kLatentBlock, 2) latent_kernel(AttnParams p) {
   const int wh = w % S::WH, wt = w / S::WH;
 
   Work work;
-  if (!work_of(blockIdx.x, (uint32_t)p.col_tiles, (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
-  const int32_t part = work.part, row = work.group, head0 = work.unit * HT;
+  if (!work_of<CHOSEN>(blockIdx.x, (uint32_t)p.col_tiles, (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
   const int64_t most = table_tokens(a.table_width, a.page_size);
+  const int32_t part = work.part, head0 = work.unit * HT;
+  const int32_t row = CHOSEN ? work.group : by_length(a, work.group, p.groups, 1, most, lane);
   const int32_t seen = clamp_to(a.lengths[row], most);
   const int32_t n = CHOSEN ? a.num_chosen : seen;
   const Split sp = split_of(n, p.most, p.least, p.unit);

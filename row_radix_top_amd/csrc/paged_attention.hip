@@ -113,12 +113,13 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 
   Work work;
-  if (!work_of(blockIdx.x, (uint32_t)(a.num_kv_heads * p.col_tiles), (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
-  const int32_t part = work.part, group = work.group;
+  if (!work_of<CHOSEN>(blockIdx.x, (uint32_t)(a.num_kv_heads * p.col_tiles), (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
+  const int64_t most = table_tokens(a.table_width, a.page_size);
+  const int32_t part = work.part;
+  const int32_t group = CHOSEN ? work.group : by_length(a, work.group, p.groups, p.group_rows, most, lane);
   const int32_t kvh = work.unit % a.num_kv_heads, tile = work.unit / a.num_kv_heads;
   const int32_t r0 = group * p.group_rows;
   const int32_t heads_per = a.num_heads / a.num_kv_heads;
-  const int64_t most = table_tokens(a.table_width, a.page_size);
 
   const int32_t n = CHOSEN ? a.num_chosen : group_length(p, r0, most, lane);
   const Split sp = split_of(n, p.most, p.least, p.unit);

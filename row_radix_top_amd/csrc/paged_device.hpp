@@ -151,16 +151,46 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // of a (group, part) are given to one XCD, one after the other.  They read
 // neighbouring bytes of the same tokens: with head h of every token on XCD
 // h % 8 each XCD's L2 would see one 256-byte column of the cache, a fraction
-// of its channels.  False past the last one.
+// of its channels.
+// Rows of chosen positions are alike: a group's parts go to one XCD, whose L2
+// then holds its table once (64 rows of 2048 of 65536 positions: 70 us against
+// 72).  Others: side by side, as a sequence on one XCD alone would leave the
+// XCDs with unequal shares, and every other eight in the reverse order, so that
+// none gets the longer of each two.  False past the last one.
 struct Work {
   int32_t group, part, unit;
 };
+template <bool CHOSEN>
 __device__ __forceinline__ bool work_of(uint32_t block, uint32_t inner, uint32_t groups, uint32_t most, Work* w) {
-  const uint32_t idx = block >> 3, outer = idx / inner * 8 + (block & 7);
+  const uint32_t idx = block >> 3, eight = idx / inner;
   w->unit = (int32_t)(idx % inner);
-  w->part = (int32_t)(outer / groups);
-  w->group = (int32_t)(outer - (uint32_t)w->part * groups);
-  return w->part < (int32_t)most;
+  if constexpr (CHOSEN) {
+    const uint32_t outer = eight * 8 + (block & 7);
+    w->part = (int32_t)(outer / groups);
+    w->group = (int32_t)(outer - (uint32_t)w->part * groups);
+    return w->part < (int32_t)most;
+  }
+  const uint32_t outer = eight * 8 + ((block & 7) ^ (eight & 1 ? 7u : 0u));
+  w->group = (int32_t)(outer / most);
+  w->part = (int32_t)(outer - (uint32_t)w->group * most);
+  return w->group < (int32_t)groups;
+}
+// Groups longest first, within each 64 of them: the group that stands at place
+// `at`.  What starts last ends the launch and is better short: 64 rows of 1 to
+// 32768 positions x 8 heads took 880 us in their own order with a sequence's
+// parts on one XCD, 755 so.  Wave uniform; every wavefront finds the same.
+__device__ __forceinline__ int32_t by_length(const paged_attention_args& a, int32_t at, int32_t groups, int32_t group_rows,
+                                             int64_t most, int lane) {
+  const int32_t base = at & ~63, count = groups - base < 64 ? groups - base : 64;
+  const bool here = lane < count;
+  const int32_t len = here ? clamp_to(a.lengths[(int64_t)(base + lane) * group_rows + group_rows - 1], most) : -1;
+  if (__builtin_amdgcn_ballot_w64(here && len != __builtin_amdgcn_readfirstlane(len)) == 0) return at;
+  int32_t before = 0;
+  for (int32_t j = 0; j < count; ++j) {
+    const int32_t other = __builtin_amdgcn_readlane(len, j);
+    before += other > len || (other == len && j < lane) ? 1 : 0;
+  }
+  return base + (int32_t)__builtin_ctzll(__builtin_amdgcn_ballot_w64(here && before == at - base));
 }
 
 constexpr float kLn2 = 0.69314718055994530942f;

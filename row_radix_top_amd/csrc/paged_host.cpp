@@ -68,10 +68,12 @@ constexpr int32_t kLatentLeast = 128;
 
 // How many parts the longest row gets, at most; units: workgroups of an
 // unsplit launch.  Times in us for 1, 2, 4, 8 and 16 parts at 256 CUs:
-//   4 x 8 units of 8192 positions        97   57   36   28   29
-//   8 units of 32768                    368  191  102   57   35 (64: 30)
-//   64 x 8 ragged, 1 to 32768           968  877  878  845  856
-//   256 x 8 ragged, 500 to 4096         490  476  480  517  540
+//   4 x 8 units of 8192 positions        83   49   31   29   29
+//   8 units of 32768                    311  164   88   49   31 (32: 30)
+//   16 x 8 ragged, 4000 to 16384        225  152  152  142  144
+//   64 x 8 ragged, 1 to 32768           895  800  755  752  767
+//   64 x 8 of 16384                     801  814  801  782  778
+//   256 x 8 ragged, 500 to 4096         482  479  489  522  607
 //   64 x 4 of 2048 chosen                31   33   35   38   38
 // So: two workgroups a CU; four parts at least where rows may differ in length
 // (the longest one ends the launch), one a CU is enough where all are alike.
