@@ -21,12 +21,25 @@ namespace rrt {
 //     next without leaving the lane.
 // The expanded keys and values are rounded to the 16-bit type, as a program
 // that keeps them would; that is the operator's own rounding beside those of
-// the weights and the output.
+// the weights and the output.  A row that sees n tokens averages their keys'
+// roundings away: what is left in its log-sum-exp falls as 1 / sqrt(n), from
+// 1e-3 of it at one token to 4e-6 at 2048 (bf16).  The keys of a sequence's
+// first kExactTiles tiles therefore come with what their rounding left, as a
+// second 16-bit number, and score with both (twice the bits, for rows of few
+// tokens all that they see).  The weights of the first kExactWeights tiles are
+// taken in two parts too: an output of few tokens is off by 1.35 times its own
+// rounding so, 1.55 times without.
+// 8192 tokens x 32 heads: 630 us without second parts, 690 with 16 tiles, 870
+// with the keys' of all tiles.
+//
+// A scale of the cache reaches the keys as its power of two alone, which moves
+// no bit of a rope part; the rest of it multiplies the scores.
 // ---------------------------------------------------------------------------
 constexpr int kExpandBlock = 256;
 constexpr int kHead = PAGED_HEAD_DIM;
 constexpr int kRopeDim = PAGED_ROPE_DIM;
 constexpr int kBlock16 = 1024;                              // bytes of a block
+constexpr int kExactTiles = 16, kExactWeights = 4;          // 1024 and 256 tokens
 constexpr int kKeyTile = 16 * kBlock16, kRopeTile = 8 * kBlock16, kValueTile = 16 * kBlock16;
 
 using lds_u32x4 = __attribute__((address_space(3))) u32x4;
@@ -44,6 +57,16 @@ __device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, u
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(from) : "memory");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A cache's scale as a signed power of two and a factor in [1, 2).
+struct KeyScale {
+  float power, rest;
+};
+__device__ __forceinline__ KeyScale key_scale(const float* scale) {
+  const uint32_t x = scale == nullptr ? 0x3f800000u : __float_as_uint(scale[0]), e = x >> 23 & 255;
+  if (e == 0 || e == 255) return {__uint_as_float(x), 1.0f};  // zero, subnormal or not finite
+  return {__uint_as_float(x & 0xff800000u), __uint_as_float((x & 0x007fffffu) | 0x3f800000u)};
+}
 
 __device__ __forceinline__ int32_t context_of(const PrefillParams& p, int32_t s) {
   return clamp_to(p.a.lengths[s], table_tokens(p.a.table_width, p.a.page_size));
@@ -84,7 +107,9 @@ __device__ __forceinline__ int32_t sequence_of_tile(const PrefillParams& p, int3
 // all value dims for a tile, so that keys come out with consecutive dims in a
 // lane and values with consecutive tokens, as their fragments want them.
 // Latent vectors and weights pass through LDS in slices of 32 of the summed
-// dims, two slices deep (48 KB: two workgroups a CU hide each other's waits),
+// dims, two slices deep (48 KB: two workgroups a CU hide each other's waits;
+// 8192 tokens x 32 heads take 95 to 110 us, 0.7 PFLOP/s, and a third slice or
+// several heads a workgroup no less),
 // 16-byte chunks at c ^ (row / 4 % 4): a read's 16 rows then meet every bank
 // once.
 // ---------------------------------------------------------------------------
@@ -97,6 +122,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
   constexpr int PITCH = SL * 2;      // bytes of a slice's row
   __shared__ __align__(1024) char sm[2][ROWS * PITCH];  // tokens, key weights, value weights
   __shared__ int64_t splace[TOK];
+  __shared__ bool sexact[2];
   const latent_prefill_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -105,10 +131,12 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 
   // Places of the tokens: wavefronts 0 and 1 find a tile's each.
   if (w < 2) {
+    bool exact = false;
     int64_t off = -1;
     int32_t before = 0;
     const int32_t tile = tile0 + w;
     const int32_t s = tile < p.capacity ? sequence_of_tile(p, tile, lane, &before) : -1;
+    exact = s >= 0 && tile - before < kExactTiles;
     if (s >= 0) {
       const int32_t pos = (tile - before) * kCtxTile + lane;
       if (pos < context_of(p, s))
@@ -118,6 +146,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
       if (head == 0 && lane == 0) p.valid[tile] = bits;
     }
     splace[w * 64 + lane] = s < 0 ? -2 : off;
+    if (lane == 0) sexact[w] = exact;
   }
   __syncthreads();
   const bool real[2] = {splace[0] != -2, splace[64] != -2};
@@ -201,18 +230,29 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
   }
 
   const float by = F8 && a.scale != nullptr ? a.scale[0] : 1.0f;
+  const float key_by = F8 ? key_scale(a.scale).power : 1.0f;
   if (keys) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 32 tokens
       if (!real[j >> 1]) continue;
-      char* to = p.keys + ((int64_t)head * p.capacity + tile0 + (j >> 1)) * kKeyTile + (lane & 31) * 16 + half * 8;
+      const int64_t at = ((int64_t)head * p.capacity + tile0 + (j >> 1)) * kKeyTile + (lane & 31) * 16 + half * 8;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // dims w*64 + i*32 + e*8 + half*4 .. +4 of the lane's token
-          const f32x16& x = acc[i][j];
-          *(u32x2*)(to + ((j & 1) * 8 + w * 4 + i * 2 + (e >> 1)) * kBlock16 + (e & 1) * 512) =
-              u32x2{T::pack(x[e * 4] * by, x[e * 4 + 1] * by), T::pack(x[e * 4 + 2] * by, x[e * 4 + 3] * by)};
+          float x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = acc[i][j][e * 4 + c] * key_by;
+          const u32x2 high = {T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+          const int64_t to = at + ((j & 1) * 8 + w * 4 + i * 2 + (e >> 1)) * kBlock16 + (e & 1) * 512;
+          *(u32x2*)(p.keys + to) = high;
+          if (!sexact[j >> 1]) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // what the rounding left; nothing of what left the type's range
+            const float h = c & 1 ? T::hi(high[c >> 1]) : T::lo(high[c >> 1]);
+            x[c] = fabsf(h) <= T::kLargest ? x[c] - h : 0.0f;
+          }
+          *(u32x2*)(p.lows + to) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
         }
     }
   } else if (real[w & 1]) {
@@ -250,7 +290,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
         if constexpr (F8) {
           x = widen<T>(*(const u32x2*)(from + s * 16 + half * 8));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = T::pack(T::lo(x[i]) * by, T::hi(x[i]) * by);
+          for (int i = 0; i < 4; ++i) x[i] = T::pack(T::lo(x[i]) * key_by, T::hi(x[i]) * key_by);
         } else {
           x = *(const u32x4*)(from + s * 32 + half * 16);
         }
@@ -262,8 +302,10 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 
 // ---------------------------------------------------------------------------
 // Attention of 128 query rows of one head a workgroup, 32 a wavefront, over
-// the context's tiles in order; two tiles in LDS, one being loaded and one in
-// use.  S^T and O^T keep a query row in a lane (and the lane 32 further), so
+// the context's tiles in order.  Values lie in LDS twice, being loaded and in
+// use; keys once (72 KB with their second parts, so that two workgroups fit a
+// CU): the next tile's come under the softmax and the product with the values,
+// which measures as two buffers do.  S^T and O^T keep a query row in a lane (and the lane 32 further), so
 // the maximum takes one exchange and everything else none.  The reference of
 // the weights moves only when a score passes it by 2^8 (see the absorbed
 // form).
@@ -272,7 +314,13 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // last few need (keys past a row's end masked, values that are not finite kept
 // from rows that do not see them) costs registers, and the copies and spills
 // that came with it cost the loop a wait for memory on every tile (790 us
-// against 690 for 8192 tokens x 32 heads, causal: 1.0 PFLOP/s).
+// against 630 for 8192 tokens x 32 heads).
+//
+// Those 630 us are 1.09 PFLOP/s.  The matrix units are busy 61 % of the time at
+// the 1.7 GHz that the power limit leaves under this load; every fragment that
+// LDS gives feeds one matrix instruction, so its reads take as long as those.
+// Longer rings of reads, both token blocks' chains in turn and wave priorities
+// changed nothing.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;
 constexpr float kLazyStep = 8.0f;
@@ -280,8 +328,9 @@ constexpr int kAheadBlocks = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
-  constexpr int TILE = kKeyTile + kRopeTile + kValueTile;  // 40 KB
-  __shared__ __align__(1024) char sm[2][TILE];
+  // Keys, rope parts and what the keys' rounding left: one tile; values: two.
+  __shared__ __align__(1024) char sk[kKeyTile + kRopeTile + kKeyTile];
+  __shared__ __align__(1024) char sv[2][kValueTile];
   const latent_prefill_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -348,23 +397,31 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) q[s][e] = T::pack(T::lo(q[s][e]) * sign, T::hi(q[s][e]) * sign);
   }
-  const float scale = p.scale_log2 != 0.0f ? fabsf(p.scale_log2) : 1.0f;
+  const float scale = p.scale_log2 != 0.0f ? fabsf(p.scale_log2) * key_scale(a.scale).rest : 1.0f;
 
-  // 40 blocks of a tile, ten a wavefront: keys, rope parts, values as they lie.
-  const char* kp = p.keys + ((int64_t)head * p.capacity + tile0) * kKeyTile + w * kBlock16;
+  // 16 blocks of keys, 8 of rope parts, 16 of values, and 16 of what the keys'
+  // rounding left, a quarter of each a wavefront, as they lie.
+  const int64_t key_at = ((int64_t)head * p.capacity + tile0) * kKeyTile + w * kBlock16;
+  const char* kp = p.keys + key_at;
+  const char* lp = p.lows + key_at;
   const char* rp = p.ropes + (int64_t)tile0 * kRopeTile + w * kBlock16;
   const char* vp = p.values + ((int64_t)head * p.capacity + tile0) * kValueTile + w * kBlock16;
-  auto issue = [&](int32_t i, int b) {
-    const uint32_t to = lds_at(&sm[b][0]) + (uint32_t)w * kBlock16, at = (uint32_t)lane * 16;
-    const char* kt = kp + (int64_t)i * kKeyTile;
-    const char* rt = rp + (int64_t)i * kRopeTile;
-    const char* vt = vp + (int64_t)i * kValueTile;
+  const uint32_t lane16 = (uint32_t)lane * 16;
+  auto issue_keys = [&](int32_t i) {
+    const uint32_t to = lds_at(&sk[0]) + (uint32_t)w * kBlock16;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) load_to_lds(kt + k * 4096, at, to + k * 4096);
+    for (int k = 0; k < 4; ++k) load_to_lds(kp + (int64_t)i * kKeyTile + k * 4096, lane16, to + k * 4096);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) load_to_lds(rt + k * 4096, at, to + kKeyTile + k * 4096);
+    for (int k = 0; k < 2; ++k) load_to_lds(rp + (int64_t)i * kRopeTile + k * 4096, lane16, to + kKeyTile + k * 4096);
+    if (i < kExactTiles)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) load_to_lds(vt + k * 4096, at, to + kKeyTile + kRopeTile + k * 4096);
+      for (int k = 0; k < 4; ++k)
+        load_to_lds(lp + (int64_t)i * kKeyTile + k * 4096, lane16, to + kKeyTile + kRopeTile + k * 4096);
+  };
+  auto issue_values = [&](int32_t i) {
+    const uint32_t to = lds_at(&sv[i & 1][0]) + (uint32_t)w * kBlock16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_to_lds(vp + (int64_t)i * kValueTile + k * 4096, lane16, to + k * 4096);
   };
   // Which of a tile's tokens are in the cache; read through the scalar cache
   // and a tile ahead, so that no wait for vector memory is among the loads.
@@ -378,7 +435,8 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   f32x16 s[2];
   u32x4 pw[4];
 
-  auto scores = [&](uint32_t base) {
+  auto scores = [&](bool exact) {
+    const uint32_t base = lds_at(&sk[0]) + lane16;
     auto key = [&](int n) {  // n: token block * 12 + step
       const int tb = n / 12, k = n % 12;
       return lds_read16(base + (k < 8 ? (tb * 8 + k) * kBlock16 : kKeyTile + (tb * 4 + k - 8) * kBlock16));
@@ -392,6 +450,17 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     for (int n = 0; n < 24; ++n) {
       if (n + kAheadBlocks - 1 < 24) ring[(n + kAheadBlocks - 1) % kAheadBlocks] = key(n + kAheadBlocks - 1);
       s[n / 12] = T::mfma32(ring[n % kAheadBlocks], q[n % 12], s[n / 12]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!exact) return;
+    auto low = [&](int n) { return lds_read16(base + kKeyTile + kRopeTile + n * kBlock16); };
+#pragma unroll
+    for (int n = 0; n < kAheadBlocks - 1; ++n) ring[n] = low(n);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      if (n + kAheadBlocks - 1 < 16) ring[(n + kAheadBlocks - 1) % kAheadBlocks] = low(n + kAheadBlocks - 1);
+      s[n / 8] = T::mfma32(ring[n % kAheadBlocks], q[n % 8], s[n / 8]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -429,13 +498,14 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], scale, r));
+        s[k >> 1][(k & 1) * 8 + e] = x[e];
         part[e & 3] += x[e];
       }
       pw[k] = u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
     }
     sum += (part[0] + part[1]) + (part[2] + part[3]);
   };
-  auto values = [&](uint32_t vbase) {
+  auto values = [&](uint32_t vbase, bool exact) {
     auto value = [&](int n) { return lds_read16(vbase + n * kBlock16); };
     u32x4 ring[kAheadBlocks];
 #pragma unroll
@@ -447,6 +517,19 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
       o[n & 3] = T::mfma32(ring[n % kAheadBlocks], pw[n >> 2], o[n & 3]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    if (!exact) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      u32x4 left;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int e = (k & 1) * 8 + c * 2;
+        left[c] = T::pack(s[k >> 1][e] - T::lo(pw[k][c]), s[k >> 1][e + 1] - T::hi(pw[k][c]));
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] = T::mfma32(value(k * 4 + d), left, o[d]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
   // Tiles that every row of the workgroup sees whole.
@@ -454,36 +537,41 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   const int32_t whole = first_sees > 0 && fits ? first_sees / kCtxTile : 0;
   uint64_t valid = 0;
   if (tiles > 0) {
-    issue(0, 0);
+    issue_keys(0);
+    issue_values(0);
     valid = valid_of[0];
   }
   for (int32_t i = 0; i < whole; ++i) {
     wait_loads();
     __syncthreads();
-    if (i + 1 < tiles) issue(i + 1, (i + 1) & 1);
+    if (i + 1 < tiles) issue_values(i + 1);
     const uint64_t now = valid;
     if (i + 1 < tiles) valid = valid_of[i + 1];
-    const uint32_t base = lds_at(&sm[i & 1][0]) + (uint32_t)lane * 16;
-    scores(base);
+    scores(i < kExactTiles);
+    __syncthreads();  // the keys are read
+    if (i + 1 < tiles) issue_keys(i + 1);
     if (now != ~0ull) mask(now, kCtxTile);
     weights();
-    values(base + kKeyTile + kRopeTile);
+    values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights);
   }
   // Tiles that some row sees in part or not at all.
   for (int32_t i = whole; i < tiles; ++i) {
     wait_loads();
     __syncthreads();
-    if (i + 1 < tiles) issue(i + 1, (i + 1) & 1);
+    if (i + 1 < tiles) issue_values(i + 1);
     const uint64_t now = valid;
     if (i + 1 < tiles) valid = valid_of[i + 1];
     const int32_t t0 = i * kCtxTile;
-    if (t0 >= any_see) continue;  // nothing here for this wavefront
-    const uint32_t base = lds_at(&sm[i & 1][0]) + (uint32_t)lane * 16, vbase = base + kKeyTile + kRopeTile;
-    scores(base);
+    const bool any = t0 < any_see;  // else nothing here for this wavefront
+    if (any) scores(i < kExactTiles);
+    __syncthreads();
+    if (i + 1 < tiles) issue_keys(i + 1);
+    if (!any) continue;
+    const uint32_t vbase = lds_at(&sv[i & 1][0]) + lane16;
     mask(now, sees - t0);
     weights();
     if (p.flags[(int64_t)head * p.capacity + tile0 + i] == 0) {
-      values(vbase);
+      values(vbase, i < kExactWeights);
       continue;
     }
     // Values that are not finite: one token at a time, into the rows that see

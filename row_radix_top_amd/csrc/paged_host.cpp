@@ -239,7 +239,7 @@ int check_prefill(const latent_prefill_args* a) {
 
 struct PrefillPlan {
   rrt::PrefillParams p;
-  size_t rope_at, value_at, valid_at, flag_at, bytes;
+  size_t low_at, rope_at, value_at, valid_at, flag_at, bytes;
 };
 
 int plan_prefill(const latent_prefill_args* a, PrefillPlan* out) {
@@ -257,7 +257,8 @@ int plan_prefill(const latent_prefill_args* a, PrefillPlan* out) {
   p.row_tiles = (int32_t)row_tiles;
   const size_t tiles = (size_t)capacity, heads = (size_t)a->num_heads;
   const size_t tile_bytes = (size_t)rrt::kCtxTile * PAGED_HEAD_DIM * 2;
-  out->rope_at = heads * tiles * tile_bytes;
+  out->low_at = heads * tiles * tile_bytes;
+  out->rope_at = out->low_at + heads * tiles * tile_bytes;
   out->value_at = out->rope_at + tiles * rrt::kCtxTile * PAGED_ROPE_DIM * 2;
   out->valid_at = out->value_at + heads * tiles * tile_bytes;
   out->flag_at = out->valid_at + tiles * sizeof(uint64_t);
@@ -379,6 +380,7 @@ int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t
   rrt::PrefillParams& p = plan.p;
   char* ws = static_cast<char*>(workspace);
   p.keys = ws;
+  p.lows = ws + plan.low_at;
   p.ropes = ws + plan.rope_at;
   p.values = ws + plan.value_at;
   p.valid = reinterpret_cast<uint64_t*>(ws + plan.valid_at);

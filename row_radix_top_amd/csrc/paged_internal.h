@@ -125,6 +125,7 @@ constexpr int32_t kCtxTile = 64;
 struct PrefillParams {
   latent_prefill_args a;
   char* keys;       // [heads][capacity] key tiles, fragment order (128 dims, 16 KB)
+  char* lows;       // as keys: what their rounding left, of each sequence's first tiles
   char* ropes;      // [capacity] rope tiles, fragment order (8 KB)
   char* values;     // [heads][capacity] value tiles, fragment order (16 KB)
   uint64_t* valid;  // [capacity]: which of a tile's tokens are in the cache

@@ -22,6 +22,9 @@ def _gpu():
     require_gpu()
 
 
+TWO_PARTS = 1024  # a sequence's first tokens, whose keys are kept to twice the bits
+
+
 class Case:
     def __init__(self, lengths, new, *, heads=3, dim=256, dtype="bfloat16", store="same", page_size=16, seed=0, gap=0,
                  poison=True, spread=1.0):
@@ -76,7 +79,9 @@ class Case:
         the keys and values rounded to the 16-bit type on top.  A key off by u
         relative to each of its 128 formed dims moves a score by at most u
         sum |q k| scale, which changes the weight by twice that; a value off by
-        u |v| moves the output by u A.  The products W c themselves are sums of
+        u |v| moves the output by u A.  Keys of a sequence's first 1024 tokens
+        come in two parts and are off by u^2 only, with 128 more products to
+        sum, each within 2^-24 of the sum.  The products W c themselves are sums of
         dim fp32 terms: (dim + 2) 2^-24 of their absolute sum, which moves a
         score by that of sum |q| (|W| |c|) and an output by that of p |W| |c|."""
         import torch
@@ -105,7 +110,8 @@ class Case:
                         ak, av = np.abs(y[:, :self.dim]) @ np.abs(wk[h]).T, np.abs(y[:, :self.dim]) @ np.abs(wv[h]).T
                         grow = (self.dim + 2) * f
                         # keys below the 16-bit type's normal range round by an absolute 2^-25 in fp16
-                        e = float(((np.abs(kn) * u + ak * grow + (2.0 ** -25 if fp16 else 0)) @ aq).max() * self.scale)
+                        ku = np.where(np.flatnonzero(keep) < TWO_PARTS, u * u + 130 * f, u)[:, None]
+                        e = float(((np.abs(kn) * ku + ak * grow + (2.0 ** -25 if fp16 else 0)) @ aq).max() * abs(self.scale))
                         p = np.exp(k @ q[t, h] * self.scale - lg)
                         to = to + p @ (np.abs(v) * (u + 2 * e * (1 + u)) + av * grow + (2.0 ** -25 if fp16 else 0))
                         tl = tl + e
@@ -135,6 +141,26 @@ def test_ragged_chunks(dtype, store, dim, page_size):
 @pytest.mark.parametrize("n,new", [(1, 1), (63, 63), (64, 1), (127, 127), (128, 128), (129, 129), (257, 200)])
 def test_one_sequence(n, new):
     Case([n], [new], heads=2, seed=n).check("one sequence")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("store", ["same", "float8_e4m3fn"])
+def test_past_the_tokens_kept_in_two_parts(dtype, store):
+    Case([1025, 1100, 2100, 1024], [2, 40, 3, 1], heads=2, dtype=dtype, store=store, seed=9).check("two parts")
+
+
+@pytest.mark.parametrize("by", [0.0, -0.04, 448.0])
+def test_scales_of_the_cache(by):
+    c = Case([70, 9], [70, 3], heads=2, store="float8_e4m3fn", seed=10)
+    c.by.fill_(by)
+    c.check("cache scale")
+
+
+def test_softmax_scales_of_zero_and_below():
+    for scale in (0.0, -0.05):
+        c = Case([200, 9], [70, 3], heads=2, seed=11)
+        c.scale = scale
+        c.check("softmax scale")
 
 
 def test_many_sequences():
