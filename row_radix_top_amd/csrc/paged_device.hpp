@@ -153,7 +153,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // h % 8 each XCD's L2 would see one 256-byte column of the cache, a fraction
 // of its channels.
 // Rows of chosen positions are alike: a group's parts go to one XCD, whose L2
-// then holds its table once (64 rows of 2048 of 65536 positions: 70 us against
+// then holds its table once (64 rows of 2048 of up to 32768 positions: 70 us against
 // 72).  Others: side by side, as a sequence on one XCD alone would leave the
 // XCDs with unequal shares, and every other eight in the reverse order, so that
 // none gets the longer of each two.  False past the last one.
