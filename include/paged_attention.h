@@ -18,6 +18,8 @@
  *   - Strides count elements.  Workspaces are 16-byte aligned, hold nothing
  *     between launches (no initialisation) and must not be shared by launches
  *     that may overlap: give each stream, and each captured graph, its own.
+ *   - Outputs do not overlap inputs, and the cache is not written while it is
+ *     read.
  *
  * The cache: a pool of num_pages pages of page_size tokens.  Position p of
  * sequence s lies in page block_table[s, p / page_size] at offset
@@ -56,8 +58,7 @@ typedef enum {
  * paged_layout -- block tables and slot maps of one step from request lengths.
  *
  *   lengths      int32 [num_seqs], tokens of each sequence after the step,
- *                clamped to [0, table_width * page_size] and to 2^30; pages
- *                times page_size stay below 2^31 (not checked).
+ *                clamped to [0, table_width * page_size] and to 2^30.
  *   new_tokens   int32 [num_seqs], how many of them are new, clamped to
  *                [0, length].
  *   free_pages   int32 [num_free], pages to hand out, in order.
@@ -66,10 +67,11 @@ typedef enum {
  *                ceil(length / page_size)) get the next free pages (-1 once
  *                they run out); all others are left as they were.
  *   starts       int32 [num_seqs + 1], receives the exclusive prefix sum of
- *                the new tokens; below 2^31 in total (not checked).
+ *                the new tokens; sums stop at 2^31 - 1.
  *   slots        int32 [capacity]: token t (of sequence s, the tokens of a
  *                sequence in order) gets page * page_size + offset, or -1
- *                where its table entry is negative.  Past the last token: -1.
+ *                where its table entry is negative or its slot would pass
+ *                2^31 - 1.  Past the last token: -1.
  *   row_lengths  int32 [capacity]: position + 1, the length that topk_ragged
  *                and the attention take for the token's row.  Past: 0.
  *   row_seqs     int32 [capacity]: the token's sequence.  Past: -1.
@@ -191,7 +193,7 @@ int latent_attention(const paged_attention_args* args, void* workspace, hipStrea
  *                  fit gets NaN in out and lse.
  *   out, lse       [num_tokens, num_heads, 128] and [num_tokens, num_heads].
  *   workspace      latent_prefill_workspace_size() bytes: the expanded keys
- *                  and values, 512 bytes a token and head.
+ *                  and values, 768 bytes a token and head.
  */
 typedef struct {
   const void* q;

@@ -73,11 +73,13 @@ __device__ __forceinline__ int32_t context_of(const PrefillParams& p, int32_t s)
 }
 __device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t per) { return (int32_t)(((int64_t)n + per - 1) / per); }
 
+// Inclusive sums over the wavefront; they stop at 2^31 - 1, so that lengths
+// that do not fit the workspace by far still lie past it.
 __device__ __forceinline__ int32_t scan_up(int32_t x, int lane) {
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int32_t y = __shfl_up(x, off);
-    if (lane >= off) x += y;
+    if (lane >= off) x = __builtin_elementwise_add_sat(x, y);
   }
   return x;
 }
@@ -88,11 +90,11 @@ __device__ __forceinline__ int32_t sequence_of_tile(const PrefillParams& p, int3
   int32_t base = 0;
   for (int32_t s0 = 0; s0 < p.a.num_seqs; s0 += 64) {
     const int32_t mine = s0 + lane < p.a.num_seqs ? tiles_of(context_of(p, s0 + lane), kCtxTile) : 0;
-    const int32_t upto = base + scan_up(mine, lane);
+    const int32_t upto = __builtin_elementwise_add_sat(base, scan_up(mine, lane));
     const uint64_t past = __builtin_amdgcn_ballot_w64(upto > tile);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
-      *before = __builtin_amdgcn_readlane(upto - mine, l);
+      *before = l == 0 ? base : __builtin_amdgcn_readlane(upto, l - 1);
       return s0 + l;
     }
     base = __builtin_amdgcn_readlane(upto, 63);
@@ -352,13 +354,14 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
         ctx = tiles_of(context_of(p, s), kCtxTile);
       }
       const int32_t mine = tiles_of(n, kRows);
-      const int32_t upto = rows_base + scan_up(mine, lane), cupto = ctx_base + scan_up(ctx, lane);
+      const int32_t upto = __builtin_elementwise_add_sat(rows_base, scan_up(mine, lane));
+      const int32_t cupto = __builtin_elementwise_add_sat(ctx_base, scan_up(ctx, lane));
       const uint64_t past = __builtin_amdgcn_ballot_w64(upto > want);
       if (past != 0) {
         const int l = __builtin_ctzll(past);
         seq = s0 + l;
-        local = __builtin_amdgcn_readlane(upto, l) - 1 - want;
-        tile0 = __builtin_amdgcn_readlane(cupto - ctx, l);
+        local = __builtin_amdgcn_readlane(mine, l) - 1 - (want - (l == 0 ? rows_base : __builtin_amdgcn_readlane(upto, l - 1)));
+        tile0 = l == 0 ? ctx_base : __builtin_amdgcn_readlane(cupto, l - 1);
         start = __builtin_amdgcn_readlane(from, l);
         count = __builtin_amdgcn_readlane(n, l);
         break;
@@ -427,6 +430,8 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   // and a tile ahead, so that no wait for vector memory is among the loads.
   using scalar_u64 = const __attribute__((address_space(4))) uint64_t;
   scalar_u64* valid_of = (scalar_u64*)(p.valid + tile0);
+  using scalar_u32 = const __attribute__((address_space(4))) uint32_t;
+  scalar_u32* flag_of = (scalar_u32*)(p.flags + (int64_t)head * p.capacity + tile0);
 
   float ref = -INFINITY, sum = 0.0f;  // base-2 logarithm; of this lane's tokens
   f32x16 o[4];
@@ -552,7 +557,8 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     if (i + 1 < tiles) issue_keys(i + 1);
     if (now != ~0ull) mask(now, kCtxTile);
     weights();
-    values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights);
+    // The second parts of weights meet finite values only.
+    values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights && flag_of[i] == 0);
   }
   // Tiles that some row sees in part or not at all.
   for (int32_t i = whole; i < tiles; ++i) {
@@ -570,7 +576,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     const uint32_t vbase = lds_at(&sv[i & 1][0]) + lane16;
     mask(now, sees - t0);
     weights();
-    if (p.flags[(int64_t)head * p.capacity + tile0 + i] == 0) {
+    if (flag_of[i] == 0) {
       values(vbase, i < kExactWeights);
       continue;
     }

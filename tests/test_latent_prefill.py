@@ -212,6 +212,21 @@ def test_later_tokens_that_are_not_finite_do_not_reach_earlier_rows(store):
     assert bool(out[k:].isnan().all()) and bool(lse[k:].isnan().all())
 
 
+def test_values_past_the_range_reach_the_rows_that_see_them():
+    """A value that fp16 does not hold is an infinity in the rows that see it, whole tiles and others."""
+    import torch
+    c = Case([260], [260], heads=2, dtype="float16", seed=12)
+    c.wv[:, 0] = 200.0
+    flat = c.c.view(-1, c.dim + ROPE)
+    slot = int(c.slots(0)[5])
+    flat[torch.as_tensor(c.slots(0), device="cuda"), :c.dim] -= flat[torch.as_tensor(c.slots(0), device="cuda"), :c.dim].mean(
+        dim=1, keepdim=True)  # values of dim 0 near 0
+    flat[slot, :c.dim] += 3.0
+    out, lse = c.run()
+    assert bool((out[5:, :, 0] == math.inf).all()) and bool(out[:5].isfinite().all())
+    assert bool(out[:, :, 1:].isfinite().all()) and bool(lse.isfinite().all())
+
+
 def test_context_tokens_too_small():
     """Sequences that do not fit give NaN; those before them are right."""
     c = Case([100, 500, 90], [10, 20, 30], heads=2, seed=9)
