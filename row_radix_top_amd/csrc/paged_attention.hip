@@ -27,6 +27,11 @@ namespace rrt {
 //
 // P is rounded to the 16-bit type for the matrix instruction (half a step
 // relative to each weight); m, l, S and O stay fp32.
+//
+// Bound by reading the cache.  64 rows of 1 to 32768 positions, 64 heads on 8,
+// bf16: 747 us, 5.5 TB/s where a plain read reaches 6.4; 4 rows of 8192: 24.5
+// us, 5.5 TB/s; 64 rows of 2048 chosen positions, 40 heads on 4, e4m3: 31 to
+// 33 us, 4.2 TB/s of scattered 512-byte rows.
 // ---------------------------------------------------------------------------
 constexpr int kAttnBlock = 256;
 constexpr int kTok = 32;  // tokens of a wavefront's tile
