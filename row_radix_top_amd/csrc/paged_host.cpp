@@ -60,7 +60,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // A part's fewest positions and the unit its length is rounded to: four
 // wavefronts take 32 tokens each.
 constexpr int32_t kUnit = 128;
-constexpr int32_t kLeast = 256;
+constexpr int32_t kLeast = 256, kLeastChosen = 512;
 constexpr int32_t kMostParts = 128;
 // The latent kernel's: tiles of 64 tokens, one workgroup on a CU.
 constexpr int32_t kLatentUnit = 64;
@@ -74,11 +74,33 @@ constexpr int32_t kLatentLeast = 128;
 //   64 x 8 ragged, 1 to 32768           895  800  755  752  767
 //   64 x 8 of 16384                     801  814  801  782  778
 //   256 x 8 ragged, 500 to 4096         482  479  489  522  607
-//   64 x 4 of 2048 chosen                31   33   35   38   38
+//   25 x 4 of 2048 chosen                27   25   26   27   27
+//   40 x 4 of 2048 chosen                31   40   37   34   34
+//   4 x 4 of 512 chosen                  14   19   18   18   18
 // So: two workgroups a CU; four parts at least where rows may differ in length
-// (the longest one ends the launch), one a CU is enough where all are alike.
-int64_t parts_for(bool latent, bool chosen, int64_t units, int64_t cus) {
-  if (latent || chosen) return ceil_div(cus, units);
+// (the longest one ends the launch); where all are alike no more than one a CU,
+// and a second launch only for parts of 512.
+//
+// The latent kernel takes a CU for itself, so that a workgroup too many is
+// another round.  1, 2, 3, 4, 5 and 8 parts, 128 heads in units of 64:
+//   80 units of 2048 chosen              92   61   52   69   69   75
+//   200 units of 2048 chosen             98  119  131  144  149  201
+//   40 units of 8192                    217  118   86   68   58   45 (12: 43, 13: 59)
+//   80 units ragged, 1 to 16384         601  318  223  179  159  166
+//   128 units ragged, 1 to 16384        604  329  238  212  213  229
+//   256 units ragged, 1 to 8192         312  239  245  257  281  334
+//   256 units ragged, 1 to 1024          53   64   82   97  105  169
+// So: what fits one round where rows are alike or that is four parts or more;
+// otherwise four or, of many units, two, none below 1024 positions.  One row of
+// 256 positions takes 13 us in one part and 16 in two, one of 512 20 and 17.
+int64_t parts_for(bool latent, bool chosen, int64_t units, int64_t longest, int64_t cus) {
+  if (latent) {
+    if (longest < 512) return 1;
+    const int64_t once = std::max<int64_t>(1, cus / units);
+    if (chosen || once >= 4) return once;
+    return std::max(once, std::min<int64_t>(units * 8 <= cus * 5 ? 4 : 2, longest / 1024));
+  }
+  if (chosen) return std::max<int64_t>(1, cus / units);
   return std::max<int64_t>(4, ceil_div(2 * cus, units));
 }
 
@@ -156,7 +178,7 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
     out->fn = rrt::latent_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, heads);
   } else {
     p.unit = kUnit;
-    p.least = kLeast;
+    p.least = chosen ? kLeastChosen : kLeast;
     // Rows of a sequence read its cache together unless each has its own
     // chosen positions.
     p.group_rows = chosen ? 1 : a->next_n;
@@ -168,7 +190,7 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
     out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, p.group_rows, tiles);
   }
   const int64_t longest = chosen ? a->num_chosen : rrt::table_tokens(a->table_width, a->page_size);
-  int64_t most = a->max_splits > 0 ? a->max_splits : parts_for(latent, chosen, units, cus);
+  int64_t most = a->max_splits > 0 ? a->max_splits : parts_for(latent, chosen, units, longest, cus);
   most = std::max<int64_t>(1, std::min<int64_t>({most, (int64_t)kMostParts, longest / p.least}));
   p.most = (int32_t)most;
   out->grid = ceil_div((int64_t)p.groups * most, 8) * 8 * (units / p.groups);  // see work_of
