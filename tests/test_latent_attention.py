@@ -100,6 +100,13 @@ class Case:
         return out, lse
 
 
+@pytest.mark.parametrize("splits", [0, 2])
+def test_many_ragged_rows(splits):
+    """Rows run longest first, 64 at a time: each exactly once."""
+    rng = np.random.default_rng(6)
+    Case(rng.integers(0, 400, size=70), heads=2, dim=256, seed=6).check("many rows", max_splits=splits)
+
+
 def _choose(rng, lengths, k):
     rows = []
     for n in lengths:

@@ -147,6 +147,17 @@ def test_later_tokens_that_are_not_finite_do_not_reach_earlier_rows():
     assert bool(out[1:].isnan().all())
 
 
+@pytest.mark.parametrize("next_n", [1, 2])
+@pytest.mark.parametrize("n", [64, 65, 150])
+def test_many_ragged_rows(n, next_n):
+    """Rows run longest first, 64 groups at a time: each exactly once."""
+    rng = np.random.default_rng(n)
+    last = rng.integers(0, 300, size=n)
+    lengths = last if next_n == 1 else np.stack([np.maximum(last - 1, 0), last], axis=1)
+    Case(lengths, heads=2, kv=1, dim=64, seed=n).check("many rows")
+    Case(lengths, heads=2, kv=1, dim=64, seed=n).check("many rows", max_splits=3)
+
+
 def _choose(rng, lengths, k, keep=1.0):
     rows = []
     for n in lengths:
