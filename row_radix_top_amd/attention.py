@@ -437,5 +437,6 @@ def latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, *, context_
                        lengths_at, out.data_ptr(), lse.data_ptr(), q.stride(0), q.stride(1), cache.stride(0),
                        cache.stride(1), block_table.stride(0), context_tokens, tokens, n, heads, dim, cache.shape[1],
                        cache.shape[0], block_table.shape[1], softmax_scale, code, store)
-    _launch("latent_prefill", args, workspace, (context_tokens, tokens, n, heads, dim), q)
+    _launch("latent_prefill", args, workspace,
+            (context_tokens, tokens, n, heads, dim, cache.shape[1], block_table.shape[1]), q)
     return out, lse

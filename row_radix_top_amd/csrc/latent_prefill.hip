@@ -6,7 +6,7 @@
 namespace rrt {
 
 // ---------------------------------------------------------------------------
-// Two kernels.  `expand` forms k_h = W_k,h c and v_h = W_v,h c for every
+// Two kernels (and a join where few rows share out their contexts).  `expand` forms k_h = W_k,h c and v_h = W_v,h c for every
 // context token and head (2 DC 256 flop each) and leaves them in the workspace
 // in fragment order: 1 KB blocks that are, lane by lane, the operands that the
 // attention's matrix instructions take.  `prefill` streams them through LDS
@@ -325,8 +325,52 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // changed nothing.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;
+constexpr int kLeastTiles = 8;  // of a part of a split context
 constexpr float kLazyStep = 8.0f;
 constexpr int kAheadBlocks = 4;
+
+// A tile of query rows: its sequence, its place within the sequence's chunk
+// (the last one first: it has the most work), the context tiles before the
+// sequence's, the chunk's first row and rows.  False past the last one.
+struct RowTile {
+  int32_t seq, local, tile0, start, count;
+};
+__device__ __forceinline__ bool row_tile_of(const PrefillParams& p, int32_t want, int lane, RowTile* t) {
+  const latent_prefill_args& a = p.a;
+  int32_t rows_base = 0, ctx_base = 0;
+  for (int32_t s0 = 0; s0 < a.num_seqs; s0 += 64) {
+    const int32_t s = s0 + lane;
+    int32_t from = 0, n = 0, ctx = 0;
+    if (s < a.num_seqs) {
+      from = clamp_to(a.starts[s], a.num_tokens);
+      n = clamp_to(a.starts[s + 1], a.num_tokens) - from;
+      n = n < 0 ? 0 : n;
+      ctx = tiles_of(context_of(p, s), kCtxTile);
+    }
+    const int32_t mine = tiles_of(n, kRows);
+    const int32_t upto = __builtin_elementwise_add_sat(rows_base, scan_up(mine, lane));
+    const int32_t cupto = __builtin_elementwise_add_sat(ctx_base, scan_up(ctx, lane));
+    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > want);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      t->seq = s0 + l;
+      t->local = __builtin_amdgcn_readlane(mine, l) - 1 -
+                 (want - (l == 0 ? rows_base : __builtin_amdgcn_readlane(upto, l - 1)));
+      t->tile0 = l == 0 ? ctx_base : __builtin_amdgcn_readlane(cupto, l - 1);
+      t->start = __builtin_amdgcn_readlane(from, l);
+      t->count = __builtin_amdgcn_readlane(n, l);
+      return true;
+    }
+    rows_base = __builtin_amdgcn_readlane(upto, 63);
+    ctx_base = __builtin_amdgcn_readlane(cupto, 63);
+  }
+  return false;
+}
+// Parts that a row tile's context tiles are shared out to.
+__device__ __forceinline__ int32_t parts_of(int32_t tiles, int32_t most) {
+  const int32_t n = tiles / kLeastTiles;
+  return n < 1 ? 1 : n < most ? n : most;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
@@ -337,40 +381,11 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int32_t head = (int32_t)(blockIdx.x % (uint32_t)a.num_heads);
-  const int32_t want = (int32_t)(blockIdx.x / (uint32_t)a.num_heads);
+  const int32_t slot = (int32_t)(blockIdx.x / (uint32_t)a.num_heads), part = slot % p.parts;
 
-  // The sequence of this query tile, its tile within the sequence (the last
-  // one first: it has the most work) and the context tiles before it.
-  int32_t seq = -1, local = 0, tile0 = 0, start = 0, count = 0;
-  {
-    int32_t rows_base = 0, ctx_base = 0;
-    for (int32_t s0 = 0; s0 < a.num_seqs; s0 += 64) {
-      const int32_t s = s0 + lane;
-      int32_t from = 0, n = 0, ctx = 0;
-      if (s < a.num_seqs) {
-        from = clamp_to(a.starts[s], a.num_tokens);
-        n = clamp_to(a.starts[s + 1], a.num_tokens) - from;
-        n = n < 0 ? 0 : n;
-        ctx = tiles_of(context_of(p, s), kCtxTile);
-      }
-      const int32_t mine = tiles_of(n, kRows);
-      const int32_t upto = __builtin_elementwise_add_sat(rows_base, scan_up(mine, lane));
-      const int32_t cupto = __builtin_elementwise_add_sat(ctx_base, scan_up(ctx, lane));
-      const uint64_t past = __builtin_amdgcn_ballot_w64(upto > want);
-      if (past != 0) {
-        const int l = __builtin_ctzll(past);
-        seq = s0 + l;
-        local = __builtin_amdgcn_readlane(mine, l) - 1 - (want - (l == 0 ? rows_base : __builtin_amdgcn_readlane(upto, l - 1)));
-        tile0 = l == 0 ? ctx_base : __builtin_amdgcn_readlane(cupto, l - 1);
-        start = __builtin_amdgcn_readlane(from, l);
-        count = __builtin_amdgcn_readlane(n, l);
-        break;
-      }
-      rows_base = __builtin_amdgcn_readlane(upto, 63);
-      ctx_base = __builtin_amdgcn_readlane(cupto, 63);
-    }
-  }
-  if (seq < 0) return;
+  RowTile at_tile;
+  if (!row_tile_of(p, slot / p.parts, lane, &at_tile)) return;
+  const int32_t seq = at_tile.seq, local = at_tile.local, tile0 = at_tile.tile0, start = at_tile.start, count = at_tile.count;
   const int32_t ctx = context_of(p, seq);
   const int32_t row0 = local * kRows;  // first row of the tile, within the chunk
   const bool fits = (int64_t)tile0 + tiles_of(ctx, kCtxTile) <= p.capacity;
@@ -382,6 +397,10 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   const int32_t last = row0 + kRows < count ? row0 + kRows : count;  // rows of the tile end here
   const int32_t longest = ctx - count + last;                        // positions its last row sees
   const int32_t tiles = longest > 0 && fits ? tiles_of(longest, kCtxTile) : 0;
+  const int32_t parts = parts_of(tiles, p.parts);
+  if (part >= parts) return;
+  const int32_t chunk = (tiles + parts - 1) / parts;
+  const int32_t begin = part * chunk < tiles ? part * chunk : tiles, stop = tiles - begin < chunk ? tiles : begin + chunk;
   // Positions that all rows of the wavefront see, and that any of them does.
   const int32_t wfirst = row0 + w * 32, wlast = wfirst + 31 < count - 1 ? wfirst + 31 : count - 1;
   const int32_t all_see = wfirst < count ? ctx - count + wfirst + 1 : 0;
@@ -539,39 +558,40 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 
   // Tiles that every row of the workgroup sees whole.
   const int32_t first_sees = ctx - count + row0 + 1;
-  const int32_t whole = first_sees > 0 && fits ? first_sees / kCtxTile : 0;
+  const int32_t all_whole = first_sees > 0 && fits ? first_sees / kCtxTile : 0;
+  const int32_t whole = all_whole < begin ? begin : all_whole < stop ? all_whole : stop;
   uint64_t valid = 0;
-  if (tiles > 0) {
-    issue_keys(0);
-    issue_values(0);
-    valid = valid_of[0];
+  if (begin < stop) {
+    issue_keys(begin);
+    issue_values(begin);
+    valid = valid_of[begin];
   }
-  for (int32_t i = 0; i < whole; ++i) {
+  for (int32_t i = begin; i < whole; ++i) {
     wait_loads();
     __syncthreads();
-    if (i + 1 < tiles) issue_values(i + 1);
+    if (i + 1 < stop) issue_values(i + 1);
     const uint64_t now = valid;
-    if (i + 1 < tiles) valid = valid_of[i + 1];
+    if (i + 1 < stop) valid = valid_of[i + 1];
     scores(i < kExactTiles);
     __syncthreads();  // the keys are read
-    if (i + 1 < tiles) issue_keys(i + 1);
+    if (i + 1 < stop) issue_keys(i + 1);
     if (now != ~0ull) mask(now, kCtxTile);
     weights();
     // The second parts of weights meet finite values only.
     values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights && flag_of[i] == 0);
   }
   // Tiles that some row sees in part or not at all.
-  for (int32_t i = whole; i < tiles; ++i) {
+  for (int32_t i = whole; i < stop; ++i) {
     wait_loads();
     __syncthreads();
-    if (i + 1 < tiles) issue_values(i + 1);
+    if (i + 1 < stop) issue_values(i + 1);
     const uint64_t now = valid;
-    if (i + 1 < tiles) valid = valid_of[i + 1];
+    if (i + 1 < stop) valid = valid_of[i + 1];
     const int32_t t0 = i * kCtxTile;
     const bool any = t0 < any_see;  // else nothing here for this wavefront
     if (any) scores(i < kExactTiles);
     __syncthreads();
-    if (i + 1 < tiles) issue_keys(i + 1);
+    if (i + 1 < stop) issue_keys(i + 1);
     if (!any) continue;
     const uint32_t vbase = lds_at(&sv[i & 1][0]) + lane16;
     mask(now, sees - t0);
@@ -607,6 +627,17 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   sum += __shfl_xor(sum, 32);
   if (!real) return;
   const int64_t at = (int64_t)(start + j) * a.num_heads + head;
+  if (parts > 1) {
+    const int64_t pi = at * p.parts + part;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *(f32x4*)(p.part_out + pi * kHead + d * 32 + k * 8 + half * 4) =
+            f32x4{o[d][k * 4], o[d][k * 4 + 1], o[d][k * 4 + 2], o[d][k * 4 + 3]};
+    if (half == 0) p.part_stat[pi] = float2{ref, sum};
+    return;
+  }
   const float by = !fits ? NAN : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int d = 0; d < 4; ++d)
@@ -616,6 +647,42 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
           u32x2{T::pack(o[d][k * 4] * by, o[d][k * 4 + 1] * by), T::pack(o[d][k * 4 + 2] * by, o[d][k * 4 + 3] * by)};
   if (half == 0 && a.lse != nullptr)
     a.lse[at] = !fits ? NAN : sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
+}
+
+// Joins the parts of split contexts: eight rows of a row tile and head a
+// workgroup, 32 threads of four dims each.
+constexpr int kJoinRows = 8;
+template <typename T>
+__global__ void __launch_bounds__(256) prefill_join_kernel(PrefillParams p) {
+  const latent_prefill_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int32_t head = (int32_t)(blockIdx.x % (uint32_t)a.num_heads);
+  const int32_t slot = (int32_t)(blockIdx.x / (uint32_t)a.num_heads);
+  RowTile t;
+  if (!row_tile_of(p, slot / (kRows / kJoinRows), lane, &t)) return;
+  const int32_t row0 = t.local * kRows, ctx = context_of(p, t.seq);
+  const int32_t longest = ctx - t.count + (row0 + kRows < t.count ? row0 + kRows : t.count);
+  const bool fits = (int64_t)t.tile0 + tiles_of(ctx, kCtxTile) <= p.capacity;
+  const int32_t parts = parts_of(longest > 0 && fits ? tiles_of(longest, kCtxTile) : 0, p.parts);
+  const int32_t j = row0 + slot % (kRows / kJoinRows) * kJoinRows + (tid >> 5);
+  if (parts == 1 || j >= t.count) return;
+  const int64_t at = (int64_t)(t.start + j) * a.num_heads + head;
+  const float2* stat = p.part_stat + at * p.parts;
+  const float* from = p.part_out + at * p.parts * kHead + (tid & 31) * 4;
+  float top = -INFINITY;
+  for (int32_t i = 0; i < parts; ++i) top = fmaxf(top, stat[i].x);
+  float sum = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int32_t i = 0; i < parts; ++i) {
+    const float2 m = stat[i];
+    const float by = m.x == top ? 1.0f : exp2_fast(m.x - top);
+    sum += m.y * by;
+    o += *(const f32x4*)(from + i * kHead) * by;
+  }
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *(u32x2*)((uint16_t*)a.out + at * kHead + (tid & 31) * 4) = u32x2{T::pack(o[0] * by, o[1] * by), T::pack(o[2] * by, o[3] * by)};
+  if ((tid & 31) == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 namespace {
@@ -633,6 +700,10 @@ const void* expand_kernel_ptr(int dtype, int store, int latent_dim) {
 const void* prefill_kernel_ptr(int dtype) {
   return dtype == PAGED_BF16 ? (const void*)&prefill_kernel<Bf16> : (const void*)&prefill_kernel<Fp16>;
 }
+const void* prefill_join_kernel_ptr(int dtype) {
+  return dtype == PAGED_BF16 ? (const void*)&prefill_join_kernel<Bf16> : (const void*)&prefill_join_kernel<Fp16>;
+}
 int prefill_rows() { return kRows; }
+int prefill_join_rows() { return kJoinRows; }
 
 }  // namespace rrt

@@ -261,10 +261,10 @@ int check_prefill(const latent_prefill_args* a) {
 
 struct PrefillPlan {
   rrt::PrefillParams p;
-  size_t low_at, rope_at, value_at, valid_at, flag_at, bytes;
+  size_t low_at, rope_at, value_at, valid_at, flag_at, part_at, stat_at, bytes;
 };
 
-int plan_prefill(const latent_prefill_args* a, PrefillPlan* out) {
+int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* out) {
   if (int rc = check_prefill(a)) return rc;
   std::memset(out, 0, sizeof(*out));
   if (a->num_tokens == 0 || a->num_seqs == 0) return TOPK_OK;
@@ -284,7 +284,22 @@ int plan_prefill(const latent_prefill_args* a, PrefillPlan* out) {
   out->value_at = out->rope_at + tiles * rrt::kCtxTile * PAGED_ROPE_DIM * 2;
   out->valid_at = out->value_at + heads * tiles * tile_bytes;
   out->flag_at = out->valid_at + tiles * sizeof(uint64_t);
-  out->bytes = out->flag_at + heads * tiles * sizeof(uint32_t);
+  out->part_at = (out->flag_at + heads * tiles * sizeof(uint32_t) + 15) / 16 * 16;
+  // Few row tiles: their contexts are shared out, as far as two workgroups a
+  // CU go, and joined by a third launch.  us without and with (1 sequence of
+  // 8192: 34 rows x 8 heads 201, 66; 1071 x 16 236, 178; 4 of 1000 to 8192, 902 x
+  // 16: 173, 134); a part more than fits (3 sequences, 1782 x 24) 256, 263.
+  const int64_t longest = std::min<int64_t>(a->context_tokens, rrt::table_tokens(a->table_width, a->page_size));
+  p.parts = 1;
+  if (longest >= 2048) {
+    int dev = 0, cus = 0;
+    if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
+    const int64_t units = ceil_div(a->num_tokens, rrt::prefill_rows()) * a->num_heads;
+    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * cus / units, longest / 1024, 16}));
+  }
+  const size_t splits = p.parts == 1 ? 0 : (size_t)a->num_tokens * heads * (size_t)p.parts;
+  out->stat_at = out->part_at + splits * PAGED_HEAD_DIM * sizeof(float);
+  out->bytes = out->stat_at + splits * sizeof(float2);
   return TOPK_OK;
 }
 
@@ -381,17 +396,16 @@ int latent_attention(const paged_attention_args* args, void* workspace, hipStrea
 }
 
 int latent_prefill_workspace_size(const latent_prefill_args* args, hipStream_t stream, size_t* bytes) {
-  (void)stream;
   REQUIRE(bytes != nullptr, "null bytes");
   PrefillPlan plan;
-  if (int rc = plan_prefill(args, &plan)) return rc;
+  if (int rc = plan_prefill(args, stream, &plan)) return rc;
   *bytes = plan.bytes;
   return TOPK_OK;
 }
 
 int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t stream) {
   PrefillPlan plan;
-  if (int rc = plan_prefill(args, &plan)) return rc;
+  if (int rc = plan_prefill(args, stream, &plan)) return rc;
   if (plan.bytes == 0) return TOPK_OK;
   if (workspace == nullptr) {
     char buf[96];
@@ -410,8 +424,14 @@ int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t
   if (int rc = launch(rrt::expand_kernel_ptr(args->dtype, args->store, args->latent_dim),
                       ceil_div(p.capacity, 2) * args->num_heads, 256, &p, stream, "expansion of latent vectors"))
     return rc;
-  return launch(rrt::prefill_kernel_ptr(args->dtype), (int64_t)p.row_tiles * args->num_heads, 256, &p, stream,
-                "latent_prefill");
+  p.part_out = reinterpret_cast<float*>(ws + plan.part_at);
+  p.part_stat = reinterpret_cast<float2*>(ws + plan.stat_at);
+  const int64_t row_tiles = (int64_t)p.row_tiles * args->num_heads;
+  if (int rc = launch(rrt::prefill_kernel_ptr(args->dtype), row_tiles * p.parts, 256, &p, stream, "latent_prefill"))
+    return rc;
+  if (p.parts == 1) return TOPK_OK;
+  return launch(rrt::prefill_join_kernel_ptr(args->dtype), row_tiles * (rrt::prefill_rows() / rrt::prefill_join_rows()),
+                256, &p, stream, "join of split contexts");
 }
 
 int64_t paged_debug_place(const int32_t* table_row, int32_t page_size, int32_t num_pages, int64_t page_stride,

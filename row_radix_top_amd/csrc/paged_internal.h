@@ -130,7 +130,10 @@ struct PrefillParams {
   char* values;     // [heads][capacity] value tiles, fragment order (16 KB)
   uint64_t* valid;  // [capacity]: which of a tile's tokens are in the cache
   uint32_t* flags;  // [heads][capacity]: 1 where a value is not finite
+  float* part_out;    // split contexts: [rows][heads][parts][128], not divided by the sum,
+  float2* part_stat;  // and (maximum, sum) of each
   float scale_log2;
+  int32_t parts;      // of a row tile's context, at most
   int32_t capacity;   // tiles of the workspace
   int32_t row_tiles;  // query tiles of a head that the grid covers
 };
@@ -143,6 +146,8 @@ const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, i
 const void* join_kernel_ptr(int dtype, int head_dim, bool many);
 const void* expand_kernel_ptr(int dtype, int store, int latent_dim);
 const void* prefill_kernel_ptr(int dtype);
-int prefill_rows();  // query rows of a workgroup
+const void* prefill_join_kernel_ptr(int dtype);
+int prefill_rows();       // query rows of a workgroup
+int prefill_join_rows();  // and of one of the join
 
 }  // namespace rrt

@@ -149,6 +149,21 @@ def test_past_the_tokens_kept_in_two_parts(dtype, store):
     Case([1025, 1100, 2100, 1024], [2, 40, 3, 1], heads=2, dtype=dtype, store=store, seed=9).check("two parts")
 
 
+@pytest.mark.parametrize("store", ["same", "float8_e4m3fn"])
+def test_few_rows_share_out_their_contexts(store):
+    """Long contexts are split and joined; short ones beside them are not, and rows outside are left alone."""
+    import torch
+    c = Case([5000, 70, 1500, 2600, 0], [3, 70, 130, 1, 4], heads=2, store=store, gap=5, seed=14)
+    out = torch.full((c.tokens, c.heads, HEAD), 3.0, device="cuda", dtype=c.dt)
+    lse = torch.full((c.tokens, c.heads), 3.0, device="cuda")
+    c.check("split", out=out, lse=lse)
+    for x in (out, lse):
+        assert bool((x[:5] == 3).all()) and bool((x[-5:] == 3).all())
+    c.table[0, 3:40] = -1  # a part whose tokens are mostly missing
+    c.table[3, 100:] = -1
+    c.check("split, missing pages")
+
+
 @pytest.mark.parametrize("by", [0.0, -0.04, 448.0])
 def test_scales_of_the_cache(by):
     c = Case([70, 9], [70, 3], heads=2, store="float8_e4m3fn", seed=10)
