@@ -18,6 +18,8 @@
  *   - Strides count elements.  Workspaces are 16-byte aligned, hold nothing
  *     between launches (no initialisation) and must not be shared by launches
  *     that may overlap: give each stream, and each captured graph, its own.
+ *     A size is that of the very arguments it was asked for: a call with fewer
+ *     rows may be split further and need more.
  *   - Outputs do not overlap inputs, and the cache is not written while it is
  *     read.
  *
