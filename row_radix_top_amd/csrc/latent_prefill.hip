@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // changed nothing.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;
-constexpr int kLeastTiles = 8;  // of a part of a split context
+constexpr int kLeastTiles = 4;  // of a part of a split context
 constexpr float kLazyStep = 8.0f;
 constexpr int kAheadBlocks = 4;
 

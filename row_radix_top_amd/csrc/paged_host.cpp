@@ -286,16 +286,17 @@ int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* 
   out->flag_at = out->valid_at + tiles * sizeof(uint64_t);
   out->part_at = (out->flag_at + heads * tiles * sizeof(uint32_t) + 15) / 16 * 16;
   // Few row tiles: their contexts are shared out, as far as two workgroups a
-  // CU go, and joined by a third launch.  us without and with (1 sequence of
-  // 8192: 34 rows x 8 heads 201, 66; 1071 x 16 236, 178; 4 of 1000 to 8192, 902 x
-  // 16: 173, 134); a part more than fits (3 sequences, 1782 x 24) 256, 263.
+  // CU go, and joined by a third launch.  us without, in parts of 1024 tokens
+  // and of 256: 1 sequence of 8192, 34 rows x 8 heads 201, 66, 56; 1071 x 16 236,
+  // 178, 178; 4 of 500 to 1500, 201 x 8 68, 57, 46; 1 of 1024, 5 x 16 48, 39, 33.
+  // A part more than fits (3 sequences, 1782 x 24): 256, 263.
   const int64_t longest = std::min<int64_t>(a->context_tokens, rrt::table_tokens(a->table_width, a->page_size));
   p.parts = 1;
-  if (longest >= 2048) {
+  if (longest >= 512) {
     int dev = 0, cus = 0;
     if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
     const int64_t units = ceil_div(a->num_tokens, rrt::prefill_rows()) * a->num_heads;
-    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * cus / units, longest / 1024, 16}));
+    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * cus / units, longest / 256, 16}));
   }
   const size_t splits = p.parts == 1 ? 0 : (size_t)a->num_tokens * heads * (size_t)p.parts;
   out->stat_at = out->part_at + splits * PAGED_HEAD_DIM * sizeof(float);

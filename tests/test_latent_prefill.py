@@ -153,7 +153,7 @@ def test_past_the_tokens_kept_in_two_parts(dtype, store):
 def test_few_rows_share_out_their_contexts(store):
     """Long contexts are split and joined; short ones beside them are not, and rows outside are left alone."""
     import torch
-    c = Case([5000, 70, 1500, 2600, 0], [3, 70, 130, 1, 4], heads=2, store=store, gap=5, seed=14)
+    c = Case([5000, 70, 1500, 2600, 0, 3900], [3, 70, 130, 1, 4, 2], heads=2, store=store, gap=5, seed=14)  # 3900: some parts are empty
     out = torch.full((c.tokens, c.heads, HEAD), 3.0, device="cuda", dtype=c.dt)
     lse = torch.full((c.tokens, c.heads), 3.0, device="cuda")
     c.check("split", out=out, lse=lse)
