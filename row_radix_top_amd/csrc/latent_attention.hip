@@ -34,9 +34,8 @@ namespace rrt {
 //
 // The weights are relative to a reference that follows the running maximum
 // lazily: only when a score passes it by 2^8 does the workgroup agree on a new
-// one, form the weights again and rescale (P then stays below 2^8, sums below
-// 2^8 n: far inside fp32; relative precision does not depend on the
-// reference).
+// one, form the weights again and rescale (P then stays below 2^8, or below 2^15
+// as fp16 keeps it, sums below that times n: far inside fp32).
 //
 // LDS rows are a multiple of all banks wide; 16-byte chunk c of token t's row
 // is kept at c ^ swizzle(t), which spreads both the 16 tokens of a key operand
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kLatentBlock, 2) latent_kernel(AttnParams p) {
     auto weights = [&] {
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        const float r = ref[h] == -INFINITY ? 0.0f : ref[h];
+        const float r = ref[h] == -INFINITY ? 0.0f : ref[h] - lift<T>(kLazy);
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = exp2_fast(s[h][e] - r);
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kLatentBlock, 2) latent_kernel(AttnParams p) {
     float total = 0.0f;
 #pragma unroll
     for (int k = 0; k < WT; ++k) total += ssum[k][c * 16 + col];
-    const float m = smax[0][c * 16 + col];
+    const float m = smax[0][c * 16 + col] - lift<T>(kLazy);
     const int64_t at = (int64_t)row * a.num_heads + head;
     if (sp.parts == 1) {
       const float by = total == 0.0f ? 0.0f : by_cache / total;

@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= by;
     }
-    const float r = ref == -INFINITY ? 0.0f : -ref;
+    const float r = ref == -INFINITY ? 0.0f : lift<T>(kLazyStep) - ref;
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -626,6 +626,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 
   sum += __shfl_xor(sum, 32);
   if (!real) return;
+  ref -= lift<T>(kLazyStep);  // of the weights as they are kept
   const int64_t at = (int64_t)(start + j) * a.num_heads + head;
   if (parts > 1) {
     const int64_t pi = at * p.parts + part;

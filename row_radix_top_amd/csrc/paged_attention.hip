@@ -26,7 +26,8 @@ namespace rrt {
 // all live in the lane of their column: no exchange but the maximum's.
 //
 // P is rounded to the 16-bit type for the matrix instruction (half a step
-// relative to each weight); m, l, S and O stay fp32.
+// relative to each weight, which is lifted into the type's range); m, l, S and O
+// stay fp32.
 //
 // Bound by reading the cache.  64 rows of 1 to 32768 positions, 64 heads on 8,
 // bf16: 747 us, 5.5 TB/s where a plain read reaches 6.4; 4 rows of 8192: 24.5
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
 #pragma unroll
         for (int d = 0; d < VD; ++d) o[t][d] *= by;
       }
-      const float ref = m[t] == -INFINITY ? 0.0f : m[t];
+      const float ref = m[t] == -INFINITY ? 0.0f : m[t] - T::kLift;
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -384,11 +385,11 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
       if (sp.parts == 1) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         *(uint32_t*)((uint16_t*)a.out + at * D + dim) = T::pack(x * inv, y * inv);
-        if (dim == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (cm + __log2f(sum)) * kLn2;
+        if (dim == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (cm - T::kLift + __log2f(sum)) * kLn2;
       } else {
         const int64_t pi = at * p.most + part;
         *(float2*)(p.part_out + pi * D + dim) = float2{x, y};
-        if (dim == 0) p.part_stat[pi] = float2{cm, sum};
+        if (dim == 0) p.part_stat[pi] = float2{cm - T::kLift, sum};
       }
     }
   }

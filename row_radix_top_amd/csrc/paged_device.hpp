@@ -24,6 +24,12 @@ using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 // l % 16 for the rows l / 16 * 4 .. + 4; mfma32: D[32][32] += A[32][16]
 // B[16][32], A's row and B's column l % 32 for k = l / 32 * 8 .. + 8, D's column
 // l % 32 for the rows 8 j + l / 32 * 4 + i as value 4 j + i.
+// kLift: a softmax weight of at most 1 is kept times 2^kLift.  fp16 holds nothing
+// below 2^-24 and full precision only from 2^-14 up, and the many small weights
+// of a long row with one large one matter together: 65,535 weights of e^-18 are
+// 1e-3 of the output, and were zeros beside a weight of 1.  2^15 is the most
+// that fp16 takes; bf16 has the exponents of fp32 and needs none.  Sums are of
+// lifted weights too, so an output does not change and a log-sum-exp by kLift.
 struct Bf16 {
   using elem = __bf16;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -45,6 +51,7 @@ struct Bf16 {
                                                    0, 0);
   }
   static constexpr float kLargest = 3.3895313892515355e38f;
+  static constexpr float kLift = 0.0f;
 };
 
 struct Fp16 {
@@ -68,6 +75,7 @@ struct Fp16 {
                                                   0);
   }
   static constexpr float kLargest = 65504.0f;
+  static constexpr float kLift = 15.0f;
 };
 
 // Eight e4m3 values (two words) to eight 16-bit ones (four words).
@@ -142,6 +150,13 @@ __device__ __forceinline__ float max_xor16(float x) {
 __device__ __forceinline__ float max_xor32(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The exponent's offset that lifts weights which are at most 2^lazy, relative to
+// their reference.
+template <typename T>
+constexpr float lift(float lazy) {
+  return T::kLift > lazy ? T::kLift - lazy : 0.0f;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
