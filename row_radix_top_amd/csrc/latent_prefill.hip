@@ -32,8 +32,10 @@ namespace rrt {
 // 8192 tokens x 32 heads: 630 us without second parts, 690 with 16 tiles, 870
 // with the keys' of all tiles.
 //
-// A scale of the cache reaches the keys as its power of two alone, which moves
-// no bit of a rope part; the rest of it multiplies the scores.
+// A scale of the cache reaches the keys as a power of two alone, its own or, for
+// fp16, the nearest in 2^-8 .. 2^7, which moves no bit of a rope part and leaves
+// the range that fp16 has for the keys' second parts; the rest of it multiplies the
+// scores.
 // ---------------------------------------------------------------------------
 constexpr int kExpandBlock = 256;
 constexpr int kHead = PAGED_HEAD_DIM;
@@ -58,14 +60,19 @@ __device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, u
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// A cache's scale as a signed power of two and a factor in [1, 2).
+// A cache's scale as what the keys are kept times (a signed power of two: the
+// scale's own, or the nearest that the type holds rope parts with) and what is left
+// of it for the scores, in [1, 2) for the scale's own.
 struct KeyScale {
   float power, rest;
 };
+template <typename T>
 __device__ __forceinline__ KeyScale key_scale(const float* scale) {
-  const uint32_t x = scale == nullptr ? 0x3f800000u : __float_as_uint(scale[0]), e = x >> 23 & 255;
-  if (e == 0 || e == 255) return {__uint_as_float(x), 1.0f};  // zero, subnormal or not finite
-  return {__uint_as_float(x & 0xff800000u), __uint_as_float((x & 0x007fffffu) | 0x3f800000u)};
+  const float x = scale == nullptr ? 1.0f : scale[0], size = fabsf(x);
+  if (!(size > 0.0f && size < INFINITY)) return {x, 1.0f};
+  const int own = __builtin_amdgcn_frexp_expf(size) - 1;
+  const int e = own < T::kKeyLeast ? T::kKeyLeast : own > T::kKeyMost ? T::kKeyMost : own;
+  return {copysignf(ldexpf(1.0f, e), x), ldexpf(size, -e)};
 }
 
 __device__ __forceinline__ int32_t context_of(const PrefillParams& p, int32_t s) {
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
   }
 
   const float by = F8 && a.scale != nullptr ? a.scale[0] : 1.0f;
-  const float key_by = F8 ? key_scale(a.scale).power : 1.0f;
+  const float key_by = F8 ? key_scale<T>(a.scale).power : 1.0f;
   if (keys) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 32 tokens
@@ -419,7 +426,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) q[s][e] = T::pack(T::lo(q[s][e]) * sign, T::hi(q[s][e]) * sign);
   }
-  const float scale = p.scale_log2 != 0.0f ? fabsf(p.scale_log2) * key_scale(a.scale).rest : 1.0f;
+  const float scale = p.scale_log2 != 0.0f ? fabsf(p.scale_log2) * key_scale<T>(a.scale).rest : 1.0f;
 
   // 16 blocks of keys, 8 of rope parts, 16 of values, and 16 of what the keys'
   // rounding left, a quarter of each a wavefront, as they lie.
