@@ -18,8 +18,11 @@
  *   - Strides count elements.  Workspaces are 16-byte aligned, hold nothing
  *     between launches (no initialisation) and must not be shared by launches
  *     that may overlap: give each stream, and each captured graph, its own.
- *     A size is that of the very arguments it was asked for: a call with fewer
- *     rows may be split further and need more.
+ *     A size holds for the arguments it was asked for and for the same ones
+ *     with fewer rows (num_rows; num_tokens, num_seqs), a narrower table, fewer
+ *     chosen positions or a smaller context: one workspace for a server's
+ *     largest step serves its others.  Sizes are host arithmetic; no call
+ *     checks them, as no call is told the workspace's.
  *   - Outputs do not overlap inputs, and the cache is not written while it is
  *     read.
  *

@@ -154,9 +154,13 @@ struct AttnPlan {
   size_t bytes;
 };
 
-int plan_attention(const paged_attention_args* a, bool latent, hipStream_t stream, AttnPlan* out) {
+// reserve: NULL, or receives the bytes of workspace that this launch or one of
+// fewer rows may use.
+int plan_attention(const paged_attention_args* a, bool latent, hipStream_t stream, AttnPlan* out,
+                   size_t* reserve = nullptr) {
   if (int rc = check_attention(a, latent)) return rc;
   std::memset(out, 0, sizeof(*out));
+  if (reserve != nullptr) *reserve = 0;
   if (a->num_rows == 0) return TOPK_OK;
   int dev = 0, cus = 0;
   if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
@@ -190,11 +194,25 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
     out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, p.group_rows, tiles);
   }
   const int64_t longest = chosen ? a->num_chosen : rrt::table_tokens(a->table_width, a->page_size);
-  int64_t most = a->max_splits > 0 ? a->max_splits : parts_for(latent, chosen, units, longest, cus);
-  most = std::max<int64_t>(1, std::min<int64_t>({most, (int64_t)kMostParts, longest / p.least}));
-  p.most = (int32_t)most;
-  out->grid = ceil_div((int64_t)p.groups * most, 8) * 8 * (units / p.groups);  // see work_of
-  out->bytes = most == 1 ? 0 : (size_t)a->num_rows * a->num_heads * most * (a->head_dim * sizeof(float) + sizeof(float2));
+  const int64_t each = units / p.groups;
+  auto most_for = [&](int64_t groups) {
+    const int64_t most = a->max_splits > 0 ? a->max_splits : parts_for(latent, chosen, groups * each, longest, cus);
+    return std::max<int64_t>(1, std::min<int64_t>({most, (int64_t)kMostParts, longest / p.least}));
+  };
+  auto bytes_for = [&](int64_t groups) -> size_t {
+    const int64_t most = most_for(groups);
+    if (most == 1) return 0;
+    return (size_t)(groups * p.group_rows) * a->num_heads * most * (a->head_dim * sizeof(float) + sizeof(float2));
+  };
+  p.most = (int32_t)most_for(p.groups);
+  out->grid = ceil_div((int64_t)p.groups * p.most, 8) * 8 * each;  // see work_of
+  out->bytes = bytes_for(p.groups);
+  if (reserve == nullptr) return TOPK_OK;
+  // Fewer rows may be split into more parts each.  Past two units a CU the rules
+  // give every number of rows as many parts, and more rows need more.
+  *reserve = out->bytes;
+  for (int64_t g = std::min<int64_t>(p.groups - 1, 2 * (int64_t)cus / each + 1); g > 0; --g)
+    *reserve = std::max(*reserve, bytes_for(g));
   return TOPK_OK;
 }
 
@@ -264,9 +282,10 @@ struct PrefillPlan {
   size_t low_at, rope_at, value_at, valid_at, flag_at, part_at, stat_at, bytes;
 };
 
-int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* out) {
+int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* out, size_t* reserve = nullptr) {
   if (int rc = check_prefill(a)) return rc;
   std::memset(out, 0, sizeof(*out));
+  if (reserve != nullptr) *reserve = 0;
   if (a->num_tokens == 0 || a->num_seqs == 0) return TOPK_OK;
   rrt::PrefillParams& p = out->p;
   p.a = *a;
@@ -291,16 +310,28 @@ int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* 
   // 178, 178; 4 of 500 to 1500, 201 x 8 68, 57, 46; 1 of 1024, 5 x 16 48, 39, 33.
   // A part more than fits (3 sequences, 1782 x 24): 256, 263.
   const int64_t longest = std::min<int64_t>(a->context_tokens, rrt::table_tokens(a->table_width, a->page_size));
-  p.parts = 1;
-  if (longest >= 512) {
-    int dev = 0, cus = 0;
+  int dev = 0, cus = 0;
+  if (longest >= 512)
     if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
-    const int64_t units = ceil_div(a->num_tokens, rrt::prefill_rows()) * a->num_heads;
-    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * cus / units, longest / 256, 16}));
-  }
-  const size_t splits = p.parts == 1 ? 0 : (size_t)a->num_tokens * heads * (size_t)p.parts;
+  auto parts_for = [&](int64_t tokens) -> int64_t {
+    const int64_t units = ceil_div(tokens, rrt::prefill_rows()) * a->num_heads;
+    return std::max<int64_t>(1, std::min<int64_t>({2 * cus / units, longest / 256, 16}));
+  };
+  auto splits_for = [&](int64_t tokens) -> size_t {
+    const int64_t parts = parts_for(tokens);
+    return parts == 1 ? 0 : (size_t)tokens * heads * (size_t)parts;
+  };
+  p.parts = (int32_t)parts_for(a->num_tokens);
+  constexpr size_t kSplitBytes = PAGED_HEAD_DIM * sizeof(float) + sizeof(float2);
+  const size_t splits = splits_for(a->num_tokens);
   out->stat_at = out->part_at + splits * PAGED_HEAD_DIM * sizeof(float);
-  out->bytes = out->stat_at + splits * sizeof(float2);
+  out->bytes = out->part_at + splits * kSplitBytes;
+  if (reserve == nullptr) return TOPK_OK;
+  // Fewer rows may be split into more parts each: the most rows of each number
+  // of row tiles, as far as any are split.
+  *reserve = out->bytes;
+  for (int64_t rows = rrt::prefill_rows(); rows < a->num_tokens && parts_for(rows) > 1; rows += rrt::prefill_rows())
+    *reserve = std::max(*reserve, out->part_at + splits_for(rows) * kSplitBytes);
   return TOPK_OK;
 }
 
@@ -375,9 +406,7 @@ int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* par
 int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes) {
   REQUIRE(bytes != nullptr, "null bytes");
   AttnPlan plan;
-  if (int rc = plan_attention(args, false, stream, &plan)) return rc;
-  *bytes = plan.bytes;
-  return TOPK_OK;
+  return plan_attention(args, false, stream, &plan, bytes);
 }
 
 int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream) {
@@ -387,9 +416,7 @@ int paged_attention(const paged_attention_args* args, void* workspace, hipStream
 int latent_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes) {
   REQUIRE(bytes != nullptr, "null bytes");
   AttnPlan plan;
-  if (int rc = plan_attention(args, true, stream, &plan)) return rc;
-  *bytes = plan.bytes;
-  return TOPK_OK;
+  return plan_attention(args, true, stream, &plan, bytes);
 }
 
 int latent_attention(const paged_attention_args* args, void* workspace, hipStream_t stream) {
@@ -399,9 +426,7 @@ int latent_attention(const paged_attention_args* args, void* workspace, hipStrea
 int latent_prefill_workspace_size(const latent_prefill_args* args, hipStream_t stream, size_t* bytes) {
   REQUIRE(bytes != nullptr, "null bytes");
   PrefillPlan plan;
-  if (int rc = plan_prefill(args, stream, &plan)) return rc;
-  *bytes = plan.bytes;
-  return TOPK_OK;
+  return plan_prefill(args, stream, &plan, bytes);
 }
 
 int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t stream) {
