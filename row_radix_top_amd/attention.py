@@ -5,7 +5,8 @@ device memory and streams, every step of an operator runs in the HIP kernels,
 and there is no fallback.
 
 Outputs and workspaces that are not given are allocated by torch on the call's
-stream.  Nothing is differentiable.
+stream.  Nothing is differentiable: where autograd is on, tensors that require
+gradients are refused (call under ``torch.no_grad()``, or detach them).
 """
 
 from __future__ import annotations
@@ -123,6 +124,13 @@ def _on(stream, x):
     return torch.cuda.stream(stream)
 
 
+def _no_gradients(name: str) -> None:
+    """Tensors whose gradients a call would drop without a word are refused;
+    where autograd is off they are taken as they are."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has no gradients: call it under torch.no_grad() or detach its tensors")
+
+
 def _code(x, name: str, cache: bool = False) -> int:
     code = _CODES.get(x.dtype)
     if code is None or (code == _E4M3 and not cache):
@@ -155,6 +163,8 @@ def _scales(x, name: str, dev: int, n: int, code: int):
         raise ValueError(f"{name} belongs to a float8_e4m3fn cache")
     if x.dtype is not torch.float32 or x.get_device() != dev or x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {n} on cuda:{dev}")
+    if x.requires_grad:
+        _no_gradients(name)
     return x.data_ptr()
 
 
@@ -261,6 +271,8 @@ def paged_append(slots, k, v, k_cache, v_cache, *, k_scale=None, v_scale=None, s
     of the same type or float8_e4m3fn, then as x / scale with float32
     [num_kv_heads] scales (None: 1).  No slot may occur twice."""
     load()
+    if k.requires_grad or v.requires_grad or k_cache.requires_grad or v_cache.requires_grad:
+        _no_gradients("paged_append")
     if _elsewhere(k_cache, stream):
         with _on(stream, k_cache):
             return paged_append(slots, k, v, k_cache, v_cache, k_scale=k_scale, v_scale=v_scale)
@@ -286,6 +298,8 @@ def latent_append(slots, latent, rope, cache, *, scale=None, stream=None) -> Non
     [num_tokens, 64] to their slots of cache [num_pages, page_size, latent_dim
     + 64], as paged_append does; scale: float32 [1]."""
     load()
+    if latent.requires_grad or rope.requires_grad or cache.requires_grad:
+        _no_gradients("latent_append")
     if _elsewhere(cache, stream):
         with _on(stream, cache):
             return latent_append(slots, latent, rope, cache, scale=scale)
@@ -365,6 +379,9 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, s
     get zeros and -inf.
     """
     load()
+    if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad
+            or (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
+        _no_gradients("paged_attention")
     if _elsewhere(q, stream):
         with _on(stream, q):
             return paged_attention(q, k_cache, v_cache, block_table, lengths, chosen=chosen,
@@ -391,6 +408,9 @@ def latent_attention(q, cache, block_table, lengths, *, softmax_scale: float, ch
     latent_dim], lse).  Other arguments as for paged_attention; scale:
     float32 [1] of a float8_e4m3fn cache."""
     load()
+    if (q.requires_grad or cache.requires_grad
+            or (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
+        _no_gradients("latent_attention")
     if _elsewhere(q, stream):
         with _on(stream, q):
             return latent_attention(q, cache, block_table, lengths, softmax_scale=softmax_scale, chosen=chosen,
@@ -412,6 +432,9 @@ def latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, *, context_
     latent_dim]; context_tokens: at least the sum of the lengths.  Returns
     (out [num_tokens, num_heads, 128], lse).  See paged_attention.h."""
     load()
+    if (q.requires_grad or cache.requires_grad or w_k.requires_grad or w_v.requires_grad
+            or (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
+        _no_gradients("latent_prefill")
     if _elsewhere(q, stream):
         with _on(stream, q):
             return latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, context_tokens=context_tokens,
