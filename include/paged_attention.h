@@ -198,8 +198,9 @@ int latent_attention(const paged_attention_args* args, void* workspace, hipStrea
  *                  fit gets NaN in out and lse.
  *   out, lse       [num_tokens, num_heads, 128] and [num_tokens, num_heads].
  *   workspace      latent_prefill_workspace_size() bytes: the expanded keys
- *                  and values, 768 bytes a token and head, and the
- *                  partial outputs of split contexts.
+ *                  and values, 512 bytes a token and head and 256 more of a
+ *                  sequence's first 1024 tokens, and the partial outputs of
+ *                  split contexts.
  */
 typedef struct {
   const void* q;

@@ -41,7 +41,7 @@ constexpr int kExpandBlock = 256;
 constexpr int kHead = PAGED_HEAD_DIM;
 constexpr int kRopeDim = PAGED_ROPE_DIM;
 constexpr int kBlock16 = 1024;                              // bytes of a block
-constexpr int kExactTiles = 16, kExactWeights = 4;          // 1024 and 256 tokens
+constexpr int kExactWeights = 4;                            // tiles whose weights come in two parts
 constexpr int kKeyTile = 16 * kBlock16, kRopeTile = 8 * kBlock16, kValueTile = 16 * kBlock16;
 
 using lds_u32x4 = __attribute__((address_space(3))) u32x4;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
   constexpr int PITCH = SL * 2;      // bytes of a slice's row
   __shared__ __align__(1024) char sm[2][ROWS * PITCH];  // tokens, key weights, value weights
   __shared__ int64_t splace[TOK];
-  __shared__ bool sexact[2];
+  __shared__ int32_t slow[2];  // where the tiles' second parts go, -1 where they have none
   const latent_prefill_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -140,12 +140,10 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 
   // Places of the tokens: wavefronts 0 and 1 find a tile's each.
   if (w < 2) {
-    bool exact = false;
     int64_t off = -1;
     int32_t before = 0;
     const int32_t tile = tile0 + w;
     const int32_t s = tile < p.capacity ? sequence_of_tile(p, tile, lane, &before) : -1;
-    exact = s >= 0 && tile - before < kExactTiles;
     if (s >= 0) {
       const int32_t pos = (tile - before) * kCtxTile + lane;
       if (pos < context_of(p, s))
@@ -155,7 +153,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
       if (head == 0 && lane == 0) p.valid[tile] = bits;
     }
     splace[w * 64 + lane] = s < 0 ? -2 : off;
-    if (lane == 0) sexact[w] = exact;
+    if (lane == 0) slow[w] = s >= 0 && tile - before < kExactTiles ? low_tile(p, s, tile - before, tile) : -1;
   }
   __syncthreads();
   const bool real[2] = {splace[0] != -2, splace[64] != -2};
@@ -244,7 +242,9 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 32 tokens
       if (!real[j >> 1]) continue;
-      const int64_t at = ((int64_t)head * p.capacity + tile0 + (j >> 1)) * kKeyTile + (lane & 31) * 16 + half * 8;
+      const int64_t at = ((int64_t)head * p.capacity + tile0 + (j >> 1)) * kKeyTile;
+      const int32_t low = slow[j >> 1];
+      const int64_t low_at = ((int64_t)head * p.low_tiles + low) * kKeyTile;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -253,15 +253,15 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[c] = acc[i][j][e * 4 + c] * key_by;
           const u32x2 high = {T::pack(x[0], x[1]), T::pack(x[2], x[3])};
-          const int64_t to = at + ((j & 1) * 8 + w * 4 + i * 2 + (e >> 1)) * kBlock16 + (e & 1) * 512;
-          *(u32x2*)(p.keys + to) = high;
-          if (!sexact[j >> 1]) continue;
+          const int to = ((j & 1) * 8 + w * 4 + i * 2 + (e >> 1)) * kBlock16 + (e & 1) * 512 + (lane & 31) * 16 + half * 8;
+          *(u32x2*)(p.keys + at + to) = high;
+          if (low < 0) continue;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {  // what the rounding left; nothing of what left the type's range
             const float h = c & 1 ? T::hi(high[c >> 1]) : T::lo(high[c >> 1]);
             x[c] = fabsf(h) <= T::kLargest ? x[c] - h : 0.0f;
           }
-          *(u32x2*)(p.lows + to) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+          *(u32x2*)(p.lows + low_at + to) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
         }
     }
   } else if (real[w & 1]) {
@@ -430,9 +430,8 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 
   // 16 blocks of keys, 8 of rope parts, 16 of values, and 16 of what the keys'
   // rounding left, a quarter of each a wavefront, as they lie.
-  const int64_t key_at = ((int64_t)head * p.capacity + tile0) * kKeyTile + w * kBlock16;
-  const char* kp = p.keys + key_at;
-  const char* lp = p.lows + key_at;
+  const char* kp = p.keys + ((int64_t)head * p.capacity + tile0) * kKeyTile + w * kBlock16;
+  const char* lp = p.lows + ((int64_t)head * p.low_tiles + low_tile(p, seq, 0, tile0)) * kKeyTile + w * kBlock16;
   const char* rp = p.ropes + (int64_t)tile0 * kRopeTile + w * kBlock16;
   const char* vp = p.values + ((int64_t)head * p.capacity + tile0) * kValueTile + w * kBlock16;
   const uint32_t lane16 = (uint32_t)lane * 16;

@@ -299,7 +299,8 @@ int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* 
   const size_t tiles = (size_t)capacity, heads = (size_t)a->num_heads;
   const size_t tile_bytes = (size_t)rrt::kCtxTile * PAGED_HEAD_DIM * 2;
   out->low_at = heads * tiles * tile_bytes;
-  out->rope_at = out->low_at + heads * tiles * tile_bytes;
+  p.low_tiles = (int32_t)std::min<int64_t>(capacity, (int64_t)rrt::kExactTiles * a->num_seqs);
+  out->rope_at = out->low_at + heads * (size_t)p.low_tiles * tile_bytes;
   out->value_at = out->rope_at + tiles * rrt::kCtxTile * PAGED_ROPE_DIM * 2;
   out->valid_at = out->value_at + heads * tiles * tile_bytes;
   out->flag_at = out->valid_at + tiles * sizeof(uint64_t);

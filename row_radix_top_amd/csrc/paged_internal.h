@@ -121,11 +121,12 @@ struct AttnParams {
 // The expanded form works on tiles of kCtxTile context tokens; a sequence
 // has ceil(length / kCtxTile) of them, after those of the sequences before it.
 constexpr int32_t kCtxTile = 64;
+constexpr int32_t kExactTiles = 16;  // of a sequence, whose keys are kept in two parts
 
 struct PrefillParams {
   latent_prefill_args a;
   char* keys;       // [heads][capacity] key tiles, fragment order (128 dims, 16 KB)
-  char* lows;       // as keys: what their rounding left, of each sequence's first tiles
+  char* lows;       // [heads][low_tiles], as keys: what their rounding left, of each sequence's first tiles
   char* ropes;      // [capacity] rope tiles, fragment order (8 KB)
   char* values;     // [heads][capacity] value tiles, fragment order (16 KB)
   uint64_t* valid;  // [capacity]: which of a tile's tokens are in the cache
@@ -135,8 +136,15 @@ struct PrefillParams {
   float scale_log2;
   int32_t parts;      // of a row tile's context, at most
   int32_t capacity;   // tiles of the workspace
+  int32_t low_tiles;  // of second parts: kExactTiles a sequence, or every tile if those are fewer
   int32_t row_tiles;  // query tiles of a head that the grid covers
 };
+
+// Where the second parts of a tile (the local-th of sequence seq) lie among
+// those of a head.
+RRT_HD int32_t low_tile(const PrefillParams& p, int32_t seq, int32_t local, int32_t tile) {
+  return p.low_tiles < p.capacity ? seq * kExactTiles + local : tile;
+}
 
 // Kernel lookup: nullptr if there is no such instance.
 const void* layout_kernel_ptr();

@@ -88,6 +88,14 @@ def test_a_prefill_size_holds_for_smaller_chunks(heads):
             most = need
 
 
+def test_a_long_context_reserves_second_parts_for_its_first_tokens_alone():
+    """A head: keys and values of 512 bytes a token, 256 more of the first 1024 tokens, a flag a tile, the one row's
+    partial outputs of 128 values and two statistics in at most 16 parts.  All heads: rope parts and a mask a tile."""
+    tokens, tiles, heads = 131072, 131072 // 64 + 1, 128
+    need = _size("latent_prefill", _prefill(context_tokens=tokens, num_heads=heads, num_seqs=1, num_tokens=1))
+    assert need <= heads * (tiles * 64 * 512 + 1024 * 256 + tiles * 4 + 16 * 520) + tiles * (64 * 128 + 8) + 16
+
+
 def _cases():
     """Of each operator: a large batch and smaller ones that are split further."""
     rng = np.random.default_rng(1)
@@ -101,7 +109,8 @@ def _cases():
                              LatentCase([890], heads=70, dim=256, store="float8_e4m3fn", seed=3)],
         "latent_prefill": [PrefillCase([600, 900], [600, 800], heads=4, seed=1),
                            PrefillCase([700, 90], [3, 90], heads=4, seed=2),
-                           PrefillCase([1300], [2], heads=4, store="float8_e4m3fn", seed=3)],
+                           PrefillCase([1300], [2], heads=4, store="float8_e4m3fn", seed=3),
+                           PrefillCase([2500, 40, 1700], [2, 5, 3], heads=3, seed=4)],
     }
 
 
@@ -127,11 +136,12 @@ def _need(c):
     return need
 
 
-@pytest.mark.parametrize("entry", ["paged_attention", "latent_attention", "latent_prefill"])
-def test_sizes_of_a_workspace(entry):
+@pytest.mark.parametrize("entry,case", [("paged_attention", 1), ("latent_attention", 1), ("latent_prefill", 1),
+                                        ("latent_prefill", 3)])
+def test_sizes_of_a_workspace(entry, case):
     """Exactly the size that is asked for will do, all ones before the call; a byte less is refused."""
     import torch
-    c = _cases()[entry][1]
+    c = _cases()[entry][case]
     need = _need(c)
     assert need > 0
     exact = torch.full((need + 64,), 0xff, dtype=torch.uint8, device="cuda")
