@@ -201,6 +201,12 @@ int latent_attention(const paged_attention_args* args, void* workspace, hipStrea
  *                  and values, 512 bytes a token and head and 256 more of a
  *                  sequence's first 1024 tokens, and the partial outputs of
  *                  split contexts.
+ *
+ * Keys and values are kept in q's type, the keys of a sequence's first 1024
+ * tokens to twice its bits.  A row whose weight lies on one key behind those has
+ * a log-sum-exp off by up to u * softmax_scale * sum |q k| (u: half a step of the
+ * type); with many keys alike in weight it is within 4e-6.  In fp16 an expanded
+ * key or value past 65504 is an infinity for the rows that see it.
  */
 typedef struct {
   const void* q;

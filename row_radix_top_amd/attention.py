@@ -376,7 +376,9 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, s
     float32 [num_kv_heads] scales (None: 1); head_dim 64 or 128.  block_table:
     int32 [num_sequences, width].  lengths: int32 [num_rows] or [batch,
     next_n].  softmax_scale: head_dim ** -0.5 if None.  Rows that see nothing
-    get zeros and -inf.
+    get zeros and -inf.  workspace: a contiguous tensor for split rows' parts,
+    which holds nothing between calls; one that is large enough for a batch is
+    for the same call with fewer rows (None: a new one).
     """
     load()
     if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad
@@ -430,7 +432,8 @@ def latent_prefill(q, cache, block_table, starts, lengths, w_k, w_v, *, context_
     the paged cache.  starts: int32 [num_seqs + 1], lengths: int32 [num_seqs],
     both as paged_layout gives and takes them; w_k, w_v: [num_heads, 128,
     latent_dim]; context_tokens: at least the sum of the lengths.  Returns
-    (out [num_tokens, num_heads, 128], lse).  See paged_attention.h."""
+    (out [num_tokens, num_heads, 128], lse).  How keys and values are rounded:
+    latent_prefill in paged_attention.h."""
     load()
     if (q.requires_grad or cache.requires_grad or w_k.requires_grad or w_v.requires_grad
             or (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):

@@ -6,9 +6,9 @@
 namespace rrt {
 
 // ---------------------------------------------------------------------------
-// Two kernels (and a join where few rows share out their contexts).  `expand` forms k_h = W_k,h c and v_h = W_v,h c for every
-// context token and head (2 DC 256 flop each) and leaves them in the workspace
-// in fragment order: 1 KB blocks that are, lane by lane, the operands that the
+// Two kernels (and a join where few rows share out their contexts).  `expand`
+// forms k_h = W_k,h c and v_h = W_v,h c for every context token and head (2 DC
+// 256 flop each) and leaves them in the workspace in fragment order: 1 KB blocks that are, lane by lane, the operands that the
 // attention's matrix instructions take.  `prefill` streams them through LDS
 // with plain linear copies, and no operand needs a shuffle, a transpose or a
 // swizzle there.
@@ -20,17 +20,22 @@ namespace rrt {
 //     holds after S^T = K Q^T, so the weights go from one product into the
 //     next without leaving the lane.
 // The expanded keys and values are rounded to the 16-bit type, as a program
-// that keeps them would; that is the operator's own rounding beside those of
-// the weights and the output.  A row that sees n tokens averages their keys'
-// roundings away: what is left in its log-sum-exp falls as 1 / sqrt(n), from
-// 1e-3 of it at one token to 4e-6 at 2048 (bf16).  The keys of a sequence's
-// first kExactTiles tiles therefore come with what their rounding left, as a
-// second 16-bit number, and score with both (twice the bits, for rows of few
-// tokens all that they see).  The weights of the first kExactWeights tiles are
-// taken in two parts too: an output of few tokens is off by 1.35 times its own
-// rounding so, 1.55 times without.
-// 8192 tokens x 32 heads: 630 us without second parts, 690 with 16 tiles, 870
-// with the keys' of all tiles.
+// that keeps them would (one past fp16's range is an infinity); that is the
+// operator's own rounding beside those of the weights and the output.  It moves
+// a score by at most u sum |q k| over the 128 formed dims, u half a step of the
+// type.  A row of many tokens with scores alike averages that away: what is left
+// in its log-sum-exp falls as 1 / sqrt(n), from 1e-3 of it at one token to 4e-6 at
+// 2048 (bf16).  The keys of a sequence's first kExactTiles tiles therefore come
+// with what their rounding left, as a second 16-bit number, and score with both
+// (twice the bits, for rows of few tokens all that they see).  A key behind them
+// that outweighs a row's others is averaged with nothing: the log-sum-exp is
+// then off by up to 8e-3 at a score of 20 in bf16 and 5e-4 in fp16, against 2e-5
+// among the first.  The weights of the first kExactWeights tiles are taken in
+// two parts too: an output of few tokens is off by 1.35 times its own rounding
+// so, 1.55 times without.
+// 8192 tokens x 32 heads, side by side: 634 us without second parts, 680 with
+// those of 16 tiles' keys and 700 with the weights' (as built), 729 with 32
+// tiles' keys, 872 with all.
 //
 // A scale of the cache reaches the keys as a power of two alone, its own or, for
 // fp16, the nearest in 2^-8 .. 2^7, which moves no bit of a rope part and leaves
@@ -323,13 +328,15 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // last few need (keys past a row's end masked, values that are not finite kept
 // from rows that do not see them) costs registers, and the copies and spills
 // that came with it cost the loop a wait for memory on every tile (790 us
-// against 630 for 8192 tokens x 32 heads).
+// against 690 for 8192 tokens x 32 heads, both without second parts).  The nine
+// registers that spill still lie around that last path, none in this loop.
 //
-// Those 630 us are 1.09 PFLOP/s.  The matrix units are busy 61 % of the time at
-// the 1.7 GHz that the power limit leaves under this load; every fragment that
-// LDS gives feeds one matrix instruction, so its reads take as long as those.
-// Longer rings of reads, both token blocks' chains in turn and wave priorities
-// changed nothing.
+// 8192 tokens x 32 heads take 700 us, 0.98 PFLOP/s, at the 1.7 GHz that the
+// power limit leaves under this load.  While a CU is at work its matrix units
+// are busy 65 % of the time and its LDS 33 %; a wavefront waits for its turn to
+// issue 47 % of the time and for loads or barriers 16 %.  So it is the two
+// wavefronts of a SIMD taking turns, not one full unit: longer rings of reads,
+// both token blocks' chains in turn and wave priorities changed nothing.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;
 constexpr int kLeastTiles = 4;  // of a part of a split context
@@ -408,9 +415,8 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   if (part >= parts) return;
   const int32_t chunk = (tiles + parts - 1) / parts;
   const int32_t begin = part * chunk < tiles ? part * chunk : tiles, stop = tiles - begin < chunk ? tiles : begin + chunk;
-  // Positions that all rows of the wavefront see, and that any of them does.
+  // Positions that any row of the wavefront sees.
   const int32_t wfirst = row0 + w * 32, wlast = wfirst + 31 < count - 1 ? wfirst + 31 : count - 1;
-  const int32_t all_see = wfirst < count ? ctx - count + wfirst + 1 : 0;
   const int32_t any_see = wfirst < count ? ctx - count + wlast + 1 : 0;
 
   u32x4 q[12];

@@ -30,9 +30,10 @@ namespace rrt {
 // stay fp32.
 //
 // Bound by reading the cache.  64 rows of 1 to 32768 positions, 64 heads on 8,
-// bf16: 747 us, 5.5 TB/s where a plain read reaches 6.4; 4 rows of 8192: 24.5
-// us, 5.5 TB/s; 64 rows of 2048 chosen positions, 40 heads on 4, e4m3: 31 to
-// 33 us, 4.2 TB/s of scattered 512-byte rows.
+// bf16: 744 us, 5.6 TB/s where a plain read reaches 6.4 (e4m3: 397, 5.2); 4 rows
+// of 8192: 24.6 us, 5.5 TB/s; 64 rows of 2048 chosen positions, 40 heads on 4:
+// 47.7 us, 5.7 TB/s of scattered rows, e4m3 34, 4.0 TB/s; 32 x 2 rows of 16384
+// positions, 64 heads on 4: 215 us, 5.0 TB/s, e4m3 114, 4.7.
 // ---------------------------------------------------------------------------
 constexpr int kAttnBlock = 256;
 constexpr int kTok = 32;  // tokens of a wavefront's tile
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
     };
     // Ragged tiles come last and in a loop of their own: the copies of the
     // sums that they need cost the others registers and spills (32 x 2 rows of
-    // 16384 positions, 64 heads on 4: 329 us against 229, e4m3 240 against 129).
+    // 16384 positions, 64 heads on 4, a call: 329 us against 229, e4m3 240 against 129).
     if constexpr (MODE == kRows) {
       while (more && t + kTok <= shortest) step(Flag<false>{});
       while (more) step(Flag<true>{});

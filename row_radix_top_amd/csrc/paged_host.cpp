@@ -310,6 +310,10 @@ int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* 
   // and of 256: 1 sequence of 8192, 34 rows x 8 heads 201, 66, 56; 1071 x 16 236,
   // 178, 178; 4 of 500 to 1500, 201 x 8 68, 57, 46; 1 of 1024, 5 x 16 48, 39, 33.
   // A part more than fits (3 sequences, 1782 x 24): 256, 263.
+  // Rows are counted as if they filled their tiles, since how many sequences are
+  // more than padding is not known here.  64 sequences of a row each are split
+  // although their tiles fill the chip (8 heads, 4096 tokens: 1050 us, 1025 in one
+  // part; 256 of up to 4096, 4 heads: 1240, 1135; 16 of 8192: 535, 568).
   const int64_t longest = std::min<int64_t>(a->context_tokens, rrt::table_tokens(a->table_width, a->page_size));
   int dev = 0, cus = 0;
   if (longest >= 512)
