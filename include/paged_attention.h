@@ -198,15 +198,15 @@ int latent_attention(const paged_attention_args* args, void* workspace, hipStrea
  *                  fit gets NaN in out and lse.
  *   out, lse       [num_tokens, num_heads, 128] and [num_tokens, num_heads].
  *   workspace      latent_prefill_workspace_size() bytes: the expanded keys
- *                  and values, 512 bytes a token and head and 256 more of a
+ *                  and values, 514 bytes a token and head and 256 more of a
  *                  sequence's first 1024 tokens, and the partial outputs of
  *                  split contexts.
  *
- * Keys and values are kept in q's type, the keys of a sequence's first 1024
- * tokens to twice its bits.  A row whose weight lies on one key behind those has
- * a log-sum-exp off by up to u * softmax_scale * sum |q k| (u: half a step of the
- * type); with many keys alike in weight it is within 4e-6.  In fp16 an expanded
- * key or value past 65504 is an infinity for the rows that see it.
+ * Values are kept in q's type; in fp16 one past 65504 is an infinity for the
+ * rows that see it.  Keys are kept to fp16's 11 bits at any size, those of a
+ * sequence's first 1024 tokens to twice as many.  A row whose weight lies on one
+ * key behind those has a log-sum-exp off by up to 2^-11 softmax_scale sum |q k|;
+ * with many keys alike in weight it is within 1e-6.
  */
 typedef struct {
   const void* q;

@@ -1,6 +1,8 @@
 // The expanded form of latent attention: keys and values of every head formed
 // from the latent vectors of the context, then causal attention over them.
 
+#include <type_traits>
+
 #include "paged_device.hpp"
 
 namespace rrt {
@@ -8,10 +10,10 @@ namespace rrt {
 // ---------------------------------------------------------------------------
 // Two kernels (and a join where few rows share out their contexts).  `expand`
 // forms k_h = W_k,h c and v_h = W_v,h c for every context token and head (2 DC
-// 256 flop each) and leaves them in the workspace in fragment order: 1 KB blocks that are, lane by lane, the operands that the
-// attention's matrix instructions take.  `prefill` streams them through LDS
-// with plain linear copies, and no operand needs a shuffle, a transpose or a
-// swizzle there.
+// 256 flop each) and leaves them in the workspace in fragment order: 1 KB blocks
+// that are, lane by lane, the operands that the attention's matrix instructions
+// take.  `prefill` streams them through LDS with plain linear copies, and no
+// operand needs a shuffle, a transpose or a swizzle there.
 //
 // A context tile is 64 tokens.  With tb = token / 32, half = lane / 32:
 //   key block (tb, s):   lane holds token tb*32 + lane % 32, dims s*16 + half*8 .. +8
@@ -19,28 +21,28 @@ namespace rrt {
 //     tb*32 + ks*16 + half*4 + {0..3, 8..11}: the tokens whose weights the lane
 //     holds after S^T = K Q^T, so the weights go from one product into the
 //     next without leaving the lane.
-// The expanded keys and values are rounded to the 16-bit type, as a program
-// that keeps them would (one past fp16's range is an infinity); that is the
-// operator's own rounding beside those of the weights and the output.  It moves
-// a score by at most u sum |q k| over the 128 formed dims, u half a step of the
-// type.  A row of many tokens with scores alike averages that away: what is left
-// in its log-sum-exp falls as 1 / sqrt(n), from 1e-3 of it at one token to 4e-6 at
-// 2048 (bf16).  The keys of a sequence's first kExactTiles tiles therefore come
-// with what their rounding left, as a second 16-bit number, and score with both
-// (twice the bits, for rows of few tokens all that they see).  A key behind them
-// that outweighs a row's others is averaged with nothing: the log-sum-exp is
-// then off by up to 8e-3 at a score of 20 in bf16 and 5e-4 in fp16, against 2e-5
-// among the first.  The weights of the first kExactWeights tiles are taken in
-// two parts too: an output of few tokens is off by 1.35 times its own rounding
-// so, 1.55 times without.
-// 8192 tokens x 32 heads, side by side: 634 us without second parts, 680 with
-// those of 16 tiles' keys and 700 with the weights' (as built), 729 with 32
-// tiles' keys, 872 with all.
+// Expanded values are rounded to the 16-bit type, as a program that keeps them
+// would (one past fp16's range is an infinity).  Keys, which a score of 20 takes
+// twenty times as they are off, are rounded to fp16 for bf16 too, at the same
+// rate and eight times closer, and with them rope parts and queries.  The range
+// is that of fp32 all the same: a token's key, its rope part and a row's queries
+// are kept times powers of two wherever their size asks for it (keep_exp), which
+// costs tiles of ordinary sizes nothing.
+// A key's rounding moves a score by at most u sum |q k| over the 128 formed dims,
+// u = 2^-11.  A row of many tokens with scores alike averages that away, as
+// 1 / sqrt(n), so the keys of a sequence's first kExactTiles tiles come with what
+// their rounding left, as a second fp16 number, and score with both (for rows of
+// few tokens all that they see).  A key behind them that outweighs a row's
+// others is averaged with nothing: the log-sum-exp is then off by up to 1.2e-3
+// at a score of 20, against 6e-6 among the first.  The weights of the first
+// kExactWeights tiles are taken in two parts too: an output of few tokens is off
+// by 1.35 times its own rounding so, 1.55 times without.
+// 8192 tokens x 32 heads, bf16, attention side by side: 703 us with bf16 keys, 721
+// with fp16 (what fp16's products draw of the power limit).  With bf16
+// keys it was 634 us without second parts, 680 with those of 16 tiles' keys,
+// 729 with 32 tiles', 872 with all.
 //
-// A scale of the cache reaches the keys as a power of two alone, its own or, for
-// fp16, the nearest in 2^-8 .. 2^7, which moves no bit of a rope part and leaves
-// the range that fp16 has for the keys' second parts; the rest of it multiplies the
-// scores.
+// A scale of the cache multiplies the scores, not the keys.
 // ---------------------------------------------------------------------------
 constexpr int kExpandBlock = 256;
 constexpr int kHead = PAGED_HEAD_DIM;
@@ -65,19 +67,16 @@ __device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, u
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// A cache's scale as what the keys are kept times (a signed power of two: the
-// scale's own, or the nearest that the type holds rope parts with) and what is left
-// of it for the scores, in [1, 2) for the scale's own.
-struct KeyScale {
-  float power, rest;
-};
-template <typename T>
-__device__ __forceinline__ KeyScale key_scale(const float* scale) {
-  const float x = scale == nullptr ? 1.0f : scale[0], size = fabsf(x);
-  if (!(size > 0.0f && size < INFINITY)) return {x, 1.0f};
-  const int own = __builtin_amdgcn_frexp_expf(size) - 1;
-  const int e = own < T::kKeyLeast ? T::kKeyLeast : own > T::kKeyMost ? T::kKeyMost : own;
-  return {copysignf(ldexpf(1.0f, e), x), ldexpf(size, -e)};
+// keep_exp: a token's key (or rope part) is kept in fp16 times 2^-this, given its
+// largest magnitude: 0 for the ordinary (and for what is not finite), else what
+// makes the largest as large as fp16 takes.  A dim below 2^-30 of its token's
+// largest loses bits, and is lost in a score's fp32 sum unless the queries are as
+// uneven the other way.
+constexpr int kKeepLeast = -112, kKeepMost = 113;
+__device__ __forceinline__ int keep_exp(float most) {
+  if (!(most > 0.0f && most < INFINITY) || (most >= 0.015625f && most <= 32768.0f)) return 0;
+  const int e = __builtin_amdgcn_frexp_expf(most) - 15;
+  return e < kKeepLeast ? kKeepLeast : e > kKeepMost ? kKeepMost : e;
 }
 
 __device__ __forceinline__ int32_t context_of(const PrefillParams& p, int32_t s) {
@@ -136,6 +135,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
   constexpr int PITCH = SL * 2;      // bytes of a slice's row
   __shared__ __align__(1024) char sm[2][ROWS * PITCH];  // tokens, key weights, value weights
   __shared__ int64_t splace[TOK];
+  __shared__ float smost[2][TOK];  // each token's largest magnitude in the key dims of a wavefront
   __shared__ int32_t slow[2];  // where the tiles' second parts go, -1 where they have none
   const latent_prefill_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -241,14 +241,36 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
     if (k + 1 < NS) store(b ^ 1);
   }
 
-  const float by = F8 && a.scale != nullptr ? a.scale[0] : 1.0f;
-  const float key_by = F8 ? key_scale<T>(a.scale).power : 1.0f;
   if (keys) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(acc[i][j][e]));
+      most = max_xor32(most);
+      if (half == 0) smost[w][j * 32 + lane] = most;
+    }
+  }
+  __syncthreads();
+  if (keys) {
+    bool uneven = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 32 tokens
       if (!real[j >> 1]) continue;
       const int64_t at = ((int64_t)head * p.capacity + tile0 + (j >> 1)) * kKeyTile;
       const int32_t low = slow[j >> 1];
+      const int e2 = keep_exp(fmaxf(smost[0][j * 32 + (lane & 31)], smost[1][j * 32 + (lane & 31)]));
+      const float key_by = ldexpf(1.0f, -e2);
+      if (w == 0) {
+        const int64_t tile_at = (int64_t)head * p.capacity + tile0 + (j >> 1);
+        const bool any = __builtin_amdgcn_ballot_w64(e2 != 0) != 0;
+        if (j & 1) uneven = uneven || any;
+        else uneven = any;
+        if (half == 0) p.key_exps[tile_at * kCtxTile + (j & 1) * 32 + lane] = (int16_t)e2;
+        if ((j & 1) && lane == 0) ((uint16_t*)(p.flags + tile_at))[1] = uneven ? 1 : 0;
+      }
       const int64_t low_at = ((int64_t)head * p.low_tiles + low) * kKeyTile;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -257,19 +279,20 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
           float x[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[c] = acc[i][j][e * 4 + c] * key_by;
-          const u32x2 high = {T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+          const u32x2 high = {Fp16::pack(x[0], x[1]), Fp16::pack(x[2], x[3])};
           const int to = ((j & 1) * 8 + w * 4 + i * 2 + (e >> 1)) * kBlock16 + (e & 1) * 512 + (lane & 31) * 16 + half * 8;
           *(u32x2*)(p.keys + at + to) = high;
           if (low < 0) continue;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {  // what the rounding left; nothing of what left the type's range
-            const float h = c & 1 ? T::hi(high[c >> 1]) : T::lo(high[c >> 1]);
-            x[c] = fabsf(h) <= T::kLargest ? x[c] - h : 0.0f;
+          for (int c = 0; c < 4; ++c) {  // what the rounding left; nothing of what is not finite
+            const float h = c & 1 ? Fp16::hi(high[c >> 1]) : Fp16::lo(high[c >> 1]);
+            x[c] = fabsf(h) <= Fp16::kLargest ? x[c] - h : 0.0f;
           }
-          *(u32x2*)(p.lows + low_at + to) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
+          *(u32x2*)(p.lows + low_at + to) = u32x2{Fp16::pack(x[0], x[1]), Fp16::pack(x[2], x[3])};
         }
     }
   } else if (real[w & 1]) {
+    const float by = F8 && a.scale != nullptr ? a.scale[0] : 1.0f;
     const int32_t tile = tile0 + (w & 1);
     char* to = p.values + ((int64_t)head * p.capacity + tile) * kValueTile + lane * 16;
     bool bad = false;
@@ -289,27 +312,36 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
               u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
         }
     const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
-    if (lane == 0) p.flags[(int64_t)head * p.capacity + tile] = any != 0 ? 1u : 0u;
+    if (lane == 0) ((uint16_t*)(p.flags + (int64_t)head * p.capacity + tile))[0] = any != 0 ? 1 : 0;
   }
   // Rope parts, copied once for all heads: wavefront w takes 32 tokens.
-  if (head == 0) {
-    const int32_t rtile = tile0 + (w >> 1);
-    if (real[w >> 1]) {
-      const int64_t off = splace[w * 32 + (lane & 31)];
-      const char* from = cache + (off < 0 ? 0 : off) * SZ + DC * SZ;
-      char* to = p.ropes + (int64_t)rtile * kRopeTile + (w & 1) * (4 * kBlock16) + lane * 16;
+  if (head == 0 && real[w >> 1]) {
+    const int64_t rtile = tile0 + (w >> 1);
+    const int64_t off = splace[w * 32 + (lane & 31)];
+    const char* from = cache + (off < 0 ? 0 : off) * SZ + DC * SZ;
+    u32x4 x[4];
+    float most = 0.0f;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        u32x4 x;
-        if constexpr (F8) {
-          x = widen<T>(*(const u32x2*)(from + s * 16 + half * 8));
+    for (int s = 0; s < 4; ++s) {
+      if constexpr (F8)
+        x[s] = widen<T>(*(const u32x2*)(from + s * 16 + half * 8));
+      else
+        x[s] = *(const u32x4*)(from + s * 32 + half * 16);
+      if (off < 0) x[s] = u32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = T::pack(T::lo(x[i]) * key_by, T::hi(x[i]) * key_by);
-        } else {
-          x = *(const u32x4*)(from + s * 32 + half * 16);
-        }
-        *(u32x4*)(to + s * kBlock16) = off < 0 ? u32x4{0, 0, 0, 0} : x;
-      }
+      for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(T::lo(x[s][i])), fabsf(T::hi(x[s][i]))));
+    }
+    const int e2 = keep_exp(max_xor32(most));
+    const float rope_by = ldexpf(1.0f, -e2);
+    const uint64_t uneven = __builtin_amdgcn_ballot_w64(e2 != 0);
+    if (lane == 0) ((uint16_t*)(p.rope_flags + rtile))[w & 1] = uneven != 0 ? 1 : 0;
+    if (half == 0) p.rope_exps[rtile * kCtxTile + (w & 1) * 32 + lane] = (int16_t)e2;
+    char* to = p.ropes + rtile * kRopeTile + (w & 1) * (4 * kBlock16) + lane * 16;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[s][i] = Fp16::pack(T::lo(x[s][i]) * rope_by, T::hi(x[s][i]) * rope_by);
+      *(u32x4*)(to + s * kBlock16) = x[s];
     }
   }
 }
@@ -331,7 +363,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // against 690 for 8192 tokens x 32 heads, both without second parts).  The nine
 // registers that spill still lie around that last path, none in this loop.
 //
-// 8192 tokens x 32 heads take 700 us, 0.98 PFLOP/s, at the 1.7 GHz that the
+// 8192 tokens x 32 heads take 705 us, 0.97 PFLOP/s, at the 1.7 GHz that the
 // power limit leaves under this load.  While a CU is at work its matrix units
 // are busy 65 % of the time and its LDS 33 %; a wavefront waits for its turn to
 // issue 47 % of the time and for loads or barriers 16 %.  So it is the two
@@ -424,15 +456,38 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     const char* qp = (const char*)a.q + 2 * ((int64_t)(start + (real ? j : row0)) * a.q_row_stride + (int64_t)head * a.q_head_stride);
 #pragma unroll
     for (int s = 0; s < 12; ++s) q[s] = *(const u32x4*)(qp + s * 32 + half * 16);
-    // The scale's sign goes into the queries, so that the largest product has
-    // the largest score (and products are 0 where the scale is).
-    const float sign = p.scale_log2 > 0.0f ? 1.0f : p.scale_log2 < 0.0f ? -1.0f : 0.0f;
+  }
+  // The scale's sign goes into the queries, so that the largest product has the
+  // largest score (and products are 0 where the scale is).  A bf16 row goes to
+  // fp16 times 2^-qe, which makes it as large as fp16 takes: exact for what lies
+  // within 2^-31 of its largest.  Its rope part has a power of its own where that
+  // would cost it bits or the others: 2^-(qe + qgap).
+  const float total = p.scale_log2 * (a.scale == nullptr ? 1.0f : a.scale[0]);
+  const float sign = total < 0.0f ? -1.0f : total == 0.0f ? 0.0f : 1.0f;
+  const float scale = total == 0.0f ? 1.0f : fabsf(total);
+  int qe = 0, qgap = 0;
+  if constexpr (!std::is_same_v<T, Fp16>) {
+    float most[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < 12; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[s][e] = T::pack(T::lo(q[s][e]) * sign, T::hi(q[s][e]) * sign);
+      for (int e = 0; e < 4; ++e) most[s >> 3] = fmaxf(most[s >> 3], fmaxf(fabsf(T::lo(q[s][e])), fabsf(T::hi(q[s][e]))));
+    most[0] = max_xor32(most[0]), most[1] = max_xor32(most[1]);
+    const bool ordinary = total != 0.0f && most[0] < INFINITY && most[1] < INFINITY;
+    if (ordinary && fmaxf(most[0], most[1]) > 0.0f) {
+      const int en = __builtin_amdgcn_frexp_expf(most[0]) - 15, er = __builtin_amdgcn_frexp_expf(most[1]) - 15;
+      const bool one = most[0] == 0.0f || most[1] == 0.0f || (en - er <= 12 && er - en <= 12);
+      qe = one ? __builtin_amdgcn_frexp_expf(fmaxf(most[0], most[1])) - 15 : en;
+      qgap = one ? 0 : er - en;
+    }
   }
-  const float scale = p.scale_log2 != 0.0f ? fabsf(p.scale_log2) * key_scale<T>(a.scale).rest : 1.0f;
+#pragma unroll
+  for (int s = 0; s < 12; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int by = s < 8 ? -qe : -(qe + qgap);
+      q[s][e] = Fp16::pack(ldexpf(T::lo(q[s][e]) * sign, by), ldexpf(T::hi(q[s][e]) * sign, by));
+    }
 
   // 16 blocks of keys, 8 of rope parts, 16 of values, and 16 of what the keys'
   // rounding left, a quarter of each a wavefront, as they lie.
@@ -463,6 +518,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   scalar_u64* valid_of = (scalar_u64*)(p.valid + tile0);
   using scalar_u32 = const __attribute__((address_space(4))) uint32_t;
   scalar_u32* flag_of = (scalar_u32*)(p.flags + (int64_t)head * p.capacity + tile0);
+  scalar_u32* rope_flag_of = (scalar_u32*)(p.rope_flags + tile0);
 
   float ref = -INFINITY, sum = 0.0f;  // base-2 logarithm; of this lane's tokens
   f32x16 o[4];
@@ -471,11 +527,23 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   f32x16 s[2];
   u32x4 pw[4];
 
-  auto scores = [&](bool exact) {
+  // Powers of two that the keys (rope parts) of the lane's tokens e*8 + half*4 .. +4
+  // of a block of 32 are kept smaller by.
+  auto powers = [&](const int16_t* of_tile, int tb, int e, int* x) __attribute__((always_inline)) {
+    const u32x2 two = *(const u32x2*)(of_tile + tb * 32 + e * 8 + half * 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = c & 1 ? (int)two[c >> 1] >> 16 : (int)(int16_t)(two[c >> 1] & 0xffffu);
+  };
+  // uneven: some token of tile i or some row has a power of its own.  Rope parts
+  // come first and are then brought level with the keys; scores then take the
+  // scale alone, without 2^qe.
+  auto scores = [&](bool exact, int32_t i, bool uneven) __attribute__((always_inline)) {
+    const int16_t* ke = p.key_exps + ((int64_t)head * p.capacity + tile0 + i) * kCtxTile;
+    const int16_t* re = p.rope_exps + ((int64_t)tile0 + i) * kCtxTile;
     const uint32_t base = lds_at(&sk[0]) + lane16;
     auto key = [&](int n) {  // n: token block * 12 + step
       const int tb = n / 12, k = n % 12;
-      return lds_read16(base + (k < 8 ? (tb * 8 + k) * kBlock16 : kKeyTile + (tb * 4 + k - 8) * kBlock16));
+      return lds_read16(base + (k < 4 ? kKeyTile + (tb * 4 + k) * kBlock16 : (tb * 8 + k - 4) * kBlock16));
     };
     u32x4 ring[kAheadBlocks];
 #pragma unroll
@@ -485,10 +553,31 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
     for (int n = 0; n < 24; ++n) {
       if (n + kAheadBlocks - 1 < 24) ring[(n + kAheadBlocks - 1) % kAheadBlocks] = key(n + kAheadBlocks - 1);
-      s[n / 12] = T::mfma32(ring[n % kAheadBlocks], q[n % 12], s[n / 12]);
+      if (uneven && n % 12 == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int kx[4], rx[4];
+          powers(ke, n / 12, e, kx), powers(re, n / 12, e, rx);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[n / 12][e * 4 + c] = ldexpf(s[n / 12][e * 4 + c], rx[c] - kx[c] + qgap);
+        }
+      }
+      s[n / 12] = Fp16::mfma32(ring[n % kAheadBlocks], q[(n + 8) % 12], s[n / 12]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (!exact) return;
+    auto finish = [&] {
+      if (!uneven) return;
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int kx[4];
+          powers(ke, tb, e, kx);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[tb][e * 4 + c] = ldexpf(s[tb][e * 4 + c], kx[c] + qe);
+        }
+    };
+    if (!exact) return finish();
     auto low = [&](int n) { return lds_read16(base + kKeyTile + kRopeTile + n * kBlock16); };
 #pragma unroll
     for (int n = 0; n < kAheadBlocks - 1; ++n) ring[n] = low(n);
@@ -496,9 +585,10 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
       if (n + kAheadBlocks - 1 < 16) ring[(n + kAheadBlocks - 1) % kAheadBlocks] = low(n + kAheadBlocks - 1);
-      s[n / 8] = T::mfma32(ring[n % kAheadBlocks], q[n % 8], s[n / 8]);
+      s[n / 8] = Fp16::mfma32(ring[n % kAheadBlocks], q[n % 8], s[n / 8]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    finish();
   };
   // Leaves out tokens that are not in the cache or past `left` (of the tile).
   auto mask = [&](uint64_t valid, int32_t left) {
@@ -513,11 +603,11 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
       }
     }
   };
-  auto weights = [&] {
+  auto weights = [&](float by_tile) {
     float top = s[0][0];
 #pragma unroll
     for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
-    top = max_xor32(top) * scale;
+    top = max_xor32(top) * by_tile;
     if (__builtin_amdgcn_ballot_w64(top > ref + kLazyStep) != 0) {
       const float m = fmaxf(ref, top);
       const float by = m == ref ? 1.0f : exp2_fast(ref - m);
@@ -533,7 +623,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], scale, r));
+        x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], by_tile, r));
         s[k >> 1][(k & 1) * 8 + e] = x[e];
         part[e & 3] += x[e];
       }
@@ -568,47 +658,57 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     }
   };
 
-  // Tiles that every row of the workgroup sees whole.
+  // Tiles that every row of the workgroup sees whole, where all of them and the
+  // rows are of ordinary size.
   const int32_t first_sees = ctx - count + row0 + 1;
   const int32_t all_whole = first_sees > 0 && fits ? first_sees / kCtxTile : 0;
-  const int32_t whole = all_whole < begin ? begin : all_whole < stop ? all_whole : stop;
+  int32_t whole = all_whole < begin ? begin : all_whole < stop ? all_whole : stop;
   uint64_t valid = 0;
   if (begin < stop) {
     issue_keys(begin);
     issue_values(begin);
     valid = valid_of[begin];
   }
+  const bool uneven_rows = __builtin_amdgcn_ballot_w64(qgap != 0) != 0;
+  bool uneven_tiles = uneven_rows;
+  for (int32_t i = begin + lane; i < whole; i += 64)
+    uneven_tiles = uneven_tiles || (p.flags[(int64_t)head * p.capacity + tile0 + i] >> 16) != 0 || p.rope_flags[tile0 + i] != 0;
+  if (__syncthreads_or(uneven_tiles ? 1 : 0)) whole = begin;
+  const float row_scale = ldexpf(scale, qe);
   for (int32_t i = begin; i < whole; ++i) {
     wait_loads();
     __syncthreads();
     if (i + 1 < stop) issue_values(i + 1);
     const uint64_t now = valid;
     if (i + 1 < stop) valid = valid_of[i + 1];
-    scores(i < kExactTiles);
+    scores(i < kExactTiles, i, false);
     __syncthreads();  // the keys are read
     if (i + 1 < stop) issue_keys(i + 1);
     if (now != ~0ull) mask(now, kCtxTile);
-    weights();
+    weights(row_scale);
     // The second parts of weights meet finite values only.
-    values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights && flag_of[i] == 0);
+    values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights && (flag_of[i] & 0xffffu) == 0);
   }
-  // Tiles that some row sees in part or not at all.
+  // Tiles that some row sees in part or not at all, and those out of the ordinary.
   for (int32_t i = whole; i < stop; ++i) {
     wait_loads();
     __syncthreads();
     if (i + 1 < stop) issue_values(i + 1);
     const uint64_t now = valid;
     if (i + 1 < stop) valid = valid_of[i + 1];
+    const uint32_t flags = flag_of[i];
+    const bool odd = (flags & 0xffffu) != 0;  // some value is not finite
+    const bool uneven = uneven_rows || (flags >> 16) != 0 || rope_flag_of[i] != 0;
     const int32_t t0 = i * kCtxTile;
     const bool any = t0 < any_see;  // else nothing here for this wavefront
-    if (any) scores(i < kExactTiles);
+    if (any) scores(i < kExactTiles, i, uneven);
     __syncthreads();
     if (i + 1 < stop) issue_keys(i + 1);
     if (!any) continue;
     const uint32_t vbase = lds_at(&sv[i & 1][0]) + lane16;
     mask(now, sees - t0);
-    weights();
-    if (flag_of[i] == 0) {
+    weights(uneven ? scale : row_scale);
+    if (!odd) {
       values(vbase, i < kExactWeights);
       continue;
     }

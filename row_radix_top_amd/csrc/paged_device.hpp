@@ -30,10 +30,6 @@ using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 // 1e-3 of the output, and were zeros beside a weight of 1.  2^15 is the most
 // that fp16 takes; bf16 has the exponents of fp32 and needs none.  Sums are of
 // lifted weights too, so an output does not change and a log-sum-exp by kLift.
-// kKeyLeast, kKeyMost: powers of two that expanded keys of an e4m3 cache may be
-// kept times.  An e4m3 value (2^-9 to 448) times any of them is exact in the
-// type; fp16 would take 2^-15, but a product near 1 then keeps 10 bits in all, and
-// with 2^-8 still 17.
 struct Bf16 {
   using elem = __bf16;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -56,7 +52,6 @@ struct Bf16 {
   }
   static constexpr float kLargest = 3.3895313892515355e38f;
   static constexpr float kLift = 0.0f;
-  static constexpr int kKeyLeast = -100, kKeyMost = 100;
 };
 
 struct Fp16 {
@@ -81,7 +76,6 @@ struct Fp16 {
   }
   static constexpr float kLargest = 65504.0f;
   static constexpr float kLift = 15.0f;
-  static constexpr int kKeyLeast = -8, kKeyMost = 7;
 };
 
 // Eight e4m3 values (two words) to eight 16-bit ones (four words).

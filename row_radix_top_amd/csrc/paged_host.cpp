@@ -279,7 +279,8 @@ int check_prefill(const latent_prefill_args* a) {
 
 struct PrefillPlan {
   rrt::PrefillParams p;
-  size_t low_at, rope_at, value_at, valid_at, flag_at, part_at, stat_at, bytes;
+  size_t low_at, rope_at, value_at, valid_at, flag_at, rope_flag_at, key_exp_at, rope_exp_at, part_at,
+      stat_at, bytes;
 };
 
 int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* out, size_t* reserve = nullptr) {
@@ -304,7 +305,10 @@ int plan_prefill(const latent_prefill_args* a, hipStream_t stream, PrefillPlan* 
   out->value_at = out->rope_at + tiles * rrt::kCtxTile * PAGED_ROPE_DIM * 2;
   out->valid_at = out->value_at + heads * tiles * tile_bytes;
   out->flag_at = out->valid_at + tiles * sizeof(uint64_t);
-  out->part_at = (out->flag_at + heads * tiles * sizeof(uint32_t) + 15) / 16 * 16;
+  out->rope_flag_at = out->flag_at + heads * tiles * sizeof(uint32_t);
+  out->key_exp_at = (out->rope_flag_at + tiles * sizeof(uint32_t) + 15) / 16 * 16;
+  out->rope_exp_at = out->key_exp_at + heads * tiles * rrt::kCtxTile * sizeof(int16_t);
+  out->part_at = out->rope_exp_at + tiles * rrt::kCtxTile * sizeof(int16_t);
   // Few row tiles: their contexts are shared out, as far as two workgroups a
   // CU go, and joined by a third launch.  us without, in parts of 1024 tokens
   // and of 256: 1 sequence of 8192, 34 rows x 8 heads 201, 66, 56; 1071 x 16 236,
@@ -452,6 +456,9 @@ int latent_prefill(const latent_prefill_args* args, void* workspace, hipStream_t
   p.values = ws + plan.value_at;
   p.valid = reinterpret_cast<uint64_t*>(ws + plan.valid_at);
   p.flags = reinterpret_cast<uint32_t*>(ws + plan.flag_at);
+  p.rope_flags = reinterpret_cast<uint32_t*>(ws + plan.rope_flag_at);
+  p.key_exps = reinterpret_cast<int16_t*>(ws + plan.key_exp_at);
+  p.rope_exps = reinterpret_cast<int16_t*>(ws + plan.rope_exp_at);
   if (int rc = launch(rrt::expand_kernel_ptr(args->dtype, args->store, args->latent_dim),
                       ceil_div(p.capacity, 2) * args->num_heads, 256, &p, stream, "expansion of latent vectors"))
     return rc;

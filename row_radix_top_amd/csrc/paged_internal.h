@@ -125,12 +125,15 @@ constexpr int32_t kExactTiles = 16;  // of a sequence, whose keys are kept in tw
 
 struct PrefillParams {
   latent_prefill_args a;
-  char* keys;       // [heads][capacity] key tiles, fragment order (128 dims, 16 KB)
+  char* keys;       // [heads][capacity] key tiles, fragment order (128 dims, 16 KB), in fp16
   char* lows;       // [heads][low_tiles], as keys: what their rounding left, of each sequence's first tiles
-  char* ropes;      // [capacity] rope tiles, fragment order (8 KB)
+  char* ropes;      // [capacity] rope tiles, fragment order (8 KB), in fp16
   char* values;     // [heads][capacity] value tiles, fragment order (16 KB)
   uint64_t* valid;  // [capacity]: which of a tile's tokens are in the cache
-  uint32_t* flags;  // [heads][capacity]: 1 where a value is not finite
+  uint32_t* flags;  // [heads][capacity]: low half 1 where a value is not finite, high half where a key's power is not 0
+  uint32_t* rope_flags;  // [capacity]: where a rope part's power is not 0, a half for 32 tokens each
+  int16_t* key_exps;     // [heads][capacity][64]: a flagged tile's keys are kept times 2^-this
+  int16_t* rope_exps;    // [capacity][64]: rope parts are kept times 2^-this
   float* part_out;    // split contexts: [rows][heads][parts][128], not divided by the sum,
   float2* part_stat;  // and (maximum, sum) of each
   float scale_log2;

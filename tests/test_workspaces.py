@@ -89,11 +89,12 @@ def test_a_prefill_size_holds_for_smaller_chunks(heads):
 
 
 def test_a_long_context_reserves_second_parts_for_its_first_tokens_alone():
-    """A head: keys and values of 512 bytes a token, 256 more of the first 1024 tokens, a flag a tile, the one row's
-    partial outputs of 128 values and two statistics in at most 16 parts.  All heads: rope parts and a mask a tile."""
+    """A head: keys and values of 512 bytes a token and a power of two, 256 more of the first 1024 tokens, a flag a
+    tile, the one row's partial outputs of 128 values and two statistics in at most 16 parts.  All heads: rope parts
+    and their powers, a mask and a flag a tile."""
     tokens, tiles, heads = 131072, 131072 // 64 + 1, 128
     need = _size("latent_prefill", _prefill(context_tokens=tokens, num_heads=heads, num_seqs=1, num_tokens=1))
-    assert need <= heads * (tiles * 64 * 512 + 1024 * 256 + tiles * 4 + 16 * 520) + tiles * (64 * 128 + 8) + 16
+    assert need <= heads * (tiles * 64 * 514 + 1024 * 256 + tiles * 4 + 16 * 520) + tiles * (64 * 130 + 12) + 32
 
 
 def _cases():
