@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 constexpr int kRows = 128;
 constexpr int kLeastTiles = 4;  // of a part of a split context
 constexpr float kLazyStep = 8.0f;
+constexpr float kFar = 1048576.0f;
 constexpr int kAheadBlocks = 4;
 
 // A tile of query rows: its sequence, its place within the sequence's chunk
@@ -616,6 +617,14 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= by;
     }
+    // Differences to the reference come unrounded out of one fma, but the reference
+    // is a rounded product: far out, where half a step of it is a factor, products
+    // are rounded first, so that the largest is the reference.
+    float by = by_tile;
+    if (__builtin_amdgcn_ballot_w64(fabsf(ref) > kFar && ref != -INFINITY) != 0) {
+      s[0] *= by_tile, s[1] *= by_tile;
+      by = 1.0f;
+    }
     const float r = ref == -INFINITY ? 0.0f : lift<T>(kLazyStep) - ref;
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], by_tile, r));
+        x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], by, r));
         s[k >> 1][(k & 1) * 8 + e] = x[e];
         part[e & 3] += x[e];
       }
@@ -674,7 +683,7 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
   for (int32_t i = begin + lane; i < whole; i += 64)
     uneven_tiles = uneven_tiles || (p.flags[(int64_t)head * p.capacity + tile0 + i] >> 16) != 0 || p.rope_flags[tile0 + i] != 0;
   if (__syncthreads_or(uneven_tiles ? 1 : 0)) whole = begin;
-  const float row_scale = ldexpf(scale, qe);
+  const float row_scale = fmaxf(ldexpf(scale, qe), 1.17549435e-38f);  // masked scores times 0 are no numbers
   for (int32_t i = begin; i < whole; ++i) {
     wait_loads();
     __syncthreads();
