@@ -360,15 +360,16 @@ __global__ void __launch_bounds__(kExpandBlock, 2) expand_kernel(PrefillParams p
 // last few need (keys past a row's end masked, values that are not finite kept
 // from rows that do not see them) costs registers, and the copies and spills
 // that came with it cost the loop a wait for memory on every tile (790 us
-// against 690 for 8192 tokens x 32 heads, both without second parts).  The nine
+// against 690 for 8192 tokens x 32 heads, both without second parts).  The dozen
 // registers that spill still lie around that last path, none in this loop.
 //
-// 8192 tokens x 32 heads take 705 us, 0.97 PFLOP/s, at the 1.7 GHz that the
-// power limit leaves under this load.  While a CU is at work its matrix units
-// are busy 65 % of the time and its LDS 33 %; a wavefront waits for its turn to
-// issue 47 % of the time and for loads or barriers 16 %.  So it is the two
-// wavefronts of a SIMD taking turns, not one full unit: longer rings of reads,
-// both token blocks' chains in turn and wave priorities changed nothing.
+// 8192 tokens x 32 heads take 709 us (766 on a hot card), 0.97 PFLOP/s, at the
+// 1.65 to 1.8 GHz that the power limit leaves under this load.  While a CU is at
+// work its matrix units are busy 63 % of the time and its LDS 32 %; a wavefront
+// waits for its turn to issue 45 % of the time and for loads or barriers 18 %.
+// So it is the two wavefronts of a SIMD taking turns, not one full unit: longer
+// rings of reads, both token blocks' chains in turn and wave priorities changed
+// nothing.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;
 constexpr int kLeastTiles = 4;  // of a part of a split context

@@ -133,3 +133,28 @@ def test_a_large_token_does_not_cost_its_neighbours(dtype, store):
         paged_ref.check(lse[rows].double().cpu().numpy(), elog[rows], tlog[rows], "their lse")
     if large < 2.0 ** 10:
         c.check("all rows")
+
+
+@pytest.mark.parametrize("keys,ropes", [(0, 0), (40, 30), (-30, 20)])
+def test_other_sizes_in_split_contexts_and_beside_what_is_not_finite(keys, ropes):
+    """Contexts that are shared out, some of their tokens of other sizes than the rest; and a later token
+    that is not finite, which earlier rows do not see."""
+    import torch
+
+    def sized(c):
+        c.wk *= 2.0 ** keys
+        c.c[::2, :, c.dim:] *= 2.0 ** ropes  # every other page
+        c.q[:, :, :HEAD] *= 2.0 ** -keys
+        return c
+
+    sized(Case([3000, 1200], [2, 3], heads=2, seed=51)).check("split, other sizes")
+    c = sized(Case([260], [200], heads=2, seed=52))
+    bad = np.zeros(c.pages * c.page_size, dtype=bool)
+    bad[c.slots(0)[[150, 259]]] = True
+    c.poison(bad)
+    out, lse = c.run()
+    exp, elog, tol, tlog = c.expected()
+    k = 150 - 60
+    paged_ref.check(out[:k].double().cpu().numpy(), exp[:k], tol[:k], "earlier rows")
+    paged_ref.check(lse[:k].double().cpu().numpy(), elog[:k], tlog[:k], "earlier rows' lse")
+    assert bool(out[k:].isnan().all())
