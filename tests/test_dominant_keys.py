@@ -158,3 +158,17 @@ def test_other_sizes_in_split_contexts_and_beside_what_is_not_finite(keys, ropes
     paged_ref.check(out[:k].double().cpu().numpy(), exp[:k], tol[:k], "earlier rows")
     paged_ref.check(lse[:k].double().cpu().numpy(), elog[:k], tlog[:k], "earlier rows' lse")
     assert bool(out[k:].isnan().all())
+
+
+def test_rows_and_tokens_of_other_sizes_among_the_ordinary():
+    """Some rows and some tokens alone take the other way through the tiles."""
+    c = Case([700, 130], [300, 130], heads=2, seed=61)
+    c.q[5, :, HEAD:] *= 2.0 ** -20
+    c.q[200, :, :HEAD] *= 2.0 ** -25
+    c.q[201] *= 2.0 ** 60
+    c.check("rows")
+    c.q[201] *= 2.0 ** -60
+    flat = c.c.view(-1, c.dim + ROPE)
+    for token, by in ((70, 2.0 ** -12), (300, 2.0 ** 9), (511, 2.0 ** -30)):
+        flat[int(c.slots(0)[token])] *= by
+    c.check("rows and tokens")
