@@ -3,7 +3,7 @@
 
 #include <type_traits>
 
-#include "paged_device.hpp"
+#include "lds_device.hpp"
 
 namespace rrt {
 
@@ -51,22 +51,6 @@ constexpr int kRopeDim = PAGED_ROPE_DIM;
 constexpr int kBlock16 = 1024;                              // bytes of a block
 constexpr int kExactWeights = 4;                            // tiles whose weights come in two parts
 constexpr int kKeyTile = 16 * kBlock16, kRopeTile = 8 * kBlock16, kValueTile = 16 * kBlock16;
-
-using lds_u32x4 = __attribute__((address_space(3))) u32x4;
-
-__device__ __forceinline__ uint32_t lds_at(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
-}
-__device__ __forceinline__ u32x4 lds_read16(uint32_t at) { return *(lds_u32x4*)at; }
-// 16 bytes from each lane's address to LDS at `to` (wave uniform) + 16 x lane.
-// No register is written: wait_loads() alone waits for it.
-__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory", "m0");
-}
-__device__ __forceinline__ void load_to_lds(const char* from, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(from) : "memory", "m0");
-}
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // keep_exp: a token's key (or rope part) is kept in fp16 times 2^-this, given its
 // largest magnitude: 0 for the ordinary, 2^-8 to 2^15 (and for what is not finite),

@@ -8,48 +8,9 @@
 #include <cstdio>
 #include <cstring>
 
-#include "paged_internal.h"
-#include "topk_internal.h"
+#include "paged_host.hpp"
 
 namespace {
-
-using rrt::set_error;
-
-// Every check that fails names the argument; nothing has been launched then.
-#define REQUIRE(cond, text) \
-  do {                      \
-    if (!(cond)) return set_error(TOPK_EINVAL, text); \
-  } while (0)
-
-bool aligned(const void* p, uintptr_t by) { return reinterpret_cast<uintptr_t>(p) % by == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int launch(const void* fn, int64_t grid, int block, void* params, hipStream_t stream, const char* what) {
-  char buf[192];
-  if (fn == nullptr) {
-    std::snprintf(buf, sizeof(buf), "%s: no kernel instance for these arguments", what);
-    return set_error(TOPK_EINVAL, buf);
-  }
-  if (grid > INT32_MAX) {
-    std::snprintf(buf, sizeof(buf), "%s: %lld workgroups are more than one launch takes", what, (long long)grid);
-    return set_error(TOPK_EINVAL, buf);
-  }
-  void* args[] = {params};
-  hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)block), args, 0, stream);
-  if (e == hipSuccess) e = hipGetLastError();
-  if (e != hipSuccess) {
-    std::snprintf(buf, sizeof(buf), "%s: launch failed: %s", what, hipGetErrorString(e));
-    return set_error(TOPK_ELAUNCH, buf);
-  }
-  return TOPK_OK;
-}
-
-int check_types(paged_dtype dtype, paged_dtype store) {
-  REQUIRE(dtype == PAGED_BF16 || dtype == PAGED_FP16, "dtype must be PAGED_BF16 or PAGED_FP16");
-  REQUIRE(store == dtype || store == PAGED_E4M3, "store must be dtype or PAGED_E4M3");
-  return TOPK_OK;
-}
 
 // ---------------------------------------------------------------------------
 // Attention
