@@ -120,6 +120,107 @@ int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* par
                  int32_t page_size, int32_t num_pages, paged_dtype dtype, paged_dtype store, hipStream_t stream);
 
 /*
+ * Sequences that share pages.  paged_fork makes the rows of a new batch go on
+ * from those of the last one, paged_copy copies their last pages, paged_free
+ * finds what no row holds, paged_compact moves pages together.  A row of
+ * length n holds the first ceil(n / page_size) entries of its table row; pages
+ * that several rows hold lie at the same place in each (as paged_fork leaves
+ * them).
+ *
+ * paged_fork -- block table of a new batch: row i goes on from row parents[i]
+ * (samples of one prompt, beams, a prefix that is in the cache; a row that
+ * nothing goes on from is given up).
+ *
+ *   block_table, lengths   of the last batch, num_seqs rows; lengths are
+ *                clamped to [0, table_width * page_size] and to 2^30.
+ *   parents      int32 [num_rows]; outside [0, num_seqs): an empty row.
+ *   keep         NULL, or int32 [num_rows]: row i keeps the first keep[i]
+ *                tokens (clamped to [0, the parent's length]).
+ *   free_pages   int32 [num_free], pages to hand out, in order.
+ *   out_table    int32, row i at out_table + i * out_stride, table_width
+ *                entries: the parent's for the tokens kept, then -1.  A last
+ *                page that is not full, as row i will write to it, is the
+ *                parent's only if no other row of the new batch holds that
+ *                page full and no row before i holds it too; else the next
+ *                free page (-1 once they run out).
+ *   out_lengths  int32 [num_rows], the tokens kept.
+ *   src, dst, tokens   int32 [num_rows]: for a row with a new last page that
+ *                page's number before and now and how many of its tokens count,
+ *                as paged_copy takes them; -1, -1, 0 for all others.
+ *   pages        int32 [1]: pages that the call needs; more than num_free
+ *                means that the free list ran out.
+ *
+ * The outputs do not overlap the inputs.  A table entry below 0 is no page: it
+ * is passed on, never copied.
+ */
+int paged_fork(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lengths,
+               int32_t num_seqs, const int32_t* parents, const int32_t* keep, int32_t num_rows,
+               const int32_t* free_pages, int32_t num_free, int32_t page_size, int32_t* out_table,
+               int64_t out_stride, int32_t* out_lengths, int32_t* src, int32_t* dst, int32_t* tokens, int32_t* pages,
+               hipStream_t stream);
+
+/* One cache of a copy, strides in bytes: page p at data + p * page_stride, its
+ * `tokens` tokens token_stride apart, each `outer` rows of `width` bytes
+ * outer_stride apart (a cache without tokens: tokens = 1). */
+typedef struct {
+  void* data;
+  int64_t page_stride, token_stride, outer_stride;
+  int32_t tokens, outer, width;
+} paged_pages;
+
+/*
+ * paged_copy -- pages src[i] to pages dst[i] of every cache, in one launch for
+ * each PAGED_COPY_CACHES of them.
+ *
+ *   src, dst   int32 [num_pairs]; a pair with either outside [0, num_pages),
+ *              or with both alike, is left out.  No page is the dst of two
+ *              pairs, or of one and the src of another.
+ *   tokens     NULL: whole pages.  Else int32 [num_pairs]: the first tokens[i]
+ *              tokens of pair i's page, clamped to [0, the cache's].
+ *   caches     num_caches of them, in host memory.
+ */
+#define PAGED_COPY_CACHES 32
+int paged_copy(const int32_t* src, const int32_t* dst, const int32_t* tokens, int32_t num_pairs,
+               const paged_pages* caches, int32_t num_caches, int32_t num_pages, hipStream_t stream);
+
+/*
+ * paged_free -- the pages that no row holds, from the block table alone: rows
+ * that ended have length 0.
+ *
+ *   free_pages   int32 [num_pages], receives them in ascending order, -1 past
+ *                the last.
+ *   refs         int32 [num_pages], receives how many table entries hold each.
+ *   count        int32 [1], receives how many are free.
+ *   workspace    paged_free_workspace_size() bytes.
+ *
+ * Entries outside [0, num_pages) are no pages.
+ */
+int paged_free_workspace_size(int32_t num_pages, size_t* bytes);
+int paged_free(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lengths,
+               int32_t num_seqs, int32_t page_size, int32_t num_pages, int32_t* free_pages, int32_t* refs,
+               int32_t* count, void* workspace, hipStream_t stream);
+
+/*
+ * paged_compact -- moves held pages to free ones with lower numbers: the k-th
+ * held page from `limit` on goes to the k-th free page below it, for as long as
+ * there are both.  limit -1: the number of held pages, so that they end up as
+ * the first of the pool.
+ *
+ *   out_table    int32, row s at out_table + s * out_stride: the table with the
+ *                pages' new numbers; may be block_table itself, with its
+ *                stride.  Entries past a row's tokens are passed on.
+ *   src, dst     int32 [num_pages / 2]: the moves, as paged_copy takes them, -1
+ *                past the last.  A page that moves is no dst.
+ *   moves, live  int32 [1]: how many pages move, and how many are held.
+ *   workspace    paged_compact_workspace_size() bytes.
+ */
+int paged_compact_workspace_size(int32_t num_pages, size_t* bytes);
+int paged_compact(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lengths,
+                  int32_t num_seqs, int32_t page_size, int32_t num_pages, int32_t limit, int32_t* out_table,
+                  int64_t out_stride, int32_t* src, int32_t* dst, int32_t* moves, int32_t* live, void* workspace,
+                  hipStream_t stream);
+
+/*
  * paged_attention -- attention of single tokens over a paged cache of keys
  * and values: out = softmax(softmax_scale * q K^T) V for each row and head.
  *

@@ -39,3 +39,12 @@ from .attention import (  # noqa: F401
     paged_attention,
     paged_layout,
 )
+from .pages import (  # noqa: F401
+    Compact,
+    Fork,
+    Pages,
+    paged_compact,
+    paged_copy,
+    paged_fork,
+    paged_free,
+)

@@ -26,7 +26,8 @@ MAX_SPLITS = 128
 EXPORTED = (
     "paged_layout", "paged_append", "paged_attention", "paged_attention_workspace_size", "latent_attention",
     "latent_attention_workspace_size", "latent_prefill", "latent_prefill_workspace_size",
-    "paged_debug_place", "paged_debug_split",
+    "paged_debug_place", "paged_debug_split", "paged_fork", "paged_copy", "paged_free", "paged_free_workspace_size",
+    "paged_compact", "paged_compact_workspace_size",
 )
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -86,6 +87,14 @@ def load() -> ctypes.CDLL:
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp, _vp]
             getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args), _vp,
                                                                ctypes.POINTER(ctypes.c_size_t)]
+        size = ctypes.POINTER(ctypes.c_size_t)
+        lib.paged_fork.argtypes = [_vp, _i64, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _vp,
+                                   _vp, _vp, _vp]
+        lib.paged_copy.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _vp]
+        lib.paged_free.argtypes = [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
+        lib.paged_compact.argtypes = [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                      _vp]
+        lib.paged_free_workspace_size.argtypes = lib.paged_compact_workspace_size.argtypes = [_i32, size]
         for name in EXPORTED:
             getattr(lib, name).restype = ctypes.c_int
         lib.paged_debug_place.argtypes = [_vp, _i32, _i32, _i64, _i64, _i32]

@@ -104,6 +104,40 @@ struct AppendParams {
   int64_t num_slots;
 };
 
+constexpr int kPagesBlock = 256;  // threads of a workgroup of the page operators
+
+struct ForkParams {
+  const int32_t *table, *lengths, *parents, *keep, *free_pages;
+  int32_t *out_table, *out_lengths, *src, *dst, *tokens, *pages;
+  int64_t table_stride, out_stride;
+  int32_t table_width, num_seqs, num_rows, num_free, page_size;
+  int32_t rows_each;  // rows of a workgroup of the second launch
+  Divisor page;       // by page_size
+};
+
+struct CopyParams {
+  const int32_t *src, *dst, *tokens;
+  int32_t num_pages, num_caches;
+  int32_t pieces;  // workgroups of a page and cache
+  paged_pages cache[PAGED_COPY_CACHES];
+  Divisor row[PAGED_COPY_CACHES], each[PAGED_COPY_CACHES];  // by a row's steps, and a token's
+};
+
+struct PoolParams {
+  const int32_t *table, *lengths;
+  int32_t* out_table;
+  uint32_t* bits;  // a page each: held or not; zeros past num_pages
+  int32_t* rank;   // compact: the move of a page from the limit on, or -1
+  int32_t *refs, *free_pages, *count;      // free
+  int32_t *src, *dst, *moves, *live;       // compact
+  int64_t table_stride, out_stride;
+  int32_t table_width, num_seqs, page_size, num_pages, limit;
+  int32_t words;       // of bits
+  int32_t row_pieces;  // workgroups of a table row
+  Divisor page;
+};
+enum { kPoolClear, kPoolHold, kPoolFree, kPoolMoves, kPoolRename };
+
 struct AttnParams {
   paged_attention_args a;
   float* part_out;     // [rows, heads, most, head_dim], unnormalised
@@ -152,6 +186,9 @@ RRT_HD int32_t low_tile(const PrefillParams& p, int32_t seq, int32_t local, int3
 // Kernel lookup: nullptr if there is no such instance.
 const void* layout_kernel_ptr();
 const void* append_kernel_ptr(int dtype, int store, bool wide);
+const void* fork_kernel_ptr(bool write);
+const void* copy_kernel_ptr(int bytes);
+const void* pool_kernel_ptr(int step);
 const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int rows, int tiles);
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads);
 const void* join_kernel_ptr(int dtype, int head_dim, bool many);

@@ -1,0 +1,272 @@
+// Pages that sequences share: forks, copies, what is free, and moves that
+// bring the held pages together.
+
+#include "paged_device.hpp"
+
+namespace rrt {
+
+constexpr int kBlock = kPagesBlock;
+
+// The sum of x over the workgroup, on all threads; s: a word a wavefront.
+__device__ __forceinline__ int32_t block_sum(int32_t x, int32_t* s) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  __syncthreads();
+  int32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < kBlock / 64; ++i) sum += s[i];
+  __syncthreads();
+  return sum;
+}
+
+__device__ __forceinline__ int32_t pages_of(int32_t n, const Divisor& page) {
+  return n == 0 ? 0 : (int32_t)divide((uint32_t)n - 1u, page) + 1;
+}
+
+// ---------------------------------------------------------------------------
+// Fork.  Row i keeps m tokens of its parent p.  Its last page, if m is no
+// multiple of the page size, is the one that the row will write to, so it has
+// to be its own: a copy, if another row of the batch holds the page full or a
+// row before i holds it in part.  A shared page lies at the same place of every
+// row, so the question is one column of the parents' table rows.
+//
+// Two launches: `mark` answers it, a wavefront a row and the other rows over its
+// lanes (src and tokens receive the answer); `write` gives the marked rows their
+// free pages, in order (each workgroup counts the marks before its rows by
+// itself), and writes the table.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int32_t kept(const ForkParams& p, int64_t most, int32_t i, int32_t* parent) {
+  const int32_t q = p.parents[i];
+  *parent = q;
+  if ((uint32_t)q >= (uint32_t)p.num_seqs) return 0;
+  const int32_t n = clamp_to(p.lengths[q], most);
+  return p.keep == nullptr ? n : clamp_to(p.keep[i], n);
+}
+
+__global__ void __launch_bounds__(kBlock) fork_mark_kernel(ForkParams p) {
+  const int lane = threadIdx.x & 63;
+  const int32_t i = (int32_t)(blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6));
+  if (i >= p.num_rows) return;
+  const int64_t most = table_tokens(p.table_width, p.page_size);
+  int32_t parent;
+  const int32_t m = kept(p, most, i, &parent);
+  const int32_t j = (int32_t)divide((uint32_t)m, p.page), part = m - j * p.page_size;
+  const int32_t last = part != 0 ? p.table[(int64_t)parent * p.table_stride + j] : -1;
+  bool copy = false;
+  if (last >= 0) {
+    for (int32_t r0 = 0; r0 < p.num_rows; r0 += 64) {
+      const int32_t r = r0 + lane;
+      bool other = false;
+      if (r < p.num_rows && r != i) {
+        int32_t q;
+        const int32_t n = kept(p, most, r, &q);
+        const int32_t left = n - j * p.page_size;  // tokens that it holds from that page on
+        if (left > 0 && (left >= p.page_size || r < i)) other = p.table[(int64_t)q * p.table_stride + j] == last;
+      }
+      if (__builtin_amdgcn_ballot_w64(other) != 0) {
+        copy = true;
+        break;
+      }
+    }
+  }
+  if (lane == 0) {
+    p.out_lengths[i] = m;
+    p.src[i] = copy ? last : -1;
+    p.tokens[i] = copy ? part : 0;
+  }
+}
+
+__global__ void __launch_bounds__(kBlock) fork_write_kernel(ForkParams p) {
+  __shared__ int32_t sums[kBlock / 64];
+  const int tid = threadIdx.x;
+  const int32_t first = (int32_t)blockIdx.x * p.rows_each;
+  const int32_t stop = p.num_rows - first < p.rows_each ? p.num_rows : first + p.rows_each;
+  int32_t before = 0;
+  for (int32_t i = tid; i < first; i += kBlock) before += p.src[i] >= 0 ? 1 : 0;
+  before = block_sum(before, sums);
+  for (int32_t i = first; i < stop; ++i) {
+    const int32_t m = p.out_lengths[i], parent = p.parents[i];
+    const bool copy = p.src[i] >= 0;
+    const int32_t got = copy && before < p.num_free ? p.free_pages[before] : -1;
+    if (copy) ++before;
+    if (tid == 0) p.dst[i] = got;
+    const int32_t need = pages_of(m, p.page);
+    const int32_t* from = p.table + (int64_t)(need > 0 ? parent : 0) * p.table_stride;
+    int32_t* to = p.out_table + (int64_t)i * p.out_stride;
+    for (int32_t j = tid; j < p.table_width; j += kBlock)
+      to[j] = j >= need ? -1 : copy && j == need - 1 ? got : from[j];
+  }
+  if (stop == p.num_rows && tid == 0) p.pages[0] = before;
+}
+
+// ---------------------------------------------------------------------------
+// Copy.  A workgroup takes a piece of one page of one cache; V bytes a thread
+// and step.  Bound by its bytes.
+// ---------------------------------------------------------------------------
+template <int V>
+struct Piece;
+template <>
+struct Piece<16> {
+  using type = u32x4;
+};
+template <>
+struct Piece<4> {
+  using type = uint32_t;
+};
+template <>
+struct Piece<1> {
+  using type = uint8_t;
+};
+
+template <int V>
+__global__ void __launch_bounds__(kBlock) copy_kernel(CopyParams p) {
+  using type = typename Piece<V>::type;
+  const uint32_t b = blockIdx.x;
+  const uint32_t piece = b % (uint32_t)p.pieces, c = b / (uint32_t)p.pieces % (uint32_t)p.num_caches;
+  const uint32_t i = b / (uint32_t)p.pieces / (uint32_t)p.num_caches;
+  const int32_t from = p.src[i], to = p.dst[i];
+  if ((uint32_t)from >= (uint32_t)p.num_pages || (uint32_t)to >= (uint32_t)p.num_pages || from == to) return;
+  const paged_pages& q = p.cache[c];
+  const int32_t tokens = p.tokens == nullptr ? q.tokens : clamp_to(p.tokens[i], q.tokens);
+  const Divisor row = p.row[c], each = p.each[c];  // steps of a row, and of a token
+  const uint32_t items = (uint32_t)tokens * each.by, step = (uint32_t)p.pieces * kBlock;
+  const char* src = (const char*)q.data + (int64_t)from * q.page_stride;
+  char* dst = (char*)q.data + (int64_t)to * q.page_stride;
+#pragma unroll 4
+  for (uint32_t x = piece * kBlock + threadIdx.x; x < items; x += step) {
+    const uint32_t t = divide(x, each), y = x - t * each.by, o = divide(y, row);
+    const int64_t at = t * q.token_stride + o * q.outer_stride + (int64_t)(y - o * row.by) * V;
+    *(type*)(dst + at) = *(const type*)(src + at);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// What is held.  `clear` zeroes the counts and a bitmap of the pool, `hold`
+// counts the table's entries (adds whose order does not matter) and sets their
+// bits, and every workgroup of the last launches counts the bits before its
+// pages by itself: 32 pages a word, 32 KB for a pool of 256 K pages, from L2.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kBlock) clear_kernel(PoolParams p) {
+  const int64_t step = (int64_t)gridDim.x * kBlock, at = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+  for (int64_t i = at; i < p.words; i += step) p.bits[i] = 0;
+  if (p.refs != nullptr)
+    for (int64_t i = at; i < p.num_pages; i += step) p.refs[i] = 0;
+}
+
+__device__ __forceinline__ int32_t held_entries(const PoolParams& p, int32_t s) {
+  return pages_of(clamp_to(p.lengths[s], table_tokens(p.table_width, p.page_size)), p.page);
+}
+
+__global__ void __launch_bounds__(kBlock) hold_kernel(PoolParams p) {
+  const int32_t s = (int32_t)(blockIdx.x / (uint32_t)p.row_pieces);
+  const int32_t need = held_entries(p, s);
+  const int32_t* row = p.table + (int64_t)s * p.table_stride;
+  const int32_t j0 = (int32_t)(blockIdx.x % (uint32_t)p.row_pieces) * (kBlock * 4) + (int32_t)threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t j = (int64_t)j0 + k * kBlock;
+    if (j >= need) break;
+    const int32_t page = row[j];
+    if ((uint32_t)page >= (uint32_t)p.num_pages) continue;
+    atomicOr(p.bits + (page >> 5), 1u << (page & 31));
+    if (p.refs != nullptr) atomicAdd(p.refs + page, 1);
+  }
+}
+
+// Held pages among [0, 32 * words), all threads.
+__device__ __forceinline__ int32_t bits_before(const PoolParams& p, int32_t words, int32_t* s) {
+  int32_t n = 0;
+  const int32_t whole = words & ~3;
+  for (int32_t i = (int32_t)threadIdx.x * 4; i < whole; i += kBlock * 4) {
+    const u32x4 x = *(const u32x4*)(p.bits + i);
+    n += __builtin_popcount(x[0]) + __builtin_popcount(x[1]) + __builtin_popcount(x[2]) + __builtin_popcount(x[3]);
+  }
+  if ((int32_t)threadIdx.x < words - whole) n += __builtin_popcount(p.bits[whole + threadIdx.x]);
+  return block_sum(n, s);
+}
+
+// A workgroup looks after kPoolPages pages: eight words, two wavefronts' worth
+// of bits each.  rank: held pages before the thread's page.
+__device__ __forceinline__ int32_t rank_of(const PoolParams& p, int32_t page, int32_t* s) {
+  const int32_t word0 = (int32_t)blockIdx.x * (kBlock / 32);
+  int32_t n = bits_before(p, word0, s);
+  for (int32_t i = word0; i < (page >> 5) && i < p.words; ++i) n += __builtin_popcount(p.bits[i]);
+  if ((page >> 5) < p.words) n += __builtin_popcount(p.bits[page >> 5] & ((1u << (page & 31)) - 1u));
+  return n;
+}
+
+__global__ void __launch_bounds__(kBlock) free_kernel(PoolParams p) {
+  __shared__ int32_t sums[kBlock / 64];
+  const int32_t page = (int32_t)(blockIdx.x * kBlock + threadIdx.x);
+  const int32_t before = rank_of(p, page, sums);
+  const int32_t live = bits_before(p, p.words, sums);
+  if (page == 0) p.count[0] = p.num_pages - live;
+  if (page >= p.num_pages) return;
+  const bool held = (p.bits[page >> 5] >> (page & 31)) & 1u;
+  if (!held) p.free_pages[page - before] = page;
+  // The places behind the last one, as many as there are held pages.
+  if (held) p.free_pages[p.num_pages - live + before] = -1;
+}
+
+// The k-th held page from the limit on and the k-th free one below it.
+__global__ void __launch_bounds__(kBlock) moves_kernel(PoolParams p) {
+  __shared__ int32_t sums[kBlock / 64];
+  const int32_t page = (int32_t)(blockIdx.x * kBlock + threadIdx.x);
+  const int32_t before = rank_of(p, page, sums);
+  const int32_t live = bits_before(p, p.words, sums);
+  const int32_t limit = p.limit < 0 ? live : p.limit;
+  // Held pages below the limit.
+  int32_t low = bits_before(p, limit >> 5, sums);
+  if (limit & 31) low += __builtin_popcount(p.bits[limit >> 5] & ((1u << (limit & 31)) - 1u));
+  const int32_t holes = limit - low, movers = live - low, moves = holes < movers ? holes : movers;
+  if (page == 0) p.moves[0] = moves, p.live[0] = live;
+  if (page < p.num_pages / 2 && page >= moves) p.src[page] = -1, p.dst[page] = -1;
+  if (page >= p.num_pages) return;
+  const bool held = (p.bits[page >> 5] >> (page & 31)) & 1u;
+  if (page < limit) {
+    const int32_t k = page - before;
+    if (!held && k < moves) p.dst[k] = page;
+  } else {
+    const int32_t k = before - low;
+    if (held && k < moves) p.src[k] = page;
+    p.rank[page] = held && k < moves ? k : -1;
+  }
+}
+
+__global__ void __launch_bounds__(kBlock) rename_kernel(PoolParams p) {
+  const int32_t s = (int32_t)(blockIdx.x / (uint32_t)p.row_pieces);
+  const int32_t need = held_entries(p, s), limit = p.limit < 0 ? p.live[0] : p.limit;
+  const int32_t* row = p.table + (int64_t)s * p.table_stride;
+  int32_t* to = p.out_table + (int64_t)s * p.out_stride;
+  const int32_t j0 = (int32_t)(blockIdx.x % (uint32_t)p.row_pieces) * (kBlock * 4) + (int32_t)threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t j = (int64_t)j0 + k * kBlock;
+    if (j >= p.table_width) break;
+    int32_t page = row[j];
+    if (j < need && page >= limit && page < p.num_pages) {
+      const int32_t at = p.rank[page];
+      if (at >= 0) page = p.dst[at];
+    }
+    to[j] = page;
+  }
+}
+
+const void* fork_kernel_ptr(bool write) {
+  return write ? (const void*)&fork_write_kernel : (const void*)&fork_mark_kernel;
+}
+const void* copy_kernel_ptr(int bytes) {
+  return bytes == 16 ? (const void*)&copy_kernel<16> : bytes == 4 ? (const void*)&copy_kernel<4> : (const void*)&copy_kernel<1>;
+}
+const void* pool_kernel_ptr(int step) {
+  switch (step) {
+    case kPoolClear: return (const void*)&clear_kernel;
+    case kPoolHold: return (const void*)&hold_kernel;
+    case kPoolFree: return (const void*)&free_kernel;
+    case kPoolMoves: return (const void*)&moves_kernel;
+    default: return (const void*)&rename_kernel;
+  }
+}
+
+}  // namespace rrt

@@ -1,0 +1,81 @@
+"""Plain implementations of the operators on shared pages, row by row and page by
+page, in Python integers."""
+
+from __future__ import annotations
+
+import numpy as np
+
+
+def clamp(x, most):
+    return min(max(int(x), 0), int(most))
+
+
+def fork(table, lengths, parents, keep, free, page):
+    """(table, lengths, src, dst, tokens, pages) of the new batch."""
+    table = np.asarray(table, dtype=np.int64)
+    width = table.shape[1]
+    most = min(width * page, 1 << 30)
+    rows = []
+    for i, p in enumerate(parents):
+        m = 0
+        if 0 <= p < len(lengths):
+            m = clamp(lengths[p], most)
+            if keep is not None:
+                m = clamp(keep[i], m)
+        rows.append(m)
+    out = np.full((len(parents), width), -1, dtype=np.int64)
+    for i, m in enumerate(rows):
+        need = -(-m // page)
+        if need:
+            out[i, :need] = table[parents[i], :need]
+    held = out.copy()
+    src, dst, tokens, taken = [], [], [], 0
+    for i, m in enumerate(rows):
+        j = m // page
+        last = int(held[i, j]) if m % page else -1
+        shared = last >= 0 and any(
+            r != i and rows[r] > j * page and held[r, j] == last and (rows[r] >= (j + 1) * page or r < i)
+            for r in range(len(rows)))
+        if not shared:
+            src.append(-1), dst.append(-1), tokens.append(0)
+            continue
+        got = int(free[taken]) if taken < len(free) else -1
+        taken += 1
+        out[i, j] = got
+        src.append(last), dst.append(got), tokens.append(m % page)
+    return out, np.array(rows), np.array(src), np.array(dst), np.array(tokens), taken
+
+
+def held(table, lengths, page, pages):
+    """Every (row, place) that holds a page of the pool."""
+    width = np.asarray(table).shape[1]
+    for s, n in enumerate(lengths):
+        for j in range(-(-clamp(n, min(width * page, 1 << 30)) // page)):
+            if 0 <= table[s][j] < pages:
+                yield s, j
+
+
+def refs(table, lengths, page, pages):
+    n = np.zeros(pages, dtype=np.int64)
+    for s, j in held(table, lengths, page, pages):
+        n[table[s][j]] += 1
+    return n
+
+
+def compact(table, lengths, page, pages, limit=None):
+    """(table, moves as (from, to), held pages)."""
+    n = refs(table, lengths, page, pages)
+    live = int((n > 0).sum())
+    limit = live if limit is None else limit
+    movers = [p for p in range(limit, pages) if n[p]]
+    holes = [p for p in range(limit) if not n[p]]
+    moves = list(zip(movers, holes))
+    to = dict(moves)
+    out = np.array(table, dtype=np.int64)
+    for s, j in held(table, lengths, page, pages):
+        out[s, j] = to.get(int(out[s, j]), int(out[s, j]))
+    return out, moves, live
+
+
+def padded(x, n, fill=-1):
+    return np.array(list(x) + [fill] * (n - len(x)), dtype=np.int64)
