@@ -272,6 +272,104 @@ int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t
 int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream);
 
 /*
+ * Attention over pages that a cheap score chooses.  paged_bounds keeps, for each
+ * page and key-value head, the largest and the smallest value of every key dim
+ * in 8 bits; paged_block_select scores a row's pages by what no key between the
+ * bounds can pass and takes the best; paged_block_attention reads those.
+ *
+ * paged_bounds -- bounds of the pages that hold new tokens, from all their
+ * tokens in the cache:  with hi_d, lo_d the largest and smallest key value of
+ * dim d over a page's tokens and s = max_d max(|hi_d|, |lo_d|) / 127,
+ *   bounds[page, head] = [ceil(hi_d / s) .., floor(lo_d / s) ..], scales = s
+ * (quotients in fp32, clamped to [-127, 127]; all zeros where s is 0).  NaN is
+ * passed over, infinities count as the type's largest value.  The scale of an
+ * e4m3 cache is not part of it: it multiplies all of a head's scores.
+ *
+ *   k            the key cache, as for paged_attention.
+ *   starts       int32 [num_seqs + 1], as paged_layout gives them: sequence s
+ *                has starts[s + 1] - starts[s] new tokens, its last ones.
+ *   lengths      int32 [num_seqs], tokens after the step.
+ *   num_tokens   the most new tokens there are, paged_layout's capacity; pages
+ *                of tokens past it are left as they were.
+ *   bounds       int8 [num_pages, num_kv_heads, 2, head_dim], page and head
+ *                strides given (in bytes), 16-byte aligned.
+ *   scales       fp32 [num_pages, num_kv_heads], rows scales_stride apart.
+ *
+ * A page that holds new tokens belongs to one sequence.
+ */
+typedef struct {
+  const void* k;
+  const int32_t* block_table;
+  const int32_t* starts;
+  const int32_t* lengths;
+  void* bounds;
+  float* scales;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t bounds_page_stride, bounds_head_stride, scales_stride;
+  int64_t table_stride;
+  int32_t num_seqs, num_tokens;
+  int32_t num_kv_heads, head_dim;
+  int32_t page_size, num_pages, table_width;
+  paged_dtype store;
+} paged_bounds_args;
+
+int paged_bounds(const paged_bounds_args* args, hipStream_t stream);
+
+/*
+ * paged_block_select -- for each row and key-value head the num_blocks pages
+ * (blocks of its sequence, 0 for the first page_size positions) with the
+ * largest scores, ascending, -1 past the last, as topk_ragged gives positions.
+ * Block b's score is
+ *   max over the heads h of the key-value head:
+ *     (float)(sum_d max(Q_hd B_d, Q_hd b_d)) * s_h * s_b
+ * with B, b the block's bounds and s_b their scale, s_h = max_d |q_hd| / 127 and
+ * Q_hd = q_hd / s_h rounded to nearest even: whole numbers but for the scales,
+ * so that equal inputs give equal choices everywhere.  Ties go to the lower
+ * block.  Blocks [0, first) and the last `last` of the row come before all
+ * others, blocks without a page after all others.  NaN in q counts as 0.
+ *
+ *   q            [num_rows, num_heads, head_dim], strides multiples of 16 bytes.
+ *   lengths      int32 [num_rows]: row r has ceil(lengths[r] / page_size)
+ *                blocks.
+ *   blocks       int32 [num_rows, num_kv_heads, num_blocks], contiguous.
+ *   workspace    paged_block_select_workspace_size() bytes; NULL when that is 0.
+ *
+ * first + last is at most num_blocks; table_width is at most 32768.
+ */
+typedef struct {
+  const void* q;
+  const void* bounds;
+  const float* scales;
+  const int32_t* block_table;
+  const int32_t* lengths;
+  int32_t* blocks;
+  int64_t q_row_stride, q_head_stride;
+  int64_t bounds_page_stride, bounds_head_stride, scales_stride;
+  int64_t table_stride;
+  int32_t num_rows, next_n;
+  int32_t num_heads, num_kv_heads, head_dim;
+  int32_t page_size, num_pages, table_width;
+  int32_t num_blocks, first, last;
+  paged_dtype dtype;
+} paged_select_args;
+
+int paged_block_select_workspace_size(const paged_select_args* args, hipStream_t stream, size_t* bytes);
+int paged_block_select(const paged_select_args* args, void* workspace, hipStream_t stream);
+
+/*
+ * paged_block_attention -- paged_attention over chosen blocks (pages of the
+ * row's sequence), chosen for each row and key-value head: blocks int32
+ * [num_rows, num_kv_heads, num_blocks], strides given, as paged_block_select
+ * gives them.  The row reads the positions of those blocks below its length;
+ * blocks outside it are left out, one that occurs twice counts twice.
+ * args->chosen is NULL.  num_blocks * page_size is at most 2^30.
+ */
+int paged_block_attention_workspace_size(const paged_attention_args* args, int32_t num_blocks, hipStream_t stream,
+                                         size_t* bytes);
+int paged_block_attention(const paged_attention_args* args, const int32_t* blocks, int64_t blocks_row_stride,
+                          int64_t blocks_head_stride, int32_t num_blocks, void* workspace, hipStream_t stream);
+
+/*
  * latent_attention -- the absorbed form: every head reads one shared latent
  * vector a token, keys c[0 .. head_dim + 64), values c[0 .. head_dim):
  * out = softmax(softmax_scale * q c^T) c.  Arguments as for paged_attention

@@ -48,3 +48,8 @@ from .pages import (  # noqa: F401
     paged_fork,
     paged_free,
 )
+from .blocks import (  # noqa: F401
+    paged_block_attention,
+    paged_block_select,
+    paged_bounds,
+)

@@ -27,7 +27,8 @@ EXPORTED = (
     "paged_layout", "paged_append", "paged_attention", "paged_attention_workspace_size", "latent_attention",
     "latent_attention_workspace_size", "latent_prefill", "latent_prefill_workspace_size",
     "paged_debug_place", "paged_debug_split", "paged_fork", "paged_copy", "paged_free", "paged_free_workspace_size",
-    "paged_compact", "paged_compact_workspace_size",
+    "paged_compact", "paged_compact_workspace_size", "paged_bounds", "paged_block_select",
+    "paged_block_select_workspace_size", "paged_block_attention", "paged_block_attention_workspace_size",
 )
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -95,6 +96,11 @@ def load() -> ctypes.CDLL:
         lib.paged_compact.argtypes = [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
                                       _vp]
         lib.paged_free_workspace_size.argtypes = lib.paged_compact_workspace_size.argtypes = [_i32, size]
+        lib.paged_bounds.argtypes = [_vp, _vp]
+        lib.paged_block_select.argtypes = [_vp, _vp, _vp]
+        lib.paged_block_select_workspace_size.argtypes = [_vp, _vp, size]
+        lib.paged_block_attention.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp]
+        lib.paged_block_attention_workspace_size.argtypes = [_vp, _i32, _vp, size]
         for name in EXPORTED:
             getattr(lib, name).restype = ctypes.c_int
         lib.paged_debug_place.argtypes = [_vp, _i32, _i32, _i64, _i64, _i32]
@@ -186,15 +192,17 @@ def _output(x, name: str, dtype, shape, like):
     return x
 
 
-def _launch(name: str, args, workspace, key, like) -> None:
+def _launch(name: str, args, workspace, key, like, size_args=(), more=()) -> None:
     """Calls entry point `name` with a workspace large enough: `workspace`, or
-    a new one.  key: what its size depends on."""
+    a new one.  key: what its size depends on; size_args, more: further arguments
+    of the size's and of the call itself."""
+    args = ctypes.byref(args)
     dev = like.get_device()
     stream = torch._C._cuda_getCurrentRawStream(dev)
     need = _sizes.get((name, dev, key))
     if need is None:
         size = ctypes.c_size_t(0)
-        _check(getattr(_lib, name + "_workspace_size")(args, stream, size), name)
+        _check(getattr(_lib, name + "_workspace_size")(args, *size_args, stream, size), name)
         need = size.value
         if len(_sizes) >= 4096:
             _sizes.clear()
@@ -207,7 +215,7 @@ def _launch(name: str, args, workspace, key, like) -> None:
               or workspace.numel() * workspace.element_size() < need):
             raise ValueError(f"workspace must be a contiguous tensor of {need} bytes or more on {like.device}")
         ptr = workspace.data_ptr()
-    _check(getattr(_lib, name)(args, ptr, stream), name)
+    _check(getattr(_lib, name)(args, *more, ptr, stream), name)
 
 
 _sizes: dict = {}  # workspace bytes by shape: a pure function of it
@@ -333,10 +341,10 @@ def latent_append(slots, latent, rope, cache, *, scale=None, stream=None) -> Non
 # ---------------------------------------------------------------------------
 
 def _attend(entry: str, q, k, v, scales, lengths, block_table, chosen, next_n, softmax_scale, kv: int, value_dim: int,
-            out, lse, workspace, max_splits: int):
-    """paged_attention and latent_attention after what differs between them:
-    k (and v) a cache [num_pages, page_size, ..., dim], scales (name, tensor,
-    size) of each."""
+            out, lse, workspace, max_splits: int, key=(), size_args=(), more=()):
+    """The attentions of rows after what differs between them: k (and v) a
+    cache [num_pages, page_size, ..., dim], scales (name, tensor, size) of
+    each; key, size_args, more: as for _launch."""
     dev = q.get_device()
     code, store = _code(q, "q"), _code(k, "the cache", True)
     if store != _E4M3 and store != code:
@@ -369,8 +377,26 @@ def _attend(entry: str, q, k, v, scales, lengths, block_table, chosen, next_n, s
                          lse.data_ptr(), qstride[0], qstride[1], kstride[0], kstride[1],
                          kstride[2] if v is not None else 0, block_table.stride(0), chosen_stride, rows, next_n, heads,
                          kv, value_dim, kshape[1], kshape[0], width, num_chosen, softmax_scale, code, store, max_splits)
-    _launch(entry, args, workspace, (rows, next_n, heads, kv, value_dim, kshape[1], width, num_chosen, max_splits), q)
+    _launch(entry, args, workspace, (rows, next_n, heads, kv, value_dim, kshape[1], width, num_chosen, max_splits, *key),
+            q, size_args, more)
     return out, lse
+
+
+def _paged(entry: str, q, k_cache, v_cache, block_table, lengths, chosen, softmax_scale, k_scale, v_scale, next_n, out, lse,
+           workspace, max_splits: int, blocks=None):
+    """The attentions over a cache of keys and values.  blocks: pointer, strides
+    and number of the chosen blocks."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
+    if v_cache.dtype is not k_cache.dtype or v_cache.get_device() != q.get_device():
+        raise TypeError("k_cache and v_cache must have the same type and device")
+    kv, dim = k_cache.shape[2], k_cache.shape[3]
+    if kv < 1 or q.dim() != 3 or q.shape[1] % kv != 0:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    more = {} if blocks is None else dict(key=(blocks[3],), size_args=(blocks[3],), more=blocks)
+    return _attend(entry, q, k_cache, v_cache, (("k_scale", k_scale, kv), ("v_scale", v_scale, kv)), lengths, block_table,
+                   chosen, next_n, dim ** -0.5 if softmax_scale is None else softmax_scale, kv, dim, out, lse, workspace,
+                   max_splits, **more)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, softmax_scale: float | None = None,
@@ -398,16 +424,8 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, s
             return paged_attention(q, k_cache, v_cache, block_table, lengths, chosen=chosen,
                                    softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale, next_n=next_n,
                                    out=out, lse=lse, workspace=workspace, max_splits=max_splits)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
-    if v_cache.dtype is not k_cache.dtype or v_cache.get_device() != q.get_device():
-        raise TypeError("k_cache and v_cache must have the same type and device")
-    kv, dim = k_cache.shape[2], k_cache.shape[3]
-    if kv < 1 or q.dim() != 3 or q.shape[1] % kv != 0:
-        raise ValueError("q's heads must be a multiple of the cache's")
-    return _attend("paged_attention", q, k_cache, v_cache, (("k_scale", k_scale, kv), ("v_scale", v_scale, kv)),
-                   lengths, block_table, chosen, next_n, dim ** -0.5 if softmax_scale is None else softmax_scale, kv,
-                   dim, out, lse, workspace, max_splits)
+    return _paged("paged_attention", q, k_cache, v_cache, block_table, lengths, chosen, softmax_scale, k_scale, v_scale,
+                  next_n, out, lse, workspace, max_splits)
 
 
 def latent_attention(q, cache, block_table, lengths, *, softmax_scale: float, chosen=None, scale=None,

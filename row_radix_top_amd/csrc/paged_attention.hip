@@ -101,19 +101,14 @@ __device__ __forceinline__ void load_values(KvTile<F8, D>& b, const char* v, int
   }
 }
 
-// What a row reads: all its positions (kOne: a sequence has one row; kRows:
-// several, which share the reads but may end at different places), or chosen
-// ones.
-enum { kOne, kRows, kChosen };
-
 template <bool B>
 struct Flag {
   static constexpr bool value = B;
 };
 
 template <typename T, bool F8, int D, int MODE, int NT>
-__global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) attn_kernel(AttnParams p) {
-  constexpr bool CHOSEN = MODE == kChosen;
+__global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows ? 3 : 2) attn_kernel(AttnParams p) {
+  constexpr bool CHOSEN = MODE == kChosen || MODE == kBlocks;
   constexpr int KS = D / 32;  // matrix steps over the key dims
   constexpr int VD = D / 16;  // value dims of a lane
   constexpr int SZ = F8 ? 1 : 2;
@@ -181,12 +176,13 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
   const char* vbase = (const char*)a.v + (int64_t)kvh * a.head_stride * SZ;
   const int32_t* table = a.block_table + (int64_t)(r0 / a.next_n) * a.table_stride;
   const int32_t* chosen = CHOSEN ? a.chosen + (int64_t)r0 * a.chosen_stride : nullptr;
+  if constexpr (MODE == kBlocks) chosen += (int64_t)kvh * p.chosen_head_stride;
   const int32_t seen = CHOSEN ? clamp_to(a.lengths[r0], most) : 0;
 
   // Places of the lane's tokens (both halves of the wavefront hold the same
   // 32); a part is never empty unless its row is.
   constexpr int kStep = 4 * kTok;
-  Places<CHOSEN> places{table, chosen, a.page_stride, a.token_stride, p.page, a.num_pages, seen, end, kStep};
+  Places<MODE> places{table, chosen, a.page_stride, a.token_stride, p.page, a.num_pages, seen, end, kStep};
 
   float m[NT], l[NT];
   f32x4 o[NT][VD];
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kRows ? 3 : 2) 
     // Ragged tiles come last and in a loop of their own: the copies of the
     // sums that they need cost the others registers and spills (32 x 2 rows of
     // 16384 positions, 64 heads on 4, a call: 329 us against 229, e4m3 240 against 129).
-    if constexpr (MODE == kRows) {
+    if constexpr (MODE == kManyRows) {
       while (more && t + kTok <= shortest) step(Flag<false>{});
       while (more) step(Flag<true>{});
     } else {
@@ -482,8 +478,9 @@ const void* attn_tiles(int tiles) {
 }
 template <typename T, bool F8, int D>
 const void* attn_modes(int mode, int tiles) {
-  return mode == kOne ? attn_tiles<T, F8, D, kOne>(tiles)
-       : mode == kRows ? attn_tiles<T, F8, D, kRows>(tiles) : attn_tiles<T, F8, D, kChosen>(tiles);
+  return mode == kOneRow ? attn_tiles<T, F8, D, kOneRow>(tiles)
+       : mode == kManyRows ? attn_tiles<T, F8, D, kManyRows>(tiles)
+       : mode == kChosen ? attn_tiles<T, F8, D, kChosen>(tiles) : attn_tiles<T, F8, D, kBlocks>(tiles);
 }
 template <typename T, bool F8>
 const void* attn_dims(int head_dim, int mode, int tiles) {
@@ -504,8 +501,7 @@ const void* join_dims(int head_dim, bool many) {
 
 }  // namespace
 
-const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int rows, int tiles) {
-  const int mode = chosen ? kChosen : rows > 1 ? kRows : kOne;
+const void* attn_kernel_ptr(int dtype, int store, int head_dim, int mode, int tiles) {
   if (dtype == PAGED_BF16)
     return store == PAGED_E4M3 ? attn_dims<Bf16, true>(head_dim, mode, tiles)
                                : attn_dims<Bf16, false>(head_dim, mode, tiles);

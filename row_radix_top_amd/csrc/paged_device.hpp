@@ -97,13 +97,13 @@ __device__ __forceinline__ int64_t readlane64(int64_t v, int lane) {
 }
 
 // Places of a lane's tokens, one a tile, `step` positions of the row apart.
-// A place takes up to two dependent reads (the chosen position, its page);
-// memory reads return in order, so each is issued one tile before it is
+// A place takes up to two dependent reads (the chosen position or block, its
+// page); memory reads return in order, so each is issued one tile before it is
 // needed and ahead of that tile's data, and nothing waits for it alone:
 //   start(i); loop { off = take(); ... issue the data loads at off ... }
 // take() returns the place of the next tile (in elements, -1: nothing there)
 // and issues the reads for the two after it.
-template <bool CHOSEN>
+template <int MODE>
 struct Places {
   const int32_t* table;
   const int32_t* chosen;
@@ -111,19 +111,30 @@ struct Places {
   Divisor by;          // page size
   int32_t num_pages, seen, end, step;
   int32_t at;          // row index of the entry in `ahead`
-  int32_t ahead;       // the chosen position there
+  int32_t ahead;       // the chosen position (block) there
   int32_t page;        // the next tile's page
   uint32_t in;         // and the offset inside it, all ones where there is no position
 
   __device__ __forceinline__ int32_t read(int32_t i) const {
-    if constexpr (CHOSEN) return chosen[i < end ? i : end - 1];
+    if constexpr (MODE == kChosen) return chosen[i < end ? i : end - 1];
+    if constexpr (MODE == kBlocks) return chosen[divide((uint32_t)(i < end ? i : end - 1), by)];
     return i;
   }
   __device__ __forceinline__ void look_up() {
-    const bool ok = at < end && (!CHOSEN || (uint32_t)ahead < (uint32_t)seen);
-    const uint32_t pos = ok ? (uint32_t)ahead : 0u, j = divide(pos, by);
-    in = ok ? pos - j * by.by : ~0u;
-    page = table[j];
+    if constexpr (MODE == kBlocks) {
+      // Entry `at` is a token of block `ahead`; below the row's length if the
+      // block begins there, which keeps the product in 32 bits.
+      const uint32_t i = (uint32_t)(at < end ? at : 0), o = i - divide(i, by) * by.by;
+      const bool begins = (uint32_t)ahead < (uint32_t)seen && (uint32_t)ahead <= divide((uint32_t)seen - 1u, by);
+      const bool ok = at < end && begins && (uint32_t)ahead * by.by + o < (uint32_t)seen;
+      in = ok ? o : ~0u;
+      page = table[ok ? ahead : 0];
+    } else {
+      const bool ok = at < end && (MODE != kChosen || (uint32_t)ahead < (uint32_t)seen);
+      const uint32_t pos = ok ? (uint32_t)ahead : 0u, j = divide(pos, by);
+      in = ok ? pos - j * by.by : ~0u;
+      page = table[j];
+    }
     at += step;
     ahead = read(at);
   }

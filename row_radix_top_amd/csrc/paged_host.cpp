@@ -117,8 +117,9 @@ struct AttnPlan {
 
 // reserve: NULL, or receives the bytes of workspace that this launch or one of
 // fewer rows may use.
+// blocks: a->chosen holds blocks, this far apart for key-value heads (else NULL).
 int plan_attention(const paged_attention_args* a, bool latent, hipStream_t stream, AttnPlan* out,
-                   size_t* reserve = nullptr) {
+                   size_t* reserve = nullptr, const int64_t* blocks = nullptr) {
   if (int rc = check_attention(a, latent)) return rc;
   std::memset(out, 0, sizeof(*out));
   if (reserve != nullptr) *reserve = 0;
@@ -152,7 +153,9 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
     p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
     p.groups = a->num_rows / p.group_rows;
     units = (int64_t)p.groups * a->num_kv_heads * p.col_tiles;
-    out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, chosen, p.group_rows, tiles);
+    const int mode = blocks != nullptr ? rrt::kBlocks : chosen ? rrt::kChosen : p.group_rows > 1 ? rrt::kManyRows : rrt::kOneRow;
+    p.chosen_head_stride = blocks != nullptr ? *blocks : 0;
+    out->fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, mode, tiles);
   }
   const int64_t longest = chosen ? a->num_chosen : rrt::table_tokens(a->table_width, a->page_size);
   const int64_t each = units / p.groups;
@@ -177,9 +180,10 @@ int plan_attention(const paged_attention_args* a, bool latent, hipStream_t strea
   return TOPK_OK;
 }
 
-int run_attention(const paged_attention_args* a, bool latent, void* workspace, hipStream_t stream) {
+int run_attention(const paged_attention_args* a, bool latent, void* workspace, hipStream_t stream,
+                  const int64_t* blocks = nullptr) {
   AttnPlan plan;
-  if (int rc = plan_attention(a, latent, stream, &plan)) return rc;
+  if (int rc = plan_attention(a, latent, stream, &plan, nullptr, blocks)) return rc;
   if (a->num_rows == 0) return TOPK_OK;
   if (plan.bytes > 0) {
     if (workspace == nullptr) {
@@ -192,13 +196,153 @@ int run_attention(const paged_attention_args* a, bool latent, void* workspace, h
     plan.p.part_stat =
         reinterpret_cast<float2*>(plan.p.part_out + (int64_t)a->num_rows * a->num_heads * plan.p.most * a->head_dim);
   }
-  const char* name = latent ? "latent_attention" : "paged_attention";
+  const char* name = latent ? "latent_attention" : blocks != nullptr ? "paged_block_attention" : "paged_attention";
   if (int rc = launch(plan.fn, plan.grid, plan.threads, &plan.p, stream, name)) return rc;
   if (plan.p.most == 1) return TOPK_OK;
   const bool many = plan.p.most > 4;
   const int64_t outputs = (int64_t)a->num_rows * a->num_heads;
   return launch(rrt::join_kernel_ptr(a->dtype, a->head_dim, many), many ? outputs : ceil_div(outputs, 4), 256, &plan.p,
                 stream, "join of split rows");
+}
+
+// The arguments of paged_attention over the tokens of num_blocks chosen blocks.
+int block_args(const paged_attention_args* a, const int32_t* blocks, int64_t row_stride, int64_t head_stride,
+               int32_t num_blocks, paged_attention_args* out) {
+  REQUIRE(a != nullptr, "null args");
+  REQUIRE(a->chosen == nullptr, "blocks are chosen in place of positions: chosen must be NULL");
+  REQUIRE(a->page_size >= 1, "page_size must be >= 1");
+  REQUIRE(num_blocks >= 1 && (int64_t)num_blocks * a->page_size <= rrt::kMostTokens,
+          "num_blocks must be >= 1, num_blocks * page_size at most 2^30");
+  REQUIRE(row_stride >= 0 && head_stride >= 0, "strides must be >= 0");
+  REQUIRE(aligned(blocks, 4), "blocks must be 4-byte aligned");
+  REQUIRE(blocks != nullptr || a->num_rows <= 0, "null blocks");
+  *out = *a;
+  // Any address stands for the blocks where there are no rows.
+  out->chosen = blocks != nullptr ? blocks : reinterpret_cast<const int32_t*>(16);
+  out->chosen_stride = row_stride;
+  out->num_chosen = num_blocks * a->page_size;
+  return TOPK_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Bounds and the choice of blocks
+// ---------------------------------------------------------------------------
+
+int check_bounds(const paged_bounds_args* a) {
+  REQUIRE(a != nullptr, "null args");
+  REQUIRE(a->store == PAGED_BF16 || a->store == PAGED_FP16 || a->store == PAGED_E4M3,
+          "store must be PAGED_BF16, PAGED_FP16 or PAGED_E4M3");
+  REQUIRE(a->num_seqs >= 0, "num_seqs must be >= 0");
+  REQUIRE(a->num_tokens >= 0, "num_tokens must be >= 0");
+  REQUIRE(a->num_kv_heads >= 1, "num_kv_heads must be >= 1");
+  REQUIRE(a->head_dim == 64 || a->head_dim == 128, "head_dim must be 64 or 128");
+  REQUIRE(a->page_size >= 1, "page_size must be >= 1");
+  REQUIRE(a->table_width >= 1, "table_width must be >= 1");
+  if (a->num_seqs == 0 || a->num_tokens == 0) return TOPK_OK;
+  REQUIRE(a->num_pages >= 1, "num_pages must be >= 1");
+  REQUIRE(a->k != nullptr && a->block_table != nullptr && a->starts != nullptr && a->lengths != nullptr &&
+              a->bounds != nullptr && a->scales != nullptr,
+          "null k, block_table, starts, lengths, bounds or scales");
+  const int64_t sz = a->store == PAGED_E4M3 ? 1 : 2;
+  REQUIRE(a->page_stride >= 0 && a->token_stride >= 0 && a->head_stride >= 0 && a->bounds_page_stride >= 0 &&
+              a->bounds_head_stride >= 0 && a->scales_stride >= 0 && a->table_stride >= 0,
+          "strides must be >= 0");
+  REQUIRE(aligned(a->k, 16) && a->page_stride * sz % 16 == 0 && a->token_stride * sz % 16 == 0 &&
+              a->head_stride * sz % 16 == 0,
+          "the cache and its strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->bounds, 16) && a->bounds_page_stride % 16 == 0 && a->bounds_head_stride % 16 == 0,
+          "bounds and their strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->block_table, 4) && aligned(a->starts, 4) && aligned(a->lengths, 4) && aligned(a->scales, 4),
+          "block_table, starts, lengths and scales must be 4-byte aligned");
+  return TOPK_OK;
+}
+
+int check_select(const paged_select_args* a) {
+  REQUIRE(a != nullptr, "null args");
+  if (int rc = check_types(a->dtype, a->dtype)) return rc;
+  REQUIRE(a->num_rows >= 0, "num_rows must be >= 0");
+  REQUIRE(a->next_n >= 1 && a->num_rows % a->next_n == 0, "next_n must be >= 1 and divide num_rows");
+  REQUIRE(a->num_heads >= 1, "num_heads must be >= 1");
+  REQUIRE(a->num_kv_heads >= 1 && a->num_heads % a->num_kv_heads == 0, "num_kv_heads must be >= 1 and divide num_heads");
+  REQUIRE(a->head_dim == 64 || a->head_dim == 128, "head_dim must be 64 or 128");
+  REQUIRE(a->page_size >= 1, "page_size must be >= 1");
+  REQUIRE(a->table_width >= 1 && a->table_width <= rrt::kMostBlocks, "table_width must be in [1, 32768]");
+  REQUIRE(a->first >= 0 && a->last >= 0 && a->num_blocks >= 1 && (int64_t)a->first + a->last <= a->num_blocks,
+          "num_blocks must be >= 1 and first + last, both >= 0, at most num_blocks");
+  if (a->num_rows == 0) return TOPK_OK;
+  REQUIRE(a->num_pages >= 1, "num_pages must be >= 1");
+  REQUIRE((int64_t)a->num_rows * a->num_heads <= INT32_MAX, "num_rows * num_heads must be below 2^31");
+  REQUIRE(a->q != nullptr && a->bounds != nullptr && a->scales != nullptr && a->block_table != nullptr &&
+              a->lengths != nullptr && a->blocks != nullptr,
+          "null q, bounds, scales, block_table, lengths or blocks");
+  REQUIRE(a->q_row_stride >= 0 && a->q_head_stride >= 0 && a->bounds_page_stride >= 0 && a->bounds_head_stride >= 0 &&
+              a->scales_stride >= 0 && a->table_stride >= 0,
+          "strides must be >= 0");
+  REQUIRE(aligned(a->q, 16) && a->q_row_stride % 8 == 0 && a->q_head_stride % 8 == 0,
+          "q and its strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->bounds, 16) && a->bounds_page_stride % 16 == 0 && a->bounds_head_stride % 16 == 0,
+          "bounds and their strides must be multiples of 16 bytes");
+  REQUIRE(aligned(a->scales, 4) && aligned(a->block_table, 4) && aligned(a->lengths, 4) && aligned(a->blocks, 4),
+          "scales, block_table, lengths and blocks must be 4-byte aligned");
+  return TOPK_OK;
+}
+
+struct SelectPlan {
+  rrt::SelectParams p;
+  int tiles;
+  bool split;
+  int64_t grid;
+  size_t lds, bytes;
+};
+
+constexpr int32_t kFusedBlocks = 4096;       // what one wavefront picks from
+constexpr size_t kFusedLds = 64 * 1024;
+
+int plan_select(const paged_select_args* a, hipStream_t stream, SelectPlan* out, size_t* reserve = nullptr) {
+  if (int rc = check_select(a)) return rc;
+  std::memset(out, 0, sizeof(*out));
+  if (reserve != nullptr) *reserve = 0;
+  if (a->num_rows == 0) return TOPK_OK;
+  int dev = 0, cus = 0;
+  if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
+  rrt::SelectParams& p = out->p;
+  p.a = *a;
+  p.page = rrt::divisor_of(a->page_size);
+  p.pitch = (int32_t)ceil_div(a->table_width, 16) * 16;
+  const int32_t per = a->num_heads / a->num_kv_heads;
+  p.hp2 = 1;
+  while (p.hp2 < per && p.hp2 < 16) p.hp2 *= 2;
+  const int64_t row_bytes = (int64_t)p.pitch * 4, seqs = a->num_rows / a->next_n;
+  const int64_t tile_rows = per <= 16 ? 16 / p.hp2 : 1;  // rows of a sixteen
+  const int64_t fit = a->table_width <= kFusedBlocks ? (int64_t)kFusedLds / row_bytes : 0;
+  out->tiles = 1;
+  if (per > 16) {
+    out->tiles = per <= 32 ? 2 : 4;
+  } else {
+    while (out->tiles < 4 && tile_rows * out->tiles < a->next_n && (fit == 0 || tile_rows * out->tiles * 2 <= fit))
+      out->tiles *= 2;
+  }
+  p.unit_rows = (int32_t)std::min<int64_t>(per <= 16 ? tile_rows * out->tiles : 1, fit > 0 ? fit : INT32_MAX);
+  p.seq_units = (int32_t)ceil_div(a->next_n, p.unit_rows);
+  const int64_t units = seqs * p.seq_units * a->num_kv_heads;
+  out->split = fit == 0 || (a->table_width > 512 && units * 2 <= cus);
+  if (out->split) {
+    // Parts of 16 blocks for each wavefront and more, two workgroups a CU.
+    const int64_t tiles = p.pitch / 16, most = std::max<int64_t>(1, std::min<int64_t>(tiles / 8, ceil_div(2 * cus, units)));
+    p.part_tiles = (int32_t)ceil_div(tiles, most);
+    p.parts = (int32_t)ceil_div(tiles, p.part_tiles);
+    out->bytes = (size_t)a->num_rows * a->num_kv_heads * row_bytes;
+  } else {
+    p.parts = 1;
+    out->lds = (size_t)row_bytes * p.unit_rows;
+  }
+  out->grid = units * p.parts;
+  if (reserve == nullptr) return TOPK_OK;
+  // Fewer rows or a narrower table may be split where these are not: half a CU
+  // each, of rows that fit kFusedLds.
+  *reserve = out->split ? out->bytes
+                        : std::min<size_t>((size_t)a->num_rows * a->num_kv_heads * row_bytes, (size_t)cus / 2 * kFusedLds);
+  return TOPK_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -381,6 +525,55 @@ int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t
 
 int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream) {
   return run_attention(args, false, workspace, stream);
+}
+
+int paged_block_attention_workspace_size(const paged_attention_args* args, int32_t num_blocks, hipStream_t stream,
+                                         size_t* bytes) {
+  REQUIRE(bytes != nullptr, "null bytes");
+  paged_attention_args a;
+  const int64_t heads = 0;
+  if (int rc = block_args(args, reinterpret_cast<const int32_t*>(16), 0, 0, num_blocks, &a)) return rc;
+  AttnPlan plan;
+  return plan_attention(&a, false, stream, &plan, bytes, &heads);
+}
+
+int paged_block_attention(const paged_attention_args* args, const int32_t* blocks, int64_t blocks_row_stride,
+                          int64_t blocks_head_stride, int32_t num_blocks, void* workspace, hipStream_t stream) {
+  paged_attention_args a;
+  if (int rc = block_args(args, blocks, blocks_row_stride, blocks_head_stride, num_blocks, &a)) return rc;
+  return run_attention(&a, false, workspace, stream, &blocks_head_stride);
+}
+
+int paged_bounds(const paged_bounds_args* args, hipStream_t stream) {
+  if (int rc = check_bounds(args)) return rc;
+  if (args->num_seqs == 0 || args->num_tokens == 0) return TOPK_OK;
+  rrt::BoundsParams p{};
+  p.a = *args;
+  p.page = rrt::divisor_of(args->page_size);
+  p.units = (int64_t)args->num_tokens / args->page_size + 2 * (int64_t)args->num_seqs;
+  return launch(rrt::bounds_kernel_ptr(args->store, args->head_dim),
+                ceil_div(p.units * args->num_kv_heads, rrt::kBlocksBlock / 64), rrt::kBlocksBlock, &p, stream,
+                "paged_bounds");
+}
+
+int paged_block_select_workspace_size(const paged_select_args* args, hipStream_t stream, size_t* bytes) {
+  REQUIRE(bytes != nullptr, "null bytes");
+  SelectPlan plan;
+  return plan_select(args, stream, &plan, bytes);
+}
+
+int paged_block_select(const paged_select_args* args, void* workspace, hipStream_t stream) {
+  SelectPlan plan;
+  if (int rc = plan_select(args, stream, &plan)) return rc;
+  if (args->num_rows == 0) return TOPK_OK;
+  if (int rc = check_workspace(workspace, plan.bytes)) return rc;
+  plan.p.scores = static_cast<float*>(workspace);
+  if (int rc = launch(rrt::select_kernel_ptr(args->dtype, args->head_dim, plan.tiles, plan.split), plan.grid,
+                      rrt::kBlocksBlock, &plan.p, stream, "paged_block_select", plan.lds))
+    return rc;
+  if (!plan.split) return TOPK_OK;
+  return launch(rrt::pick_kernel_ptr(), (int64_t)args->num_rows * args->num_kv_heads, rrt::kPickBlock, &plan.p, stream,
+                "paged_block_select");
 }
 
 int latent_attention_workspace_size(const paged_attention_args* args, hipStream_t stream, size_t* bytes) {

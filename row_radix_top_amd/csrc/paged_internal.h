@@ -138,6 +138,28 @@ struct PoolParams {
 };
 enum { kPoolClear, kPoolHold, kPoolFree, kPoolMoves, kPoolRename };
 
+constexpr int kBlocksBlock = 256;  // threads of a workgroup of the bounds and of the choice
+constexpr int kPickBlock = 1024;   // and of a choice from the workspace
+constexpr int32_t kMostBlocks = 32768;  // of a row that a choice is made from
+
+struct BoundsParams {
+  paged_bounds_args a;
+  int64_t units;  // pages that the grid covers
+  Divisor page;   // by page_size
+};
+
+struct SelectParams {
+  paged_select_args a;
+  float* scores;       // split: [rows][kv heads][pitch]
+  int32_t pitch;       // scores of a row
+  int32_t unit_rows;   // rows of a workgroup, of one sequence
+  int32_t seq_units;   // workgroups of a sequence and key-value head
+  int32_t hp2;         // columns of a row: the power of two from its heads up, at most 16
+  int32_t parts;       // split: workgroups along the blocks,
+  int32_t part_tiles;  // and sixteens of blocks of each
+  Divisor page;
+};
+
 struct AttnParams {
   paged_attention_args a;
   float* part_out;     // [rows, heads, most, head_dim], unnormalised
@@ -150,6 +172,7 @@ struct AttnParams {
   int32_t group_rows;  // rows of a group: next_n, or 1
   int32_t col_tiles;   // column tiles of a key-value head
   Divisor page;        // by page_size
+  int64_t chosen_head_stride;  // blocks: a key-value head's, in a.chosen
 };
 
 // The expanded form works on tiles of kCtxTile context tokens; a sequence
@@ -189,7 +212,14 @@ const void* append_kernel_ptr(int dtype, int store, bool wide);
 const void* fork_kernel_ptr(bool write);
 const void* copy_kernel_ptr(int bytes);
 const void* pool_kernel_ptr(int step);
-const void* attn_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int rows, int tiles);
+// What a row of the attention over a cache reads: all its positions (kOneRow: a
+// sequence has one row; kManyRows: several, which share the reads but may end at
+// different places), or chosen positions, or chosen blocks.
+enum { kOneRow, kManyRows, kChosen, kBlocks };
+const void* attn_kernel_ptr(int dtype, int store, int head_dim, int mode, int tiles);
+const void* bounds_kernel_ptr(int store, int head_dim);
+const void* select_kernel_ptr(int dtype, int head_dim, int tiles, bool split);
+const void* pick_kernel_ptr();
 const void* latent_kernel_ptr(int dtype, int store, int head_dim, bool chosen, int heads);
 const void* join_kernel_ptr(int dtype, int head_dim, bool many);
 const void* expand_kernel_ptr(int dtype, int store, int latent_dim);

@@ -8,8 +8,8 @@ import ctypes
 import pytest
 
 from row_radix_top_amd import attention as pa
-from row_radix_top_amd import binding, pages
-from tests.test_paged_refusals import _header
+from row_radix_top_amd import binding, blocks, pages
+from tests.test_paged_refusals import _attention, _header
 
 EINVAL, EWORKSPACE = -1, -3
 
@@ -136,3 +136,87 @@ def test_tensors_that_require_gradients_are_refused():
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(RuntimeError, match="paged_copy has no gradients"):
         rrt.paged_copy(i, i, [torch.zeros(2, 16, 4), torch.zeros(2, 16, 4, requires_grad=True)])
+
+
+def _struct(kind, base, changes):
+    a = kind()
+    for k, v in dict(base, **changes).items():
+        setattr(a, k, v)
+    return ctypes.byref(a)
+
+
+@pytest.mark.parametrize("struct,name", [(blocks.BoundsArgs, "paged_bounds_args"), (blocks.SelectArgs, "paged_select_args")])
+def test_ctypes_mirrors_of_arguments_follow_the_header(struct, name):
+    fields = list(_fields(name))
+    assert [n for n, _ in fields] == [f[0] for f in struct._fields_]
+    assert [s for _, s in fields] == [ctypes.sizeof(f[1]) for f in struct._fields_]
+
+
+BOUNDS = dict(k=512, block_table=256, starts=256, lengths=256, bounds=256, scales=256, page_stride=16 * 256,
+              token_stride=256, head_stride=128, bounds_page_stride=512, bounds_head_stride=256, scales_stride=2,
+              table_stride=4, num_seqs=2, num_tokens=5, num_kv_heads=2, head_dim=128, page_size=16, num_pages=4,
+              table_width=4, store=0)
+
+
+@pytest.mark.parametrize("changes,text", [
+    (dict(store=3), "store"), (dict(num_seqs=-1), "num_seqs"), (dict(num_tokens=-1), "num_tokens"),
+    (dict(num_kv_heads=0), "num_kv_heads"), (dict(head_dim=96), "head_dim"), (dict(page_size=0), "page_size"),
+    (dict(table_width=0), "table_width"), (dict(num_pages=0), "num_pages"), (dict(k=None), "null"),
+    (dict(starts=None), "null"), (dict(lengths=None), "null"), (dict(bounds=None), "null"), (dict(scales=None), "null"),
+    (dict(block_table=None), "null"), (dict(k=520), "16 bytes"), (dict(token_stride=129), "16 bytes"),
+    (dict(bounds=264), "16 bytes"), (dict(bounds_page_stride=520), "16 bytes"), (dict(page_stride=-16), "strides"),
+    (dict(starts=257), "4-byte"), (dict(store=2, head_stride=136), "16 bytes"),
+])
+def test_bounds_refuse(changes, text):
+    assert pa.load().paged_bounds(_struct(blocks.BoundsArgs, BOUNDS, changes), None) == EINVAL
+    assert text in binding.last_error()
+
+
+def test_bounds_of_nothing():
+    for changes in (dict(num_seqs=0, k=None), dict(num_tokens=0, bounds=None)):
+        assert pa.load().paged_bounds(_struct(blocks.BoundsArgs, BOUNDS, changes), None) == 0
+
+
+SELECT = dict(q=256, bounds=256, scales=256, block_table=256, lengths=256, blocks=256, q_row_stride=1024,
+              q_head_stride=128, bounds_page_stride=512, bounds_head_stride=256, scales_stride=2, table_stride=4,
+              num_rows=2, next_n=1, num_heads=8, num_kv_heads=2, head_dim=128, page_size=16, num_pages=4, table_width=4,
+              num_blocks=3, first=1, last=1, dtype=0)
+
+
+@pytest.mark.parametrize("changes,text", [
+    (dict(dtype=2), "dtype"), (dict(num_rows=-1), "num_rows"), (dict(next_n=0), "next_n"),
+    (dict(num_rows=3, next_n=2), "next_n"), (dict(num_heads=0), "num_heads"), (dict(num_kv_heads=3), "num_kv_heads"),
+    (dict(head_dim=256), "head_dim"), (dict(page_size=0), "page_size"), (dict(table_width=0), "table_width"),
+    (dict(table_width=32769), "table_width"), (dict(num_blocks=0), "num_blocks"), (dict(first=-1), "first"),
+    (dict(first=2, last=2), "at most num_blocks"), (dict(first=2147483647, last=2147483647), "at most num_blocks"),
+    (dict(num_pages=0), "num_pages"), (dict(num_rows=1 << 30), "2^31"), (dict(q=None), "null"),
+    (dict(bounds=None), "null"), (dict(scales=None), "null"), (dict(lengths=None), "null"), (dict(blocks=None), "null"),
+    (dict(block_table=None), "null"), (dict(q=264), "16 bytes"), (dict(q_head_stride=129), "16 bytes"),
+    (dict(bounds_head_stride=8), "16 bytes"), (dict(table_stride=-1), "strides"), (dict(blocks=258), "4-byte"),
+])
+def test_select_refuses(changes, text):
+    assert pa.load().paged_block_select(_struct(blocks.SelectArgs, SELECT, changes), None, None) == EINVAL
+    assert text in binding.last_error()
+
+
+def test_select_of_nothing():
+    assert pa.load().paged_block_select(_struct(blocks.SelectArgs, SELECT, dict(num_rows=0, q=None)), None, None) == 0
+
+
+def _block_attention(at=256, num_blocks=4, row=8, head=4, **changes):
+    return pa.load().paged_block_attention(ctypes.byref(_attention(**changes)), at, row, head, num_blocks, None, None)
+
+
+@pytest.mark.parametrize("changes,text", [
+    (dict(chosen=256, num_chosen=4), "chosen must be NULL"), (dict(num_blocks=0), "num_blocks"),
+    (dict(num_blocks=1 << 27), "2^30"), (dict(row=-1), "strides"), (dict(head=-1), "strides"), (dict(at=257), "4-byte"),
+    (dict(at=None), "null blocks"), (dict(page_size=0), "page_size"), (dict(head_dim=96), "head_dim"),
+    (dict(v=None), "null v"), (dict(num_kv_heads=3), "num_kv_heads"), (dict(q=264), "16 bytes"),
+])
+def test_block_attention_refuses(changes, text):
+    assert _block_attention(**changes) == EINVAL
+    assert text in binding.last_error()
+
+
+def test_block_attention_of_nothing():
+    assert _block_attention(num_rows=0, q=None, at=None) == 0
