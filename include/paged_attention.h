@@ -279,9 +279,9 @@ int paged_attention(const paged_attention_args* args, void* workspace, hipStream
  *
  * paged_bounds -- bounds of the pages that hold new tokens, from all their
  * tokens in the cache:  with hi_d, lo_d the largest and smallest key value of
- * dim d over a page's tokens and s = max_d max(|hi_d|, |lo_d|) / 127,
+ * dim d over a page's tokens and s = max_d max(|hi_d|, |lo_d|) * (1 / 127),
  *   bounds[page, head] = [ceil(hi_d / s) .., floor(lo_d / s) ..], scales = s
- * (quotients in fp32, clamped to [-127, 127]; all zeros where s is 0).  NaN is
+ * (in fp32, 1 / 127 rounded first; clamped to [-127, 127]; all zeros where s is 0).  NaN is
  * passed over, infinities count as the type's largest value.  The scale of an
  * e4m3 cache is not part of it: it multiplies all of a head's scores.
  *
@@ -322,7 +322,7 @@ int paged_bounds(const paged_bounds_args* args, hipStream_t stream);
  * Block b's score is
  *   max over the heads h of the key-value head:
  *     (float)(sum_d max(Q_hd B_d, Q_hd b_d)) * s_h * s_b
- * with B, b the block's bounds and s_b their scale, s_h = max_d |q_hd| / 127 and
+ * with B, b the block's bounds and s_b their scale, s_h = max_d |q_hd| * (1 / 127) and
  * Q_hd = q_hd / s_h rounded to nearest even: whole numbers but for the scales,
  * so that equal inputs give equal choices everywhere.  Ties go to the lower
  * block.  Blocks [0, first) and the last `last` of the row come before all

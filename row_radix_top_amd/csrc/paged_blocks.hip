@@ -4,6 +4,10 @@
 
 namespace rrt {
 
+// A scale is the largest magnitude times this rounded number, here and wherever
+// the same bounds are formed.
+constexpr float kOver127 = 1.0f / 127.0f;
+
 using i32x4 = int __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float as_e4m3(uint32_t w, int i) {
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(kBlocksBlock) bounds_kernel(BoundsParams p) {
   }
 #pragma unroll
   for (int off = 1; off < LPR; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-  const float scale = top / 127.0f, by = scale == 0.0f ? 1.0f : scale;
+  const float scale = top * kOver127, by = scale == 0.0f ? 1.0f : scale;
   uint32_t up[E / 4], down[E / 4];
 #pragma unroll
   for (int i = 0; i < E / 4; ++i) {
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kBlocksBlock) select_kernel(SelectParams p) {
           }
         }
       top = max_xor32(max_xor16(top));
-      by[t] = top / 127.0f;
+      by[t] = top * kOver127;
       const float div = by[t] == 0.0f ? 1.0f : by[t];
 #pragma unroll
       for (int i = 0; i < QS; ++i)

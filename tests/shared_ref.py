@@ -85,6 +85,7 @@ def padded(x, n, fill=-1):
 # Bounds and the choice of blocks: whole numbers and fp32 roundings as defined
 # ---------------------------------------------------------------------------
 
+OVER_127 = np.float32(1) / np.float32(127)
 LARGEST = {"bfloat16": 3.3895313892515355e38, "float16": 65504.0, "float8_e4m3fn": 448.0}
 
 
@@ -94,7 +95,7 @@ def bounds(keys, largest):
     none = np.isnan(k).all(axis=0)
     hi = np.where(none, 0, np.nanmax(np.where(none, 0, k), axis=0)).astype(np.float32)
     lo = np.where(none, 0, np.nanmin(np.where(none, 0, k), axis=0)).astype(np.float32)
-    scale = np.float32(max(np.abs(hi).max(), np.abs(lo).max())) / np.float32(127)
+    scale = np.float32(max(np.abs(hi).max(), np.abs(lo).max())) * OVER_127
     by = scale if scale != 0 else np.float32(1)
     return np.stack([np.clip(np.ceil(hi / by), -127, 127), np.clip(np.floor(lo / by), -127, 127)]), scale
 
@@ -102,7 +103,7 @@ def bounds(keys, largest):
 def scores(q, bound, scale, largest):
     """q [heads, dim] float32, bound [blocks, 2, dim] whole, scale [blocks] float32: a float32 score a block."""
     q = np.where(np.isnan(q), 0, np.clip(q, -largest, largest)).astype(np.float32)
-    by = (np.abs(q).max(axis=1) / np.float32(127)).astype(np.float32)
+    by = (np.abs(q).max(axis=1) * OVER_127).astype(np.float32)
     whole = np.clip(np.rint(q / np.where(by == 0, np.float32(1), by)[:, None]), -127, 127).astype(np.int64)
     hi, lo = bound[:, 0].astype(np.int64), bound[:, 1].astype(np.int64)
     total = np.maximum(whole, 0) @ hi.T + np.minimum(whole, 0) @ lo.T
