@@ -272,6 +272,29 @@ int paged_attention_workspace_size(const paged_attention_args* args, hipStream_t
 int paged_attention(const paged_attention_args* args, void* workspace, hipStream_t stream);
 
 /*
+ * paged_prefix_attention -- paged_attention of sequences that share their first
+ * positions (samples of one prompt, requests behind one system prompt): what is
+ * shared is read once for a group instead of once for each sequence.
+ *
+ *   group_starts  int32 [num_groups + 1], ascending: sequences
+ *                 [group_starts[g], group_starts[g + 1]) are group g.  (A
+ *                 sequence is a row of the block table: next_n rows of q.)
+ *   shared        int32 [num_groups]: how many first positions the group's
+ *                 sequences share, clamped to [0, table_width * page_size].
+ *                 Their table entries for these are alike; those of the first
+ *                 one that takes part are read.
+ *
+ * A sequence with a row shorter than that takes no part and is attended whole,
+ * by itself, as is one that no group holds.  args->chosen is NULL; max_splits
+ * holds for the shared and for the own positions of a row, at most 32 parts
+ * each.  num_groups = 0 is paged_attention.
+ */
+int paged_prefix_attention_workspace_size(const paged_attention_args* args, int32_t num_groups, hipStream_t stream,
+                                          size_t* bytes);
+int paged_prefix_attention(const paged_attention_args* args, const int32_t* group_starts, const int32_t* shared,
+                           int32_t num_groups, void* workspace, hipStream_t stream);
+
+/*
  * Attention over pages that a cheap score chooses.  paged_bounds keeps, for each
  * page and key-value head, the largest and the smallest value of every key dim
  * in 8 bits; paged_block_select scores a row's pages by what no key between the

@@ -38,6 +38,7 @@ from .attention import (  # noqa: F401
     paged_append,
     paged_attention,
     paged_layout,
+    paged_prefix_attention,
 )
 from .pages import (  # noqa: F401
     Compact,

@@ -29,6 +29,7 @@ EXPORTED = (
     "paged_debug_place", "paged_debug_split", "paged_fork", "paged_copy", "paged_free", "paged_free_workspace_size",
     "paged_compact", "paged_compact_workspace_size", "paged_bounds", "paged_block_select",
     "paged_block_select_workspace_size", "paged_block_attention", "paged_block_attention_workspace_size",
+    "paged_prefix_attention", "paged_prefix_attention_workspace_size",
 )
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -96,6 +97,8 @@ def load() -> ctypes.CDLL:
         lib.paged_compact.argtypes = [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
                                       _vp]
         lib.paged_free_workspace_size.argtypes = lib.paged_compact_workspace_size.argtypes = [_i32, size]
+        lib.paged_prefix_attention.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp]
+        lib.paged_prefix_attention_workspace_size.argtypes = [_vp, _i32, _vp, size]
         lib.paged_bounds.argtypes = [_vp, _vp]
         lib.paged_block_select.argtypes = [_vp, _vp, _vp]
         lib.paged_block_select_workspace_size.argtypes = [_vp, _vp, size]
@@ -383,9 +386,9 @@ def _attend(entry: str, q, k, v, scales, lengths, block_table, chosen, next_n, s
 
 
 def _paged(entry: str, q, k_cache, v_cache, block_table, lengths, chosen, softmax_scale, k_scale, v_scale, next_n, out, lse,
-           workspace, max_splits: int, blocks=None):
-    """The attentions over a cache of keys and values.  blocks: pointer, strides
-    and number of the chosen blocks."""
+           workspace, max_splits: int, more=()):
+    """The attentions over a cache of keys and values.  more: further arguments
+    of the entry point, the last of them its size's too."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
     if v_cache.dtype is not k_cache.dtype or v_cache.get_device() != q.get_device():
@@ -393,10 +396,9 @@ def _paged(entry: str, q, k_cache, v_cache, block_table, lengths, chosen, softma
     kv, dim = k_cache.shape[2], k_cache.shape[3]
     if kv < 1 or q.dim() != 3 or q.shape[1] % kv != 0:
         raise ValueError("q's heads must be a multiple of the cache's")
-    more = {} if blocks is None else dict(key=(blocks[3],), size_args=(blocks[3],), more=blocks)
     return _attend(entry, q, k_cache, v_cache, (("k_scale", k_scale, kv), ("v_scale", v_scale, kv)), lengths, block_table,
                    chosen, next_n, dim ** -0.5 if softmax_scale is None else softmax_scale, kv, dim, out, lse, workspace,
-                   max_splits, **more)
+                   max_splits, more[-1:], more[-1:], more)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, softmax_scale: float | None = None,
@@ -426,6 +428,30 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, *, chosen=None, s
                                    out=out, lse=lse, workspace=workspace, max_splits=max_splits)
     return _paged("paged_attention", q, k_cache, v_cache, block_table, lengths, chosen, softmax_scale, k_scale, v_scale,
                   next_n, out, lse, workspace, max_splits)
+
+
+def paged_prefix_attention(q, k_cache, v_cache, block_table, lengths, group_starts, shared, *,
+                           softmax_scale: float | None = None, k_scale=None, v_scale=None, next_n: int | None = None,
+                           out=None, lse=None, workspace=None, max_splits: int = 0, stream=None):
+    """paged_attention of sequences that share their first positions: sequences
+    [group_starts[g], group_starts[g + 1]) (int32 [num_groups + 1], ascending)
+    have the same table entries for their first shared[g] (int32 [num_groups])
+    positions, which are read once for all of them.  Sequences that are shorter,
+    or in no group, are attended by themselves.  Returns (out, lse); all other
+    arguments as for paged_attention."""
+    load()
+    if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad
+            or (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
+        _no_gradients("paged_prefix_attention")
+    if _elsewhere(q, stream):
+        with _on(stream, q):
+            return paged_prefix_attention(q, k_cache, v_cache, block_table, lengths, group_starts, shared,
+                                          softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale, next_n=next_n,
+                                          out=out, lse=lse, workspace=workspace, max_splits=max_splits)
+    dev, groups = q.get_device(), shared.numel()
+    return _paged("paged_prefix_attention", q, k_cache, v_cache, block_table, lengths, None, softmax_scale, k_scale, v_scale,
+                  next_n, out, lse, workspace, max_splits,
+                  (_ints(group_starts, "group_starts", dev, groups + 1), _ints(shared, "shared", dev, groups), groups))
 
 
 def latent_attention(q, cache, block_table, lengths, *, softmax_scale: float, chosen=None, scale=None,

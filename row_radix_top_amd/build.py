@@ -43,7 +43,7 @@ HIP_FLAGS = [
 # read.  Without it, rescaling an accumulator anywhere in a loop moves all of
 # them between the halves on every pass.
 MATRIX_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-MATRIX_FILES = ("paged_attention.hip", "paged_blocks.hip", "latent_attention.hip", "latent_prefill.hip")
+MATRIX_FILES = ("paged_attention.hip", "paged_blocks.hip", "paged_prefix.hip", "latent_attention.hip", "latent_prefill.hip")
 
 
 def hipcc() -> str:

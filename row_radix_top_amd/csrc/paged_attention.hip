@@ -107,8 +107,9 @@ struct Flag {
 };
 
 template <typename T, bool F8, int D, int MODE, int NT>
-__global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows ? 3 : 2) attn_kernel(AttnParams p) {
+__global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows && MODE != kOwnManyRows ? 3 : 2) attn_kernel(AttnParams p) {
   constexpr bool CHOSEN = MODE == kChosen || MODE == kBlocks;
+  constexpr bool OWN = MODE == kOwnOneRow || MODE == kOwnManyRows, ROWS = MODE == kManyRows || MODE == kOwnManyRows;
   constexpr int KS = D / 32;  // matrix steps over the key dims
   constexpr int VD = D / 16;  // value dims of a lane
   constexpr int SZ = F8 ? 1 : 2;
@@ -129,9 +130,10 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows ? 3 :
   const int32_t heads_per = a.num_heads / a.num_kv_heads;
 
   const int32_t n = CHOSEN ? a.num_chosen : group_length(p, r0, most, lane);
-  const Split sp = split_of(n, p.most, p.least, p.unit);
+  const int32_t from = OWN ? shared_of(p, group, most, lane) : 0;  // rows of a sequence are a group here
+  const Split sp = split_of(n - from, p.most, p.least, p.unit);
   if (part >= sp.parts) return;
-  const int32_t begin = part * sp.chunk;
+  const int32_t begin = from + part * sp.chunk;
   const int32_t end = n - begin < sp.chunk ? n : begin + sp.chunk;
 
   // Columns: (row of the group, head of the key-value head).
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows ? 3 :
     // Ragged tiles come last and in a loop of their own: the copies of the
     // sums that they need cost the others registers and spills (32 x 2 rows of
     // 16384 positions, 64 heads on 4, a call: 329 us against 229, e4m3 240 against 129).
-    if constexpr (MODE == kManyRows) {
+    if constexpr (ROWS) {
       while (more && t + kTok <= shortest) step(Flag<false>{});
       while (more) step(Flag<true>{});
     } else {
@@ -379,12 +381,12 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows ? 3 :
         x += so[k][c16][dim];
         y += so[k][c16][dim + 1];
       }
-      if (sp.parts == 1) {
+      if (sp.parts == 1 && from == 0) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         *(uint32_t*)((uint16_t*)a.out + at * D + dim) = T::pack(x * inv, y * inv);
         if (dim == 0 && a.lse != nullptr) a.lse[at] = sum == 0.0f ? -INFINITY : (cm - T::kLift + __log2f(sum)) * kLn2;
       } else {
-        const int64_t pi = at * p.most + part;
+        const int64_t pi = OWN ? at * p.pitch + p.shared_most + part : at * p.most + part;
         *(float2*)(p.part_out + pi * D + dim) = float2{x, y};
         if (dim == 0) p.part_stat[pi] = float2{cm - T::kLift, sum};
       }
@@ -480,7 +482,9 @@ template <typename T, bool F8, int D>
 const void* attn_modes(int mode, int tiles) {
   return mode == kOneRow ? attn_tiles<T, F8, D, kOneRow>(tiles)
        : mode == kManyRows ? attn_tiles<T, F8, D, kManyRows>(tiles)
-       : mode == kChosen ? attn_tiles<T, F8, D, kChosen>(tiles) : attn_tiles<T, F8, D, kBlocks>(tiles);
+       : mode == kChosen ? attn_tiles<T, F8, D, kChosen>(tiles)
+       : mode == kBlocks ? attn_tiles<T, F8, D, kBlocks>(tiles)
+       : mode == kOwnOneRow ? attn_tiles<T, F8, D, kOwnOneRow>(tiles) : attn_tiles<T, F8, D, kOwnManyRows>(tiles);
 }
 template <typename T, bool F8>
 const void* attn_dims(int head_dim, int mode, int tiles) {

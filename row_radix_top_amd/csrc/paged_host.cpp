@@ -205,6 +205,95 @@ int run_attention(const paged_attention_args* a, bool latent, void* workspace, h
                 stream, "join of split rows");
 }
 
+// ---------------------------------------------------------------------------
+// Shared prefixes
+// ---------------------------------------------------------------------------
+
+// Parts of a row's shared positions and of its own, at most: a join's wavefront
+// has a lane for each.
+constexpr int32_t kMostSharedParts = 32, kMostOwnParts = 32;
+constexpr int32_t kSharedLeast = 256;  // positions of a shared part
+
+struct PrefixPlan {
+  rrt::AttnParams p;
+  const void *shared_fn, *own_fn;
+  int64_t shared_grid, own_grid;
+  size_t bytes;
+};
+
+int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, const int32_t* shared, int32_t num_groups,
+                hipStream_t stream, PrefixPlan* out, size_t* reserve = nullptr) {
+  if (int rc = check_attention(a, false)) return rc;
+  REQUIRE(a->chosen == nullptr, "chosen must be NULL");
+  REQUIRE(num_groups >= 1, "num_groups must be >= 0");
+  REQUIRE(group_starts != nullptr && shared != nullptr, "null group_starts or shared");
+  REQUIRE(aligned(group_starts, 4) && aligned(shared, 4), "group_starts and shared must be 4-byte aligned");
+  std::memset(out, 0, sizeof(*out));
+  if (reserve != nullptr) *reserve = 0;
+  if (a->num_rows == 0) return TOPK_OK;
+  int dev = 0, cus = 0;
+  if (int rc = rrt::device_of_stream(stream, &dev, &cus)) return rc;
+  rrt::AttnParams& p = out->p;
+  p.a = *a;
+  p.scale_log2 = a->softmax_scale * kLog2e;
+  p.page = rrt::divisor_of(a->page_size);
+  p.group_starts = group_starts;
+  p.shared = shared;
+  p.num_groups = num_groups;
+  const int32_t per = a->num_heads / a->num_kv_heads;
+  const int64_t seqs = a->num_rows / a->next_n, all = (int64_t)a->num_rows * per;
+  const int64_t longest = rrt::table_tokens(a->table_width, a->page_size);
+
+  auto limited = [&](int64_t parts, int64_t least, int32_t most) {
+    if (a->max_splits > 0) parts = a->max_splits;
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>({parts, (int64_t)most, longest / least}));
+  };
+
+  // The shared part: wavefronts along the columns as far as a group has them.
+  const int64_t each = ceil_div(all, num_groups);
+  const int waves = each > 64 ? 4 : each > 32 ? 2 : 1;
+  auto shared_parts = [&](int64_t seqs, int waves) {
+    const int64_t units = ceil_div(seqs * a->next_n * per, 32 * waves) * a->num_kv_heads;
+    return limited(ceil_div(2 * cus, units), kSharedLeast, kMostSharedParts);
+  };
+  p.shared_tiles = (int32_t)std::min<int64_t>(all / (32 * waves) + num_groups, INT32_MAX);
+  p.shared_unit = rrt::prefix_unit(waves);
+  p.shared_least = kSharedLeast;
+  p.shared_most = shared_parts(seqs, waves);
+  out->shared_fn = rrt::prefix_kernel_ptr(a->dtype, a->store, a->head_dim, waves);
+  out->shared_grid = ceil_div((int64_t)p.shared_most * a->num_kv_heads, 8) * 8 * p.shared_tiles;
+
+  // The rows' own: as paged_attention.
+  const int64_t columns = (int64_t)a->next_n * per;
+  const int tiles = columns > 16 ? 2 : 1;
+  p.unit = kUnit;
+  p.least = kLeast;
+  p.group_rows = a->next_n;
+  p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
+  p.groups = (int32_t)seqs;
+  const int64_t inner = (int64_t)a->num_kv_heads * p.col_tiles;
+  auto own_parts = [&](int64_t seqs) {
+    return limited(parts_for(false, false, seqs * inner, longest, cus), p.least, kMostOwnParts);
+  };
+  p.most = own_parts(seqs);
+  p.pitch = p.shared_most + p.most;
+  out->own_fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, a->next_n > 1 ? rrt::kOwnManyRows : rrt::kOwnOneRow, tiles);
+  out->own_grid = ceil_div(seqs * p.most, 8) * 8 * inner;
+  const size_t part_bytes = a->head_dim * sizeof(float) + sizeof(float2);
+  auto bytes_for = [&](int64_t seqs, int64_t pitch) { return (size_t)(seqs * a->next_n * a->num_heads * pitch) * part_bytes; };
+  out->bytes = bytes_for(seqs, p.pitch);
+  if (reserve == nullptr) return TOPK_OK;
+  // Fewer rows, or as many in fewer groups, may be split into more parts each.
+  // Past two units a CU the rules give every number of rows as many parts.
+  *reserve = out->bytes;
+  for (int w : {1, 2, 4}) {
+    *reserve = std::max(*reserve, bytes_for(seqs, shared_parts(seqs, w) + own_parts(seqs)));
+    for (int64_t n = std::min<int64_t>(seqs, 64 * w * (int64_t)cus + 1); n > 0; --n)
+      *reserve = std::max(*reserve, bytes_for(n, shared_parts(n, w) + own_parts(n)));
+  }
+  return TOPK_OK;
+}
+
 // The arguments of paged_attention over the tokens of num_blocks chosen blocks.
 int block_args(const paged_attention_args* a, const int32_t* blocks, int64_t row_stride, int64_t head_stride,
                int32_t num_blocks, paged_attention_args* out) {
@@ -542,6 +631,34 @@ int paged_block_attention(const paged_attention_args* args, const int32_t* block
   paged_attention_args a;
   if (int rc = block_args(args, blocks, blocks_row_stride, blocks_head_stride, num_blocks, &a)) return rc;
   return run_attention(&a, false, workspace, stream, &blocks_head_stride);
+}
+
+int paged_prefix_attention_workspace_size(const paged_attention_args* args, int32_t num_groups, hipStream_t stream,
+                                          size_t* bytes) {
+  REQUIRE(bytes != nullptr, "null bytes");
+  REQUIRE(num_groups >= 0, "num_groups must be >= 0");
+  if (num_groups == 0) return paged_attention_workspace_size(args, stream, bytes);
+  const int32_t* any = reinterpret_cast<const int32_t*>(16);
+  PrefixPlan plan;
+  return plan_prefix(args, any, any, num_groups, stream, &plan, bytes);
+}
+
+int paged_prefix_attention(const paged_attention_args* args, const int32_t* group_starts, const int32_t* shared,
+                           int32_t num_groups, void* workspace, hipStream_t stream) {
+  REQUIRE(num_groups >= 0, "num_groups must be >= 0");
+  if (num_groups == 0) return run_attention(args, false, workspace, stream);
+  PrefixPlan plan;
+  if (int rc = plan_prefix(args, group_starts, shared, num_groups, stream, &plan)) return rc;
+  if (args->num_rows == 0) return TOPK_OK;
+  if (int rc = check_workspace(workspace, plan.bytes)) return rc;
+  rrt::AttnParams& p = plan.p;
+  const int64_t outputs = (int64_t)args->num_rows * args->num_heads;
+  p.part_out = static_cast<float*>(workspace);
+  p.part_stat = reinterpret_cast<float2*>(p.part_out + outputs * p.pitch * args->head_dim);
+  const char* name = "paged_prefix_attention";
+  if (int rc = launch(plan.shared_fn, plan.shared_grid, 256, &p, stream, name)) return rc;
+  if (int rc = launch(plan.own_fn, plan.own_grid, 256, &p, stream, name)) return rc;
+  return launch(rrt::prefix_join_kernel_ptr(args->dtype, args->head_dim), ceil_div(outputs, 4), 256, &p, stream, name);
 }
 
 int paged_bounds(const paged_bounds_args* args, hipStream_t stream) {

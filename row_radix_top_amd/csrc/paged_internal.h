@@ -173,6 +173,14 @@ struct AttnParams {
   int32_t col_tiles;   // column tiles of a key-value head
   Divisor page;        // by page_size
   int64_t chosen_head_stride;  // blocks: a key-value head's, in a.chosen
+  // Shared prefixes: sequences [group_starts[g], group_starts[g + 1]) have their
+  // first shared[g] positions alike.  A row's parts in the workspace are
+  // shared_most of those and then `most` of its own, `pitch` in all.
+  const int32_t *group_starts, *shared;
+  int32_t num_groups;
+  int32_t shared_most, shared_least, shared_unit;
+  int32_t shared_tiles;  // tiles of columns that the grid covers
+  int32_t pitch;
 };
 
 // The expanded form works on tiles of kCtxTile context tokens; a sequence
@@ -215,7 +223,11 @@ const void* pool_kernel_ptr(int step);
 // What a row of the attention over a cache reads: all its positions (kOneRow: a
 // sequence has one row; kManyRows: several, which share the reads but may end at
 // different places), or chosen positions, or chosen blocks.
-enum { kOneRow, kManyRows, kChosen, kBlocks };
+// Own: the positions behind those that the sequence shares.
+enum { kOneRow, kManyRows, kChosen, kBlocks, kOwnOneRow, kOwnManyRows };
+const void* prefix_kernel_ptr(int dtype, int store, int head_dim, int waves);
+const void* prefix_join_kernel_ptr(int dtype, int head_dim);
+int prefix_unit(int waves);  // tokens that a part is a multiple of
 const void* attn_kernel_ptr(int dtype, int store, int head_dim, int mode, int tiles);
 const void* bounds_kernel_ptr(int store, int head_dim);
 const void* select_kernel_ptr(int dtype, int head_dim, int tiles, bool split);

@@ -220,3 +220,23 @@ def test_block_attention_refuses(changes, text):
 
 def test_block_attention_of_nothing():
     assert _block_attention(num_rows=0, q=None, at=None) == 0
+
+
+def _prefix(starts=256, shared=256, groups=2, **changes):
+    return pa.load().paged_prefix_attention(ctypes.byref(_attention(**changes)), starts, shared, groups, None, None)
+
+
+@pytest.mark.parametrize("changes,text", [
+    (dict(groups=-1), "num_groups"), (dict(starts=None), "null group_starts"), (dict(shared=None), "null group_starts"),
+    (dict(starts=257), "4-byte"), (dict(shared=258), "4-byte"), (dict(chosen=256, num_chosen=4), "chosen must be NULL"),
+    (dict(head_dim=96), "head_dim"), (dict(v=None), "null v"), (dict(num_kv_heads=3), "num_kv_heads"),
+    (dict(q=264), "16 bytes"), (dict(max_splits=129), "max_splits"), (dict(groups=0, head_dim=96), "head_dim"),
+])
+def test_prefix_attention_refuses(changes, text):
+    assert _prefix(**changes) == EINVAL
+    assert text in binding.last_error()
+
+
+def test_prefix_attention_of_nothing():
+    assert _prefix(num_rows=0, q=None) == 0
+    assert _prefix(num_rows=0, q=None, groups=0, starts=None, shared=None) == 0
