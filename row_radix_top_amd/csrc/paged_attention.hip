@@ -121,17 +121,31 @@ __global__ void __launch_bounds__(kAttnBlock, NT == 1 && MODE != kManyRows && MO
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 
   Work work;
-  if (!work_of<CHOSEN>(blockIdx.x, (uint32_t)(a.num_kv_heads * p.col_tiles), (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
   const int64_t most = table_tokens(a.table_width, a.page_size);
+  int32_t group;
+  if constexpr (OWN) {
+    // No workgroup but the last few is without work: a part that is none, found
+    // out after two reads, costs its launch all the same (64 rows of 490 own
+    // positions, 8 heads: 36 us with one part a row, 125 with 16 of which 15 are
+    // none).
+    const uint32_t inner = (uint32_t)(a.num_kv_heads * p.col_tiles), idx = blockIdx.x >> 3, eight = idx / inner;
+    const int32_t item = (int32_t)(eight * 8 + (blockIdx.x & 7));
+    if (item >= p.planned->items) return;
+    const PrefixItem it = p.items[item];
+    work = {it.seq, it.part, (int32_t)(idx - eight * inner)};
+    group = it.seq;
+  } else {
+    if (!work_of<CHOSEN>(blockIdx.x, (uint32_t)(a.num_kv_heads * p.col_tiles), (uint32_t)p.groups, (uint32_t)p.most, &work)) return;
+    group = CHOSEN ? work.group : by_length(a, work.group, p.groups, p.group_rows, most, lane);
+  }
   const int32_t part = work.part;
-  const int32_t group = CHOSEN ? work.group : by_length(a, work.group, p.groups, p.group_rows, most, lane);
   const int32_t kvh = work.unit % a.num_kv_heads, tile = work.unit / a.num_kv_heads;
   const int32_t r0 = group * p.group_rows;
   const int32_t heads_per = a.num_heads / a.num_kv_heads;
 
-  const int32_t n = CHOSEN ? a.num_chosen : group_length(p, r0, most, lane);
-  const int32_t from = OWN ? shared_of(p, group, most, lane) : 0;  // rows of a sequence are a group here
-  const Split sp = split_of(n - from, p.most, p.least, p.unit);
+  const int32_t n = CHOSEN ? a.num_chosen : MODE == kOwnOneRow ? clamp_to(a.lengths[r0], most) : group_length(p, r0, most, lane);
+  const int32_t from = OWN ? p.share[group] : 0;  // rows of a sequence are a group here
+  const Split sp = OWN ? split_by(n - from, p.planned->own_part, p.most, p.unit) : split_of(n, p.most, p.least, p.unit);
   if (part >= sp.parts) return;
   const int32_t begin = from + part * sp.chunk;
   const int32_t end = n - begin < sp.chunk ? n : begin + sp.chunk;

@@ -221,21 +221,6 @@ __device__ __forceinline__ int32_t by_length(const paged_attention_args& a, int3
 
 // --- shared prefixes -----------------------------------------------------------
 
-// The last index below n whose value is <= x, of values in ascending order; -1 if
-// there is none.  All lanes of the wavefront take part, 64 probes at a time.
-__device__ __forceinline__ int32_t last_at_most(const int32_t* values, int32_t n, int32_t x, int lane) {
-  int32_t at = 0;
-  while (true) {
-    const int32_t step = (n + 63) / 64, i = lane * step;
-    const uint64_t below = __builtin_amdgcn_ballot_w64(i < n && values[at + i] <= x);
-    if (below == 0) return at - 1;
-    const int32_t c = __builtin_popcountll(below) - 1;
-    at += c * step;
-    n = n - c * step < step ? n - c * step : step;
-    if (step == 1) return at;
-  }
-}
-
 // First sequence of group g and how many it has.
 __device__ __forceinline__ void group_of(const AttnParams& p, int32_t g, int32_t* first, int32_t* count) {
   const int32_t seqs = p.a.num_rows / p.a.next_n;
@@ -249,17 +234,6 @@ __device__ __forceinline__ bool takes_part(const paged_attention_args& a, int32_
   bool in = true;
   for (int32_t j = 0; j < a.next_n; ++j) in = in && clamp_to(a.lengths[(int64_t)seq * a.next_n + j], most) >= n;
   return in;
-}
-
-// How many positions the sequence shares: its group's, 0 if it has no group or
-// takes no part.  Wave uniform.
-__device__ __forceinline__ int32_t shared_of(const AttnParams& p, int32_t seq, int64_t most, int lane) {
-  const int32_t g = last_at_most(p.group_starts, p.num_groups, seq, lane);
-  if (g < 0) return 0;
-  int32_t first, count;
-  group_of(p, g, &first, &count);
-  const int32_t n = clamp_to(p.shared[g], most);
-  return __builtin_amdgcn_readfirstlane(seq >= first && seq - first < count && takes_part(p.a, seq, n, most) ? n : 0);
 }
 
 constexpr float kLn2 = 0.69314718055994530942f;

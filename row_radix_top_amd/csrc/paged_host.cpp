@@ -212,7 +212,6 @@ int run_attention(const paged_attention_args* a, bool latent, void* workspace, h
 // Parts of a row's shared positions and of its own, at most: a join's wavefront
 // has a lane for each.
 constexpr int32_t kMostSharedParts = 32, kMostOwnParts = 32;
-constexpr int32_t kSharedLeast = 256;  // positions of a shared part
 
 struct PrefixPlan {
   rrt::AttnParams p;
@@ -244,26 +243,35 @@ int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, cons
   const int64_t seqs = a->num_rows / a->next_n, all = (int64_t)a->num_rows * per;
   const int64_t longest = rrt::table_tokens(a->table_width, a->page_size);
 
+  // Both kinds of positions are shared out to two workgroups a CU; how, the kernels
+  // find out from the lengths.  A part's number is bounded by what that gives a
+  // batch of rows alike, and by four times that where one may be longer.
+  p.workgroups = 2 * cus;
   auto limited = [&](int64_t parts, int64_t least, int32_t most) {
     if (a->max_splits > 0) parts = a->max_splits;
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>({parts, (int64_t)most, longest / least}));
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>({parts, (int64_t)most, ceil_div(longest, least)}));
   };
 
   // The shared part: wavefronts along the columns as far as a group has them.
   const int64_t each = ceil_div(all, num_groups);
   const int waves = each > 64 ? 4 : each > 32 ? 2 : 1;
-  auto shared_parts = [&](int64_t seqs, int waves) {
+  auto shared_parts = [&](int64_t seqs, int waves, bool one) {
     const int64_t units = ceil_div(seqs * a->next_n * per, 32 * waves) * a->num_kv_heads;
-    return limited(ceil_div(2 * cus, units), kSharedLeast, kMostSharedParts);
+    return limited(ceil_div(p.workgroups, units) * (one ? 1 : 4), 256, kMostSharedParts);
   };
-  p.shared_tiles = (int32_t)std::min<int64_t>(all / (32 * waves) + num_groups, INT32_MAX);
+  // Tiles of columns: no more than this, as every group that has any begins one.
+  const int64_t col_tiles = all <= num_groups ? all : (all - num_groups) / (32 * waves) + num_groups;
   p.shared_unit = rrt::prefix_unit(waves);
-  p.shared_least = kSharedLeast;
-  p.shared_most = shared_parts(seqs, waves);
-  out->shared_fn = rrt::prefix_kernel_ptr(a->dtype, a->store, a->head_dim, waves);
-  out->shared_grid = ceil_div((int64_t)p.shared_most * a->num_kv_heads, 8) * 8 * p.shared_tiles;
+  p.shared_most = shared_parts(seqs, waves, num_groups == 1);
+  // Sixteen tokens of one page, their bytes within 31 bits.
+  const bool p16 = a->page_size % 16 == 0 && a->token_stride < (1 << 26);
+  out->shared_fn = rrt::prefix_kernel_ptr(a->dtype, a->store, a->head_dim, waves, p16);
+  // One workgroup makes the plan.  Parts times tiles times heads are at most
+  // `workgroups` and one more for each tile and head; every group's rounds up to
+  // eight.
+  out->shared_grid = 1 + 8 * (ceil_div(p.workgroups + col_tiles * a->num_kv_heads, 8) + col_tiles);
 
-  // The rows' own: as paged_attention.
+  // The rows' own.
   const int64_t columns = (int64_t)a->next_n * per;
   const int tiles = columns > 16 ? 2 : 1;
   p.unit = kUnit;
@@ -272,24 +280,26 @@ int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, cons
   p.col_tiles = (int32_t)ceil_div(columns, 16 * tiles);
   p.groups = (int32_t)seqs;
   const int64_t inner = (int64_t)a->num_kv_heads * p.col_tiles;
-  auto own_parts = [&](int64_t seqs) {
-    return limited(parts_for(false, false, seqs * inner, longest, cus), p.least, kMostOwnParts);
-  };
+  auto own_parts = [&](int64_t seqs) { return limited(ceil_div(p.workgroups, seqs * inner) * 4, kLeast, kMostOwnParts); };
   p.most = own_parts(seqs);
   p.pitch = p.shared_most + p.most;
   out->own_fn = rrt::attn_kernel_ptr(a->dtype, a->store, a->head_dim, a->next_n > 1 ? rrt::kOwnManyRows : rrt::kOwnOneRow, tiles);
-  out->own_grid = ceil_div(seqs * p.most, 8) * 8 * inner;
+  auto items_for = [&](int64_t seqs) { return seqs + ceil_div(p.workgroups, inner); };
+  out->own_grid = ceil_div(items_for(seqs), 8) * 8 * inner;
   const size_t part_bytes = a->head_dim * sizeof(float) + sizeof(float2);
-  auto bytes_for = [&](int64_t seqs, int64_t pitch) { return (size_t)(seqs * a->next_n * a->num_heads * pitch) * part_bytes; };
+  auto bytes_for = [&](int64_t seqs, int64_t pitch) {
+    return (size_t)(seqs * a->next_n * a->num_heads * pitch) * part_bytes + sizeof(rrt::PrefixPlanned) +
+           (size_t)ceil_div(seqs, 4) * 16 + (size_t)items_for(seqs) * sizeof(rrt::PrefixItem);
+  };
   out->bytes = bytes_for(seqs, p.pitch);
   if (reserve == nullptr) return TOPK_OK;
   // Fewer rows, or as many in fewer groups, may be split into more parts each.
   // Past two units a CU the rules give every number of rows as many parts.
   *reserve = out->bytes;
   for (int w : {1, 2, 4}) {
-    *reserve = std::max(*reserve, bytes_for(seqs, shared_parts(seqs, w) + own_parts(seqs)));
+    *reserve = std::max(*reserve, bytes_for(seqs, shared_parts(seqs, w, false) + own_parts(seqs)));
     for (int64_t n = std::min<int64_t>(seqs, 64 * w * (int64_t)cus + 1); n > 0; --n)
-      *reserve = std::max(*reserve, bytes_for(n, shared_parts(n, w) + own_parts(n)));
+      *reserve = std::max(*reserve, bytes_for(n, shared_parts(n, w, false) + own_parts(n)));
   }
   return TOPK_OK;
 }
@@ -653,8 +663,13 @@ int paged_prefix_attention(const paged_attention_args* args, const int32_t* grou
   if (int rc = check_workspace(workspace, plan.bytes)) return rc;
   rrt::AttnParams& p = plan.p;
   const int64_t outputs = (int64_t)args->num_rows * args->num_heads;
-  p.part_out = static_cast<float*>(workspace);
+  // The plan first, so that all of it is aligned.
+  const int64_t seqs = args->num_rows / args->next_n;
+  p.planned = static_cast<rrt::PrefixPlanned*>(workspace);
+  p.share = reinterpret_cast<int32_t*>(p.planned + 1);
+  p.part_out = reinterpret_cast<float*>(p.share + ceil_div(seqs, 4) * 4);
   p.part_stat = reinterpret_cast<float2*>(p.part_out + outputs * p.pitch * args->head_dim);
+  p.items = reinterpret_cast<rrt::PrefixItem*>(p.part_stat + outputs * p.pitch);
   const char* name = "paged_prefix_attention";
   if (int rc = launch(plan.shared_fn, plan.shared_grid, 256, &p, stream, name)) return rc;
   if (int rc = launch(plan.own_fn, plan.own_grid, 256, &p, stream, name)) return rc;

@@ -79,6 +79,24 @@ RRT_HD Split split_of(int32_t n, int32_t most, int32_t least, int32_t unit) {
   return {parts < 1 ? 1 : (int32_t)parts, (int32_t)chunk};
 }
 
+// The same by a part's positions: parts of about `want` positions each.
+RRT_HD Split split_by(int32_t n, int32_t want, int32_t most, int32_t unit) {
+  uint32_t parts = ((uint32_t)n + (uint32_t)want - 1) / (uint32_t)want;
+  if (parts > (uint32_t)most) parts = (uint32_t)most;
+  if (parts < 1) parts = 1;
+  const uint32_t per = ((uint32_t)n + parts - 1) / parts;
+  uint32_t chunk = (per + (uint32_t)unit - 1) / (uint32_t)unit * (uint32_t)unit;
+  if (chunk < (uint32_t)unit) chunk = (uint32_t)unit;
+  return {(int32_t)(((uint32_t)n + chunk - 1) / chunk), (int32_t)chunk};
+}
+// Positions of a part: a `share`-th of all there are to read (positions times
+// workgroups), in units, no fewer than `least`.
+RRT_HD int32_t part_size(int64_t all, int32_t share, int32_t least, int32_t unit) {
+  int64_t n = (all + share - 1) / share;
+  n = n < least ? least : n > kMostTokens ? kMostTokens : n;
+  return (int32_t)((n + unit - 1) / unit * unit);
+}
+
 // ---------------------------------------------------------------------------
 // Kernel parameters
 // ---------------------------------------------------------------------------
@@ -160,6 +178,16 @@ struct SelectParams {
   Divisor page;
 };
 
+// What the launch over shared positions finds out for those behind it.
+struct PrefixPlanned {
+  int32_t items;                  // own parts, of all sequences
+  int32_t own_part, shared_part;  // positions of each
+  int32_t none;
+};
+struct PrefixItem {
+  int32_t seq, part;
+};
+
 struct AttnParams {
   paged_attention_args a;
   float* part_out;     // [rows, heads, most, head_dim], unnormalised
@@ -178,9 +206,12 @@ struct AttnParams {
   // shared_most of those and then `most` of its own, `pitch` in all.
   const int32_t *group_starts, *shared;
   int32_t num_groups;
-  int32_t shared_most, shared_least, shared_unit;
-  int32_t shared_tiles;  // tiles of columns that the grid covers
+  int32_t shared_most, shared_unit;
+  int32_t workgroups;   // that the shared and the own positions are each shared out to
   int32_t pitch;
+  PrefixPlanned* planned;
+  int32_t* share;       // [sequences]: what each shares
+  PrefixItem* items;    // the own parts there are
 };
 
 // The expanded form works on tiles of kCtxTile context tokens; a sequence
@@ -225,7 +256,7 @@ const void* pool_kernel_ptr(int step);
 // different places), or chosen positions, or chosen blocks.
 // Own: the positions behind those that the sequence shares.
 enum { kOneRow, kManyRows, kChosen, kBlocks, kOwnOneRow, kOwnManyRows };
-const void* prefix_kernel_ptr(int dtype, int store, int head_dim, int waves);
+const void* prefix_kernel_ptr(int dtype, int store, int head_dim, int waves, bool p16);
 const void* prefix_join_kernel_ptr(int dtype, int head_dim);
 int prefix_unit(int waves);  // tokens that a part is a multiple of
 const void* attn_kernel_ptr(int dtype, int store, int head_dim, int mode, int tiles);
