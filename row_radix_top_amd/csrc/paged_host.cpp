@@ -243,8 +243,8 @@ int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, cons
   const int64_t seqs = a->num_rows / a->next_n, all = (int64_t)a->num_rows * per;
   const int64_t longest = rrt::table_tokens(a->table_width, a->page_size);
 
-  // Both kinds of positions are shared out to two workgroups a CU; how, the kernels
-  // find out from the lengths.  A part's number is bounded by what that gives a
+  // Both kinds of positions are shared out to as many workgroups as run at once; how,
+  // the kernels find out from the lengths.  A part's number is bounded by what that gives a
   // batch of rows alike, and by four times that where one may be longer.
   p.workgroups = 2 * cus;
   auto limited = [&](int64_t parts, int64_t least, int32_t most) {
@@ -255,9 +255,13 @@ int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, cons
   // The shared part: wavefronts along the columns as far as a group has them.
   const int64_t each = ceil_div(all, num_groups);
   const int waves = each > 64 ? 4 : each > 32 ? 2 : 1;
+  // (One wavefront a column's tile: tiles of 128 tokens, whose workgroups have a CU's
+  // LDS to themselves.)
+  auto shared_workgroups = [&](int waves) { return waves == 1 ? cus : 2 * cus; };
+  p.shared_workgroups = shared_workgroups(waves);
   auto shared_parts = [&](int64_t seqs, int waves, bool one) {
     const int64_t units = ceil_div(seqs * a->next_n * per, 32 * waves) * a->num_kv_heads;
-    return limited(ceil_div(p.workgroups, units) * (one ? 1 : 4), 256, kMostSharedParts);
+    return limited(ceil_div(shared_workgroups(waves), units) * (one ? 1 : 4), 256, kMostSharedParts);
   };
   // Tiles of columns: no more than this, as every group that has any begins one.
   const int64_t col_tiles = all <= num_groups ? all : (all - num_groups) / (32 * waves) + num_groups;
@@ -269,7 +273,7 @@ int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, cons
   // One workgroup makes the plan.  Parts times tiles times heads are at most
   // `workgroups` and one more for each tile and head; every group's rounds up to
   // eight.
-  out->shared_grid = 1 + 8 * (ceil_div(p.workgroups + col_tiles * a->num_kv_heads, 8) + col_tiles);
+  out->shared_grid = 1 + 8 * (ceil_div(p.shared_workgroups + col_tiles * a->num_kv_heads, 8) + col_tiles);
 
   // The rows' own.
   const int64_t columns = (int64_t)a->next_n * per;

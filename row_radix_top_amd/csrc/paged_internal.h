@@ -207,7 +207,7 @@ struct AttnParams {
   const int32_t *group_starts, *shared;
   int32_t num_groups;
   int32_t shared_most, shared_unit;
-  int32_t workgroups;   // that the shared and the own positions are each shared out to
+  int32_t shared_workgroups, workgroups;  // that the shared and the own positions are shared out to
   int32_t pitch;
   PrefixPlanned* planned;
   int32_t* share;       // [sequences]: what each shares

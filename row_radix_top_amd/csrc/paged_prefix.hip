@@ -1,6 +1,8 @@
 // Attention over positions that many rows share: their keys and values are read
 // once for all of them.
 
+#include <type_traits>
+
 #include "lds_device.hpp"
 
 namespace rrt {
@@ -30,7 +32,7 @@ namespace rrt {
 constexpr float kLazyStep = 8.0f;
 // Past this a reference's own rounding shows in the difference of a score to it.
 constexpr float kFar = 1048576.0f;
-constexpr int kAhead = 4;  // operands in flight from LDS, and one in use
+constexpr int kAhead = 3;  // operands in flight from LDS, and one in use
 constexpr int32_t kSharedLeast = 256;  // positions of a part
 
 __device__ __forceinline__ int32_t prefix_scan(int32_t x, int lane) {
@@ -68,13 +70,27 @@ __device__ __forceinline__ GroupWork work_of_group(const AttnParams& p, int32_t 
 }
 __device__ __forceinline__ int32_t shared_part(const AttnParams& p, int32_t per_seq, int32_t wide, int64_t most, int lane) {
   int64_t all = 0;
+  GroupWork mine;
   for (int32_t g0 = 0; g0 < p.num_groups; g0 += 64) {
-    const GroupWork w = work_of_group(p, g0 + lane, per_seq, wide, most);
-    all += (int64_t)w.tiles * w.n;
+    mine = work_of_group(p, g0 + lane, per_seq, wide, most);
+    all += (int64_t)mine.tiles * mine.n;
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) all += shfl64(all, lane ^ off);
-  return part_size(readlane64(all, 0) * p.a.num_kv_heads, p.workgroups, kSharedLeast, p.shared_unit);
+  const int32_t part = part_size(readlane64(all, 0) * p.a.num_kv_heads, p.shared_workgroups, kSharedLeast, p.shared_unit);
+  if (p.num_groups > 64 || p.num_groups == 1) return part;
+  // Each group's last part is a short one, so that there are some more of them than
+  // workgroups that run at once, and the last few would start when the others end
+  // (twelve groups: 16 of 528, 95 us for 64).  Lane l tries l units more: the first that
+  // makes no more than run at once.
+  const float by = 1.0f / (float)(part + lane * p.shared_unit);
+  float all_of = 0.0f;
+  for (int32_t g = 0; g < p.num_groups; ++g) {
+    const float parts = __builtin_ceilf((float)__builtin_amdgcn_readlane(mine.n, g) * by);
+    all_of += fminf(parts, (float)p.shared_most) * (float)__builtin_amdgcn_readlane(mine.tiles, g);
+  }
+  const uint64_t fit = __builtin_amdgcn_ballot_w64(all_of * (float)p.a.num_kv_heads <= (float)p.shared_workgroups);
+  return fit == 0 ? part : part + __builtin_ctzll(fit) * p.shared_unit;
 }
 
 // One workgroup, beside the others: what each sequence shares, and the list of
@@ -117,7 +133,9 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, int32_t per_seq, i
   for (int off = 32; off > 0; off >>= 1) all += shfl64(all, lane ^ off);
   if (lane == 0) sums[w] = all;
   __syncthreads();
-  all = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  all = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) all += sums[k];
   const int32_t part = part_size(all * (a.num_kv_heads * p.col_tiles), p.workgroups, p.least, p.unit);
   int32_t base = 0;
   for (int32_t s0 = 0; s0 < seqs; s0 += 256) {
@@ -140,19 +158,27 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, int32_t per_seq, i
 
 template <typename T, bool F8, int D, int CW, bool P16>
 __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
-  constexpr int TB = CW == 4 ? 2 : 1;          // blocks of 32 tokens of a wavefront in a tile
-  constexpr int TW = 4 / CW;                   // wavefronts along the tokens
-  constexpr int TT = 32 * TB * TW;             // tokens of a tile
-  constexpr int QT = TT / 4;                   // and of a wavefront's loads
+  constexpr int NW = 4;                 // wavefronts
+  constexpr int TB = CW == 4 ? 2 : 1;   // blocks of 32 tokens of a wavefront in a tile
+  constexpr int TW = NW / CW;           // wavefronts along the tokens
+  constexpr int TT = 32 * TB * TW;      // tokens of a tile
+  constexpr int QT = TT / NW;           // and of a wavefront's loads
   constexpr int NP = TT / 64;                  // words of a tile's mask; tokens that a lane looks up
   constexpr int KS = D / 16, DB = D / 32;      // steps over the key dims; blocks of value dims
   constexpr uint32_t ROW = D * 2, TILE = TT * ROW;
   constexpr int SZ = F8 ? 1 : 2;
   constexpr int LPR = D * SZ / 16, RPL = 64 / LPR;  // lanes of a row's load; rows of a load
-  constexpr int NL = QT / RPL, NG = 16 / RPL;       // loads of a wavefront's quarter of a tile, of 16 tokens
-  constexpr int KB = F8 || CW == 1 ? 2 : 3;         // keys' tiles in LDS
+  constexpr int NL = QT / RPL < 1 ? 1 : QT / RPL;   // loads of a wavefront's share of a tile
+  constexpr int NG = QT < 16 ? NL : 16 / RPL;       // and of 16 tokens of it
+  static_assert(QT % RPL == 0, "whole loads");
+  // Tiles of keys and of values in LDS, and of raw e4m3 bytes: what 80 KB hold, so
+  // that two workgroups fit a CU, or (eight wavefronts, which have it to themselves)
+  // as far ahead as memory takes.
+  constexpr int KB = F8 || CW == 1 || !P16 ? 2 : 3, VB = 2;
+  constexpr int RB = F8 ? 1 : 0;
   __shared__ __align__(1024) char sk[KB][TILE];
-  __shared__ __align__(1024) char sv[2][TILE];
+  __shared__ __align__(1024) char sv[VB][TILE];
+  __shared__ __align__(1024) char sraw[F8 ? RB : 1][2][F8 ? TT * D : 16];
   const paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cw = w % CW, tw = w / CW;
@@ -249,9 +275,11 @@ __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
   const uint32_t row0 = (uint32_t)w * QT;
   constexpr int GT = TT / 16, BT = 64 / GT;
   struct Place {
-    int64_t at[P16 ? QT / 16 : NL];  // bytes: of sixteen tokens, or of the lane's row in each load
+    int64_t at[P16 ? (QT + 15) / 16 : NL];  // bytes: of sixteen tokens, or of the lane's row in each load
     uint64_t mask[NP];
-    bool whole;                      // every token counts
+    __device__ __forceinline__ bool whole() const {
+      return mask[0] == ~0ull && mask[NP - 1] == ~0ull;
+    }
   };
   int32_t page[P16 ? 1 : NP];  // of what is placed next
   uint32_t in[NP];             // and the tokens' offsets in them
@@ -273,7 +301,8 @@ __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
     }
   };
   // Tile i's places; starts the look-up of the next one's, or batch's.
-  auto place = [&](int32_t i, Place* out) {
+  auto place = [&](int32_t i) __attribute__((always_inline)) -> Place {
+    Place out;
     if constexpr (P16) {
       if (i % BT == 0) {
         const int32_t x = begin + i * TT + lane * 16, left = end - x;
@@ -286,83 +315,90 @@ __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
       }
       const int g0 = i % BT * GT;
 #pragma unroll
-      for (int g = 0; g < QT / 16; ++g) out->at[g] = readlane64(group_at, g0 + w * (QT / 16) + g);
-      out->whole = (~(group_whole >> g0) & ((1u << GT) - 1u)) == 0;
+      for (int g = 0; g < (QT + 15) / 16; ++g) out.at[g] = readlane64(group_at, g0 + (int)row0 / 16 + g);
 #pragma unroll
-      for (int k = 0; k < NP; ++k) out->mask[k] = ~0ull;
-      if (!out->whole) {
+      for (int k = 0; k < NP; ++k) out.mask[k] = ~0ull;
+      if ((~(group_whole >> g0) & ((1u << GT) - 1u)) != 0) {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          out->mask[k] = 0;
+          out.mask[k] = 0;
 #pragma nounroll
           for (int g = 0; g < 4; ++g)
-            out->mask[k] |= (uint64_t)((1u << __builtin_amdgcn_readlane(group_count, g0 + k * 4 + g)) - 1u) << (g * 16);
+            out.mask[k] |= (uint64_t)((1u << __builtin_amdgcn_readlane(group_count, g0 + k * 4 + g)) - 1u) << (g * 16);
         }
       }
     } else {
       int64_t at[NP];
-      out->whole = true;
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const bool ok = in[k] != ~0u && (uint32_t)page[k] < (uint32_t)a.num_pages;
-        out->mask[k] = __builtin_amdgcn_ballot_w64(ok);
-        out->whole = out->whole && out->mask[k] == ~0ull;
+        out.mask[k] = __builtin_amdgcn_ballot_w64(ok);
         at[k] = ok ? ((int64_t)page[k] * a.page_stride + (int64_t)in[k] * a.token_stride) * SZ : 0;
       }
 #pragma unroll
       for (int k = 0; k < NL; ++k) {
         const int t = (int)row0 + k * RPL;  // of the tile, before the lane's row
         const int64_t mine = NP == 1 || t < 64 ? at[0] : at[NP - 1];
-        out->at[k] = shfl64(mine, (t & 63) + (int)sub);
+        out.at[k] = shfl64(mine, (t & 63) + (int)sub);
       }
       if (i + 1 < tiles) look_up(i + 1);
     }
+    return out;
   };
   uint32_t inside[NG];  // bytes from the first of sixteen tokens to the lane's chunk
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    const uint32_t t = k * RPL + sub, chunk = F8 ? pos : pos ^ turn<D>(t);
+    const uint32_t t = row0 % 16 + k * RPL + sub, chunk = F8 ? pos : pos ^ turn<D>(t);
     inside[k] = t * (uint32_t)a.token_stride * SZ + chunk * 16;
   }
-  // The tokens of a tile that count, 32 for this wavefront's block tb.
-  auto counts = [&](const uint64_t* m, int tb) -> uint32_t {
-    const int t = tw * (TB * 32) + tb * 32;
-    return (uint32_t)((NP == 1 || t < 64 ? m[0] : m[NP - 1]) >> (t & 63));
+  // A tile's mask from token t on.
+  auto mask_from = [&](const Place& m, uint32_t t) __attribute__((always_inline)) -> uint64_t {
+    uint64_t x = m.mask[0];
+    if constexpr (NP > 1) {
+      const uint64_t y = m.mask[1];
+      x = t < 64 ? x : y;
+    }
+    return x >> (t & 63);
   };
 
   // --- tiles to LDS -------------------------------------------------------------
-  u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];
-  auto issue = [&](const char* base, const Place& at, char* to) {  // 16 bits: straight to LDS
+  // Straight to LDS: 16-bit rows at their turned places, raw e4m3 bytes as they are.
+  auto issue = [&](const char* base, const Place& at, char* to) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < NL; ++k) {
-      const uint32_t where = lds_at(to) + (row0 + k * RPL) * ROW;
-      if constexpr (P16) load_to_lds(base + at.at[k / NG], inside[k % NG], where);
-      else load_to_lds(base + at.at[k] + (pos ^ turn<D>(row0 + k * RPL + sub)) * 16, where);
+      const uint32_t where = lds_at(to) + (row0 + k * RPL) * (D * SZ);
+      if constexpr (P16) load_to_lds(base + readlane64(at.at[k / NG], 0), inside[k % NG], where);
+      else load_to_lds(base + at.at[k] + (F8 ? pos : pos ^ turn<D>(row0 + k * RPL + sub)) * 16, where);
     }
   };
-  auto fetch = [&](const char* base, const Place& at, u32x4* r) {  // e4m3: to registers
-#pragma unroll
-    for (int k = 0; k < NL; ++k) {
-      if constexpr (P16) r[k] = *(const u32x4*)(base + at.at[k / NG] + inside[k % NG]);
-      else r[k] = *(const u32x4*)(base + at.at[k] + pos * 16);
-    }
-  };
-  auto put = [&](const u32x4* r, char* to, const Place* m) {
+  // e4m3: the wavefront's raw bytes, widened, into a tile.
+  auto put = [&](const char* raw, char* to, const Place& m) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < NL; ++k) {
       const uint32_t t = row0 + k * RPL + sub;
+      const u32x4 x = lds_read16(lds_at(raw) + t * D + pos * 16);
       // Tokens that do not count become zeros: their places may hold NaN.
-      const bool ok = m == nullptr || m->whole || (((NP == 1 || t < 64 ? m->mask[0] : m->mask[NP - 1]) >> (t & 63)) & 1u) != 0;
-      const u32x4 lo = widen<T>(u32x2{r[k][0], r[k][1]}), hi = widen<T>(u32x2{r[k][2], r[k][3]});
+      const bool ok = (mask_from(m, t) & 1u) != 0;
+      const u32x4 lo = widen<T>(u32x2{x[0], x[1]}), hi = widen<T>(u32x2{x[2], x[3]});
       const uint32_t at = lds_at(to) + t * ROW + (((pos * 2) ^ turn<D>(t)) << 4);
       *(lds_u32x4*)at = ok ? lo : u32x4{0, 0, 0, 0};
       *(lds_u32x4*)(at ^ 16) = ok ? hi : u32x4{0, 0, 0, 0};
     }
   };
+  // Waits until all but the last n tiles' loads (of keys, or of values) have arrived.
+  auto wait_tiles = [&](int n) __attribute__((always_inline)) {
+    switch (n) {
+      case 0: return wait_loads<0>();
+      case 1: return wait_loads<NL>();
+      case 2: return wait_loads<2 * NL>();
+      case 3: return wait_loads<3 * NL>();
+      default: return wait_loads<4 * NL>();
+    }
+  };
   // The wavefront's rows of a values' tile that do not count (16 bits).
-  auto clear = [&](char* to, const uint64_t* m) {
+  auto clear = [&](char* to, const Place& m) {
     constexpr uint32_t kAll = QT == 32 ? ~0u : (1u << QT) - 1u;
-    const uint32_t mine = (uint32_t)((NP == 1 || row0 < 64 ? m[0] : m[NP - 1]) >> (row0 & 63)) & kAll;
+    const uint32_t mine = (uint32_t)mask_from(m, row0) & kAll;
     if (mine == kAll) return;
 #pragma nounroll
     for (int t = 0; t < QT; ++t)
@@ -370,13 +406,34 @@ __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
   };
 
   // --- one tile -------------------------------------------------------------------
+  // The matrix unit works behind a wavefront's back, so every product is issued
+  // among vector instructions that do not need it: the scores of tile i + 1 among
+  // the weights of tile i, the values of tile i among the maximum of tile i + 1.
+  // (A tile's steps one after the other: 4600 cycles for a wavefront alone of which
+  // 1024 on the matrix unit, and two wavefronts on a SIMD did not fill it.)
+  // The barriers keep the order as it is written.
+  constexpr int E = TB * 16;         // scores of a lane
+  constexpr int M = TB * KS;         // products of a tile's scores,
+  constexpr int N = 2 * TB * DB;     // and of its values
   float ref = -INFINITY, sum = 0.0f;  // base-2 logarithm; of this lane's tokens
-  f32x16 o[DB], s[TB];
+  float by = scale, r = 0.0f, sum_a = 0.0f, sum_b = 0.0f;
+  f32x16 o[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   u32x4 pw[2 * TB];
   const uint32_t key_at = (uint32_t)(tw * TB * 32 + col) * ROW + (((uint32_t)half ^ turn<D>((uint32_t)col)) << 4);
-  auto scores = [&](uint32_t base) {
+  // Weights of scores e and e + 1.
+  using Scores = f32x16[TB];
+  auto weigh = [&](const Scores& s, int e) __attribute__((always_inline)) {
+    const float x = exp2_fast(fmaf(s[e >> 4][e & 15], by, r)), y = exp2_fast(fmaf(s[(e + 1) >> 4][(e + 1) & 15], by, r));
+    sum_a += x;
+    sum_b += y;
+    uint32_t both = T::pack(x, y);
+    asm volatile("" : "+v"(both), "+v"(sum_a), "+v"(sum_b));  // formed here, not where they are used first
+    pw[e >> 3][(e & 7) >> 1] = both;
+  };
+  // Scores of the keys at `base` into s, the weights of `from` among them.
+  auto scores = [&](uint32_t base, Scores& s, const Scores& from, auto among) __attribute__((always_inline)) {
     const uint32_t at = base + key_at;
     auto key = [&](int m) { return lds_read16((at ^ (uint32_t)((m % KS) << 5)) + (uint32_t)(m / KS) * (32 * ROW)); };
     u32x4 ring[kAhead];
@@ -386,62 +443,53 @@ __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
     for (int tb = 0; tb < TB; ++tb) s[tb] = f32x16{};
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int m = 0; m < TB * KS; ++m) {
-      if (m + kAhead - 1 < TB * KS) ring[(m + kAhead - 1) % kAhead] = key(m + kAhead - 1);
+    for (int m = 0; m < M; ++m) {
+      if (m + kAhead - 1 < M) ring[(m + kAhead - 1) % kAhead] = key(m + kAhead - 1);
       s[m / KS] = T::mfma32(ring[m % kAhead], q[m % KS], s[m / KS]);
+      if constexpr (decltype(among)::value) {
+#pragma unroll
+        for (int e = m * (E / M); e < (m + 1) * (E / M); e += 2) weigh(from, e);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto leave_out = [&](const uint64_t* m) {
+  auto leave_out = [&](Scores& s, const Place& m) __attribute__((always_inline)) {
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
-      const uint32_t bits = counts(m, tb);
-      if (bits == 0xffffffffu) continue;
+      const uint32_t bits = (uint32_t)mask_from(m, (uint32_t)(tw * (TB * 32) + tb * 32)) >> (half * 4);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[tb][e] = (bits >> ((e >> 2) * 8 + half * 4 + (e & 3))) & 1u ? s[tb][e] : -INFINITY;
+      for (int e = 0; e < 16; ++e) s[tb][e] = (bits >> ((e >> 2) * 8 + (e & 3))) & 1u ? s[tb][e] : -INFINITY;
     }
   };
-  auto weights = [&] {
-    float top = s[0][0];
-#pragma unroll
-    for (int e = 1; e < TB * 16; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+  // The reference for scores s whose largest product is `top`.
+  auto refer = [&](Scores& s, float top) __attribute__((always_inline)) {
     top = max_xor32(top) * scale;
     if (__builtin_amdgcn_ballot_w64(top > ref + kLazyStep) != 0) {
       const float m = fmaxf(ref, top);
-      const float by = m == ref ? 1.0f : exp2_fast(ref - m);
+      const float less = m == ref ? 1.0f : exp2_fast(ref - m);
       ref = m;
-      sum *= by;
+      sum *= less;
 #pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= by;
+      for (int d = 0; d < DB; ++d) o[d] *= less;
     }
     // A difference to the reference comes unrounded out of one fma, but the
     // reference is a rounded product: far out products are rounded first, so
     // that the largest is the reference.
-    float by = scale;
+    by = scale;
     if (__builtin_amdgcn_ballot_w64(fabsf(ref) > kFar && ref != -INFINITY) != 0) {
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) s[tb] *= scale;
       by = 1.0f;
     }
-    const float r = ref == -INFINITY ? 0.0f : lift<T>(kLazyStep) - ref;
-    float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < 2 * TB; ++k) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_fast(fmaf(s[k >> 1][(k & 1) * 8 + e], by, r));
-        part4[e & 3] += x[e];
-      }
-      pw[k] = u32x4{T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7])};
-    }
-    sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
+    r = ref == -INFINITY ? 0.0f : lift<T>(kLazyStep) - ref;
+    sum_a = sum_b = 0.0f;
   };
   // Lane i of each 16 gives the address of 4 dims of token i / 4.
   const uint32_t i16 = (uint32_t)lane & 15, vt = (uint32_t)half * 4 + (i16 >> 2);
   const uint32_t vchunk = (((uint32_t)lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
   const uint32_t value_at = ((uint32_t)(tw * TB * 32) + vt) * ROW + ((vchunk ^ turn<D>(vt)) << 4) + (i16 & 1) * 8;
-  auto values = [&](uint32_t base) {
+  // The values at `base` by the weights, the largest of s among them.
+  auto values = [&](uint32_t base, const Scores& s, auto among) __attribute__((always_inline)) -> float {
     const uint32_t at = base + value_at;
     // Tokens vt .. and, eight rows further, vt + 8 ..: turn() differs by one bit.
     auto value = [&](int m) {
@@ -449,93 +497,153 @@ __global__ void __launch_bounds__(256, 2) prefix_kernel(AttnParams p) {
       const u32x2 lo = lds_read_tr(x), hi = lds_read_tr((x ^ 32) + 8 * ROW);
       return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
-    constexpr int N = 2 * TB * DB;
     u32x4 ring[kAhead];
 #pragma unroll
     for (int m = 0; m < kAhead - 1; ++m) ring[m] = value(m);
+    float top = -INFINITY;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int m = 0; m < N; ++m) {
       if (m + kAhead - 1 < N) ring[(m + kAhead - 1) % kAhead] = value(m + kAhead - 1);
       o[m % DB] = T::mfma32(ring[m % kAhead], pw[m / DB], o[m % DB]);
+      if constexpr (decltype(among)::value) {
+#pragma unroll
+        for (int e = m * (E / N); e < (m + 1) * (E / N); e += 2)
+          top = fmaxf(fmaxf(top, s[e >> 4][e & 15]), s[(e + 1) >> 4][(e + 1) & 15]);
+        asm volatile("" : "+v"(top));
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
+    return top;
   };
+  auto highest = [&](const Scores& s) __attribute__((always_inline)) -> float {
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) top = fmaxf(fmaxf(top, s[e >> 4][e & 15]), s[(e + 1) >> 4][(e + 1) & 15]);
+    return top;
+  };
+  auto close = [&] __attribute__((always_inline)) { sum += sum_a + sum_b; };
 
-  // Tile i: its scores and weights; then, once its values (and the next tile's
-  // keys) have arrived for every wavefront, its values.  That one barrier also
-  // says that the keys of tile i and the values of tile i - 1 are read: the next
-  // loads into them start behind it, values one tile ahead and keys two.
-  Place now, next, after;
+  // Step i: the weights of tile i and the scores of tile i + 1; then, once the
+  // values of tile i and the keys of tile i + 2 have arrived for every wavefront,
+  // the values.  That one barrier also says that the keys of tile i + 1 and the
+  // values of tile i - 1 are read: the next loads into them start behind it.
+  constexpr int AHEAD = F8 ? RB + 2 : KB;  // tiles that keys are placed ahead
+  Place at_tile[AHEAD + 1], whole;         // of tiles i, i + 1, ...; of one that is not masked
+#pragma unroll
+  for (int k = 0; k < NP; ++k) whole.mask[k] = ~0ull;
+  const auto keys_of = [&](int32_t i) -> char* { return &sk[0][0] + (uint32_t)(i % KB) * TILE; };
+  const auto values_of = [&](int32_t i) -> char* { return &sv[0][0] + (uint32_t)(i % VB) * TILE; };
+  const auto raw_of = [&](int32_t i, int which) -> char* { return &sraw[F8 ? i % (RB > 0 ? RB : 1) : 0][which][0]; };
+  Scores s0, s1;
+  constexpr std::bool_constant<true> kAmong;
+  constexpr std::bool_constant<false> kAlone;
   look_up(0);
-  place(0, &now);
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) {
+    if (d == 0 || d < tiles) at_tile[d] = place(d);
+    else at_tile[d] = at_tile[d - 1];
+  }
+  at_tile[AHEAD] = at_tile[AHEAD - 1];
   if constexpr (!F8) {
-    constexpr int AHEAD = KB - 1;  // tiles that keys are ahead
-    issue(kbase, now, &sk[0][0]);
-    issue(vbase, now, &sv[0][0]);
-    next = now;
-    if (tiles > 1) {
-      place(1, &next);
-      if constexpr (AHEAD == 2) issue(kbase, next, &sk[1][0]);
-    }
-    after = next;
-    if (AHEAD == 2 && tiles > 1) wait_loads<2 * NL>();
-    else wait_loads<NL>();
-    __syncthreads();  // the first tile's keys
-    int ring = 0;     // of tile i in sk
-    for (int32_t i = 0; i < tiles; ++i) {
-      const bool more = i + AHEAD < tiles;
-      const int to = ring == 0 ? KB - 1 : ring - 1;
-      if (more) {
-        if constexpr (AHEAD == 2) place(i + 2, &after);
-        issue(kbase, AHEAD == 2 ? after : next, &sk[to][0]);
-      }
-      scores(lds_at(&sk[0][0]) + (uint32_t)ring * TILE);
-      if (!now.whole) leave_out(now.mask);
-      weights();
-      // All but the keys issued above: with keys one tile ahead those too.
-      if (AHEAD == 2 && more) wait_loads<NL>();
-      else wait_loads<0>();
-      if (!now.whole) clear(&sv[i & 1][0], now.mask);
-      __syncthreads();
-      if (i + 1 < tiles) issue(vbase, next, &sv[(i + 1) & 1][0]);
-      now = next;
-      if constexpr (AHEAD == 2) next = after;
-      else if (i + 2 < tiles) place(i + 2, &next);
-      ring = ring + 1 == KB ? 0 : ring + 1;
-      values(lds_at(&sv[i & 1][0]));
-    }
+#pragma unroll
+    for (int d = 0; d < KB; ++d)
+      if (d < tiles) issue(kbase, at_tile[d], keys_of(d));
+#pragma unroll
+    for (int d = 0; d < VB - 1; ++d)
+      if (d < tiles) issue(vbase, at_tile[d], values_of(d));
+    wait_loads<0>();
   } else {
-    // Raw bytes of tile i + 2 load while tile i is used.
-    fetch(kbase, now, rk);
-    fetch(vbase, now, rv);
-    put(rk, &sk[0][0], nullptr);
-    put(rv, &sv[0][0], &now);
-    next = now;
-    if (tiles > 1) {
-      place(1, &next);
-      fetch(kbase, next, rk);
-      fetch(vbase, next, rv);
+    // The first two tiles of keys and the first of values, and RB behind each.
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      if (d >= tiles) break;
+      issue(kbase, at_tile[d], raw_of(d, 0));
+      if (d == 0) issue(vbase, at_tile[0], raw_of(0, 1));
+      wait_loads<0>();
+      put(raw_of(d, 0), keys_of(d), whole);
+      if (d == 0) put(raw_of(0, 1), values_of(0), at_tile[0]);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the raw bytes are read
     }
-    after = next;
-    __syncthreads();
-    for (int32_t i = 0; i < tiles; ++i) {
-      if (i + 1 < tiles) put(rk, &sk[(i + 1) & 1][0], nullptr);
-      if (i + 2 < tiles) {
-        place(i + 2, &after);
-        fetch(kbase, after, rk);
-      }
-      scores(lds_at(&sk[i & 1][0]));
-      if (!now.whole) leave_out(now.mask);
-      weights();
-      __syncthreads();
-      if (i + 1 < tiles) put(rv, &sv[(i + 1) & 1][0], &next);
-      if (i + 2 < tiles) fetch(vbase, after, rv);
-      now = next;
-      next = after;
-      values(lds_at(&sv[i & 1][0]));
+#pragma unroll
+    for (int d = 0; d < RB; ++d) {
+      if (d + 2 < tiles) issue(kbase, at_tile[d + 2], raw_of(d + 2, 0));
+      if (d + 1 < tiles) issue(vbase, at_tile[d + 1], raw_of(d + 1, 1));
     }
   }
+  if constexpr (!F8)
+    if (!at_tile[0].whole()) clear(values_of(0), at_tile[0]);
+  __syncthreads();
+  scores(lds_at(keys_of(0)), s0, s1, kAlone);
+  if (!at_tile[0].whole()) leave_out(s0, at_tile[0]);
+  float top = highest(s0);
+  __syncthreads();  // the first tile's keys are read
+  auto step = [&](int32_t i, Scores& s, Scores& t) __attribute__((always_inline)) {
+    // Behind the last barrier: the keys of tile i and the values of tile i - 1.
+    const bool more = i + AHEAD < tiles;
+    if (more) at_tile[AHEAD] = place(i + AHEAD);
+    if constexpr (!F8) {
+      if (more) issue(kbase, at_tile[AHEAD], keys_of(i + KB));
+    } else if (i + 2 < tiles) {
+      // Behind these: RB - 1 more of keys and RB of values, while there are any.
+      if (more) wait_loads<(2 * RB - 1) * NL>();
+      else wait_loads<0>();
+      put(raw_of(i + 2, 0), keys_of(i + 2), whole);
+      if (more) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        issue(kbase, at_tile[AHEAD], raw_of(i + AHEAD, 0));
+      }
+    }
+    refer(s, top);
+    scores(lds_at(keys_of(i + 1)), t, s, kAmong);
+    close();
+    if constexpr (!F8) {
+      // Behind the values of tile i and the keys of tile i + 2: values up to tile
+      // i + VB - 2, keys up to tile i + KB.
+      const int32_t keys = (i + KB < tiles ? i + KB : tiles - 1) - (i + 2), some = (i + VB - 2 < tiles ? i + VB - 2 : tiles - 1) - i;
+      wait_tiles((keys > 0 ? keys : 0) + some);
+      if (!at_tile[0].whole()) clear(values_of(i), at_tile[0]);
+    }
+    __syncthreads();
+    if constexpr (!F8) {
+      if (i + VB - 1 < tiles) issue(vbase, at_tile[VB - 1], values_of(i + VB - 1));
+    } else {
+      if (more) wait_loads<(2 * RB - 1) * NL>();
+      else wait_loads<0>();
+      put(raw_of(i + 1, 1), values_of(i + 1), at_tile[1]);
+      if (i + 1 + RB < tiles) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        issue(vbase, at_tile[1 + RB], raw_of(i + 1 + RB, 1));
+      }
+    }
+    if (!at_tile[1].whole()) leave_out(t, at_tile[1]);
+    top = values(lds_at(values_of(i)), t, kAmong);
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) at_tile[d] = at_tile[d + 1];
+  };
+  {
+    int32_t i = 0;
+    for (; i + 2 < tiles; i += 2) {
+      step(i, s0, s1);
+      step(i + 1, s1, s0);
+    }
+    if (i + 1 < tiles) {
+      step(i, s0, s1);
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) s0[tb] = s1[tb];
+    }
+  }
+  // The last tile's weights and values.
+  refer(s0, top);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) weigh(s0, e);
+  close();
+  if constexpr (!F8) {
+    wait_loads<0>();
+    if (tiles > 1 && !at_tile[0].whole()) clear(values_of(tiles - 1), at_tile[0]);
+  }
+  __syncthreads();
+  values(lds_at(values_of(tiles - 1)), s0, kAlone);
 
   sum += __shfl_xor(sum, 32);
   if constexpr (TW > 1) {
