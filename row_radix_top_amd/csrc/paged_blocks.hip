@@ -115,28 +115,34 @@ __global__ void __launch_bounds__(kBlocksBlock) bounds_kernel(BoundsParams p) {
 // ---------------------------------------------------------------------------
 // Choice.  With Q+ = max(Q, 0) and Q- = min(Q, 0),
 //   sum_d max(Q_d B_d, Q_d b_d) = [Q+ Q-] . [B b],
-// one product of 8-bit numbers of length 2 D: S[block][head] = bounds x queries,
-// 16 blocks x 16 columns a matrix instruction, 64 of the 2 D at a time.  The
+// one product of 8-bit numbers of length 2 D: S[head][block] = queries x bounds,
+// 16 heads x 16 blocks a matrix instruction, 64 of the 2 D at a time.  The
 // order of those 64 is the same for both operands, so each lane loads 16
 // consecutive bytes of a page's bounds as they lie.  Sums are whole numbers
 // below 2^21, exact in fp32.
 //
-// The columns of a 16 are the heads of 16 / hp2 rows of a sequence, hp2 the power
-// of two from heads a key-value head up (more than 16 heads: one row, several
-// sixteens), so a row's largest head is a maximum over neighbouring lanes.
+// The 16 are the heads of 16 / hp2 rows of a sequence, hp2 the power of two from
+// heads a key-value head up (more than 16 heads: one row, several sixteens; places
+// without a head repeat the first).  A lane holds four of them for one block, so
+// the largest head is a maximum in the lane and over at most four lanes, and a
+// block's scale, page and place are the lane's own.  (Blocks along the other side:
+// a block's four numbers each need shuffles and four maxima across lanes, 148 us
+// for 1024 rows of 1250 to 3125 blocks.)
 //
 // Fused: a workgroup scores all blocks of its rows into LDS, then each wavefront
 // picks for its rows.  Split: many workgroups score into the workspace and a
 // second launch picks.
 //
-// The pick: keys in registers (fp32 bits in order), bit by bit the largest
-// threshold that at least K reach, counted by ballots on the scalar unit, and
-// ranks by ballots again.
+// The pick: keys in registers (fp32 bits in order) and, between the lowest and the
+// highest finite one, the largest threshold that at least K reach, found by halving
+// (it ends where exactly K do: ten steps or so of the 32 that bits would take),
+// counted by ballots on the scalar unit; ranks by ballots again.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+constexpr uint32_t kInfKey = 0xff800000u;  // infinity's
 
 // n scores (n > k) to the k best's indices, ascending.  TEAM wavefronts (the
 // workgroup's, or one alone) hold 64 KEYS scores each.
@@ -144,26 +150,57 @@ template <int TEAM, int KEYS>
 __device__ __forceinline__ void pick(const float* scores, int32_t n, int32_t k, int32_t* out, int w, int lane, int32_t* s) {
   uint32_t key[KEYS];
   const int32_t base = w * KEYS * 64 + lane;
+  uint32_t low = kInfKey, high = 1;  // of this lane's finite scores
 #pragma unroll
-  for (int i = 0; i < KEYS; ++i) key[i] = base + i * 64 < n ? order_of(scores[base + i * 64]) : 0u;
-  auto total = [&](int32_t x) -> int32_t {  // over the team
-    if constexpr (TEAM == 1) return x;
-    if (lane == 0) s[w] = x;
-    __syncthreads();
-    int32_t sum = 0;
+  for (int i = 0; i < KEYS; ++i) {
+    const bool in = base + i * 64 < n;
+    const uint32_t x = in ? order_of(scores[base + i * 64]) : 1u;
+    const uint32_t y = x < 1u ? 1u : x > kInfKey ? kInfKey : x;  // NaN among the ends
+    key[i] = in ? y : 0u;
+    low = in && y < low ? y : low;
+    high = y < kInfKey && y > high ? y : high;
+  }
 #pragma unroll
-    for (int i = 0; i < TEAM; ++i) sum += s[i];
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t x = (uint32_t)__shfl_xor((int)low, off), y = (uint32_t)__shfl_xor((int)high, off);
+    low = x < low ? x : low;
+    high = y > high ? y : high;
+  }
+  if constexpr (TEAM > 1) {
+    if (lane == 0) s[w] = (int32_t)low, s[TEAM + w] = (int32_t)high;
     __syncthreads();
-    return sum;
-  };
-  uint32_t t = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t want = t | 1u << bit;
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) {
+      const uint32_t x = (uint32_t)s[i], y = (uint32_t)s[TEAM + i];
+      low = x < low ? x : low;
+      high = y > high ? y : high;
+    }
+    __syncthreads();
+  }
+  auto reach = [&](uint32_t t) -> int32_t {  // how many of the team's do
     int32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] >= want));
-    c = total(c);
+    for (int i = 0; i < KEYS; ++i) {
+      c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] >= t));
+      if (i % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // few ballots at a time: scalar registers
+    }
+    if constexpr (TEAM == 1) return c;
+    if (lane == 0) s[w] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) c += s[i];
+    __syncthreads();
+    return c;
+  };
+  // k reach t, and fewer reach `end`.
+  uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)low), end = (uint32_t)__builtin_amdgcn_readfirstlane((int)high) + 1u;
+  if (reach(kInfKey) >= k) t = kInfKey, end = kInfKey + 1u;
+  while (end - t > 1u) {
+    const uint32_t want = t + (end - t) / 2;
+    const int32_t c = reach(want);
     if (c >= k) t = want;
+    else end = want;
     if (c == k) break;
   }
   int32_t above = 0, level = 0;
@@ -172,6 +209,7 @@ __device__ __forceinline__ void pick(const float* scores, int32_t n, int32_t k, 
     above += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] > t));
     level += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] == t));
   }
+  asm volatile("" : "+v"(t));  // ballots are taken again below: all of them would fill the scalar registers
   int32_t ties = k, rank = 0;  // entries at the threshold still wanted; the next entry's place
   if constexpr (TEAM == 1) {
     ties -= above;
@@ -209,32 +247,25 @@ __device__ __forceinline__ void pick_row(const SelectParams& p, const float* sco
   const int32_t k = p.a.num_blocks;
   if (n <= k) {
     for (int32_t i = lane; i < k; i += 64) out[i] = i < n ? i : -1;
-  } else if (n <= 256) {
+  } else if (n <= 4 * 64) {
     pick<1, 4>(scores, n, k, out, 0, lane, nullptr);
-  } else if (n <= 1024) {
+  } else if (n <= 16 * 64) {
     pick<1, 16>(scores, n, k, out, 0, lane, nullptr);
+  } else if (n <= 32 * 64) {
+    pick<1, 32>(scores, n, k, out, 0, lane, nullptr);
+  } else if (n <= 48 * 64) {
+    pick<1, 48>(scores, n, k, out, 0, lane, nullptr);
   } else {
     pick<1, 64>(scores, n, k, out, 0, lane, nullptr);
   }
 }
 
-template <int CTRL>
-__device__ __forceinline__ float max_dpp(float x) {
-  return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true)));
-}
-// The largest over aligned groups of `wide` (1, 2, 4, 8, 16) lanes.
-__device__ __forceinline__ float group_max(float x, int wide) {
-  if (wide > 1) x = max_dpp<0xb1>(x);    // lanes 1 0 3 2
-  if (wide > 2) x = max_dpp<0x4e>(x);    // 2 3 0 1
-  if (wide > 4) x = max_dpp<0x141>(x);   // mirrored within 8
-  if (wide > 8) x = max_dpp<0x140>(x);   // within 16
-  return x;
-}
-
 template <typename T, int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kBlocksBlock) select_kernel(SelectParams p) {
+__global__ void __launch_bounds__(kSelectBlock, 2) select_kernel(SelectParams p) {
   constexpr int QS = D / 64, KS = 2 * QS;  // steps over the dims, and over both bounds
   extern __shared__ __align__(16) float scores[];
+  __shared__ u32x4 sq[NT][KS][64];  // a lane's queries
+  __shared__ __align__(16) float sby[NT][16];
   const paged_select_args& a = p.a;
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -252,20 +283,33 @@ __global__ void __launch_bounds__(kBlocksBlock) select_kernel(SelectParams p) {
   const int32_t r0 = seq * a.next_n + j0;
   const int32_t per = a.num_heads / a.num_kv_heads;
   const int32_t passes = per <= 16 ? 1 : (per + 16 * NT - 1) / (16 * NT);
-  const int32_t row_cols = per <= 16 ? p.hp2 : 16;
+  const int32_t hp2 = p.hp2, hp2_log = __builtin_ctz((uint32_t)hp2);
 
-  int32_t have = 0;  // of the unit's longest row
-  for (int32_t j = 0; j < rows; ++j) {
-    const int32_t n = blocks_of(p, r0 + j);
-    have = n > have ? n : have;
+  // Of the first turns' blocks, looked up before the lengths are there to say which
+  // count: nothing reads the scores of others.
+  const int32_t* table = a.block_table + (int64_t)seq * a.table_stride;
+  const int32_t W = (int32_t)blockDim.x >> 6, first_tile = SPLIT ? part * p.part_tiles : 0;
+  auto pages_at = [&](int32_t four) -> int32_t {
+    const int32_t b = (first_tile + four * 4) * 16 + lane;
+    return b < a.table_width ? table[b] : -1;
+  };
+  const int32_t page0 = pages_at(w), page1 = pages_at(w + W);
+  const int32_t mine = lane < rows ? blocks_of(p, r0 + lane) : 0;  // blocks of the lane's row
+  int32_t have = mine, least = lane < rows ? mine : INT32_MAX;     // and of the longest and the shortest
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int32_t x = __shfl_xor(have, off), y = __shfl_xor(least, off);
+    have = x > have ? x : have;
+    least = y < least ? y : least;
   }
+  have = __builtin_amdgcn_readfirstlane(have);
+  least = __builtin_amdgcn_readfirstlane(least);
   int32_t t0 = 0, t1 = (have + 15) / 16;
   if constexpr (SPLIT) {
-    t0 = part * p.part_tiles;
+    t0 = first_tile;
     t1 = t1 - t0 < p.part_tiles ? t1 : t0 + p.part_tiles;
     if (t0 >= t1) return;
   }
-  const int32_t* table = a.block_table + (int64_t)seq * a.table_stride;
   const char* bounds = (const char*)a.bounds + (int64_t)kvh * a.bounds_head_stride;
   auto score_at = [&](int32_t j) -> float* {
     if constexpr (SPLIT) return p.scores + ((int64_t)(r0 + j) * a.num_kv_heads + kvh) * p.pitch;
@@ -273,17 +317,30 @@ __global__ void __launch_bounds__(kBlocksBlock) select_kernel(SelectParams p) {
   };
 
   for (int32_t pass = 0; pass < passes; ++pass) {
-    u32x4 q[NT][KS];
-    float by[NT];
-    int32_t col_row[NT], col_have[NT];
-    bool head_real[NT];
+    // A wavefront takes four tiles at a time.  Their bounds are read four tiles
+    // ahead, and where they lie is looked up, a block a lane, four more before that.
+    const int32_t fours = (t1 - t0 + 3) / 4;
+    u32x4 ring[4][KS];
+    float scales[4];
+    int32_t pages[4];
+    auto fetch = [&](int d, int32_t page) __attribute__((always_inline)) {
+      pages[d] = __shfl(page, d * 16 + c16);
+      const int64_t at = (uint32_t)pages[d] < (uint32_t)a.num_pages ? pages[d] : 0;
+      const char* from = bounds + at * a.bounds_page_stride + g * 16;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int32_t j = per <= 16 ? (t * 16 + c16) / row_cols : 0;
-      const int32_t head = per <= 16 ? c16 % row_cols : (pass * NT + t) * 16 + c16;
-      col_row[t] = j < rows ? j : -1;
-      head_real[t] = head < per && j < rows;
-      col_have[t] = j < rows ? blocks_of(p, r0 + j) : 0;
+      for (int i = 0; i < KS; ++i) ring[d][i] = *(const u32x4*)(from + i * 64);
+      scales[d] = a.scales[at * a.scales_stride + kvh];
+    };
+    int32_t page = page0, page_next = page1;
+    if (w < fours) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) fetch(d, page);
+    }
+
+    // The queries, a sixteen a wavefront.
+    if (w < NT) {
+      const int32_t j = per <= 16 ? (w * 16 + c16) >> hp2_log : 0;
+      const int32_t head = per <= 16 ? (c16 & (hp2 - 1)) : (pass * NT + w) * 16 + c16;
       const char* from = (const char*)a.q + 2 * ((int64_t)(r0 + (j < rows ? j : 0)) * a.q_row_stride +
                                                  (int64_t)(kvh * per + (head < per ? head : 0)) * a.q_head_stride);
       float x[QS][16], top = 0.0f;
@@ -301,10 +358,12 @@ __global__ void __launch_bounds__(kBlocksBlock) select_kernel(SelectParams p) {
           }
         }
       top = max_xor32(max_xor16(top));
-      by[t] = top * kOver127;
-      const float div = by[t] == 0.0f ? 1.0f : by[t];
+      top *= kOver127;
+      if (g == 0) sby[w][c16] = top;
+      const float div = top == 0.0f ? 1.0f : top;
 #pragma unroll
-      for (int i = 0; i < QS; ++i)
+      for (int i = 0; i < QS; ++i) {
+        u32x4 ups, downs;
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4) {
           uint32_t up = 0, down = 0;
@@ -314,78 +373,76 @@ __global__ void __launch_bounds__(kBlocksBlock) select_kernel(SelectParams p) {
             up |= (uint32_t)(v > 0 ? v : 0) << (8 * e);
             down |= (uint32_t)((v < 0 ? v : 0) & 0xff) << (8 * e);
           }
-          q[t][i][e4] = up;
-          q[t][QS + i][e4] = down;
+          ups[e4] = up;
+          downs[e4] = down;
         }
-    }
-
-    // A tile's pages are looked up two tiles ahead of it, its bounds one.
-    auto page_at = [&](int32_t tile) -> int32_t {
-      const int32_t b = tile * 16 + c16;
-      return b < have ? table[b] : -1;
-    };
-    u32x4 next[KS];
-    float next_scale = 0.0f;
-    auto fetch = [&](int32_t page) {
-      const int64_t at = (uint32_t)page < (uint32_t)a.num_pages ? page : 0;
-      const char* from = bounds + at * a.bounds_page_stride + g * 16;
-#pragma unroll
-      for (int i = 0; i < KS; ++i) next[i] = *(const u32x4*)(from + i * 64);
-      next_scale = a.scales[at * a.scales_stride + kvh];
-    };
-    constexpr int W = kBlocksBlock / 64;
-    int32_t tile = t0 + w;
-    int32_t page = tile < t1 ? page_at(tile) : -1;
-    int32_t page_next = tile + W < t1 ? page_at(tile + W) : -1;
-    if (tile < t1) fetch(page);
-    for (; tile < t1; tile += W) {
-      u32x4 b[KS];
-#pragma unroll
-      for (int i = 0; i < KS; ++i) b[i] = next[i];
-      const float scale = next_scale;
-      const uint32_t valid = (uint32_t)__builtin_amdgcn_ballot_w64((uint32_t)page < (uint32_t)a.num_pages);
-      page = page_next;
-      page_next = tile + 2 * W < t1 ? page_at(tile + 2 * W) : -1;
-      if (tile + W < t1) fetch(page);
-      float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        i32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-          sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b[i]), __builtin_bit_cast(i32x4, q[t][i]),
-                                                      sum, 0, 0, 0);
-        float y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[i] = group_max(head_real[t] ? (float)sum[i] * by[t] : -INFINITY, row_cols);
-          if (per > 16) best[i] = fmaxf(best[i], y[i]);
-        }
-        if (per > 16 && t + 1 < NT) continue;
-        f32x4 z;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int blk = g * 4 + i;
-          const float v = (per > 16 ? best[i] : y[i]) * __shfl(scale, blk);
-          const int32_t at = tile * 16 + blk;
-          const bool always = at < a.first || at >= col_have[per > 16 ? 0 : t] - a.last;
-          z[i] = ((valid >> blk) & 1u) == 0 ? -INFINITY : always ? INFINITY : v;
-        }
-        const int32_t j = per > 16 ? 0 : col_row[t];
-        if (j < 0 || c16 % row_cols != 0) continue;
-        f32x4* to = (f32x4*)(score_at(j) + tile * 16 + g * 4);
-        if (pass > 0) {
-          const f32x4 old = *to;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = fmaxf(z[i], old[i]);
-        }
-        *to = z;
+        sq[w][i][lane] = ups;
+        sq[w][QS + i][lane] = downs;
       }
     }
+    __syncthreads();
+    u32x4 q[NT][KS];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < KS; ++i) q[t][i] = sq[t][i][lane];
+    for (int32_t four = w; four < fours; four += W) {
+      page = page_next;
+      page_next = pages_at(four + 2 * W);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int32_t tile = t0 + four * 4 + d, at = tile * 16 + c16;
+        i32x4 sum[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          sum[t] = i32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            sum[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, q[t][i]), __builtin_bit_cast(i32x4, ring[d][i]),
+                                                           sum[t], 0, 0, 0);
+        }
+        const float scale = scales[d];
+        const bool valid = (uint32_t)pages[d] < (uint32_t)a.num_pages;
+        if (four + W < fours) fetch(d, page);
+        if (tile >= t1) continue;
+        const bool ends = tile * 16 < a.first || tile * 16 + 16 > least - a.last;  // blocks that some row always takes
+        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const f32x4 by = *(const f32x4*)&sby[t][g * 4];
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = (float)sum[t][i] * by[i];
+            if (per > 16) y[i] = best[i] = fmaxf(best[i], y[i]);
+          }
+          if (per > 16 && t + 1 < NT) continue;
+          if (hp2 >= 2) y[0] = fmaxf(y[0], y[1]), y[1] = fmaxf(y[2], y[3]);
+          if (hp2 >= 4) y[0] = fmaxf(y[0], y[1]);
+          if (hp2 >= 8) y[0] = max_xor16(y[0]);
+          if (hp2 >= 16) y[0] = max_xor32(y[0]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (r > 0 && r * hp2 >= 4) break;
+            const int32_t j = per > 16 ? 0 : ((t * 16 + g * 4) >> hp2_log) + r;
+            float z = y[r] * scale;
+            if (ends) {
+              const int32_t n = __shfl(mine, j & 63);
+              z = at < a.first || at >= n - a.last ? INFINITY : z;
+            }
+            z = valid ? z : -INFINITY;
+            if (j >= rows || ((g * 4) & (hp2 - 1)) != 0) continue;
+            float* to = score_at(j) + at;
+            if (pass > 0) z = fmaxf(z, *to);
+            *to = z;
+          }
+        }
+      }
+    }
+    __syncthreads();  // the queries and their scales are read, the scores there
   }
   if constexpr (SPLIT) return;
-  __syncthreads();
-  for (int32_t j = w; j < rows; j += kBlocksBlock / 64)
+  for (int32_t j = w; j < rows; j += (int32_t)blockDim.x >> 6)
     pick_row(p, score_at(j), blocks_of(p, r0 + j), a.blocks + ((int64_t)(r0 + j) * a.num_kv_heads + kvh) * a.num_blocks, lane);
 }
 

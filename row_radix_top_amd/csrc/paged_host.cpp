@@ -392,14 +392,14 @@ int check_select(const paged_select_args* a) {
 
 struct SelectPlan {
   rrt::SelectParams p;
-  int tiles;
+  int tiles, block;
   bool split;
   int64_t grid;
   size_t lds, bytes;
 };
 
 constexpr int32_t kFusedBlocks = 4096;       // what one wavefront picks from
-constexpr size_t kFusedLds = 64 * 1024;
+constexpr size_t kFusedLds = 128 * 1024;
 
 int plan_select(const paged_select_args* a, hipStream_t stream, SelectPlan* out, size_t* reserve = nullptr) {
   if (int rc = check_select(a)) return rc;
@@ -419,6 +419,7 @@ int plan_select(const paged_select_args* a, hipStream_t stream, SelectPlan* out,
   const int64_t tile_rows = per <= 16 ? 16 / p.hp2 : 1;  // rows of a sixteen
   const int64_t fit = a->table_width <= kFusedBlocks ? (int64_t)kFusedLds / row_bytes : 0;
   out->tiles = 1;
+  out->block = rrt::kBlocksBlock;
   if (per > 16) {
     out->tiles = per <= 32 ? 2 : 4;
   } else {
@@ -430,14 +431,15 @@ int plan_select(const paged_select_args* a, hipStream_t stream, SelectPlan* out,
   const int64_t units = seqs * p.seq_units * a->num_kv_heads;
   out->split = fit == 0 || (a->table_width > 512 && units * 2 <= cus);
   if (out->split) {
-    // Parts of 16 blocks for each wavefront and more, two workgroups a CU.
+    // Parts of 128 blocks and more, 64 a wavefront's turn, two workgroups a CU.
     const int64_t tiles = p.pitch / 16, most = std::max<int64_t>(1, std::min<int64_t>(tiles / 8, ceil_div(2 * cus, units)));
-    p.part_tiles = (int32_t)ceil_div(tiles, most);
+    p.part_tiles = (int32_t)ceil_div(ceil_div(tiles, most), 4) * 4;
     p.parts = (int32_t)ceil_div(tiles, p.part_tiles);
     out->bytes = (size_t)a->num_rows * a->num_kv_heads * row_bytes;
   } else {
     p.parts = 1;
     out->lds = (size_t)row_bytes * p.unit_rows;
+    if (out->lds > kFusedLds / 2) out->block = rrt::kSelectBlock;  // one to a CU
   }
   out->grid = units * p.parts;
   if (reserve == nullptr) return TOPK_OK;
@@ -705,7 +707,7 @@ int paged_block_select(const paged_select_args* args, void* workspace, hipStream
   if (int rc = check_workspace(workspace, plan.bytes)) return rc;
   plan.p.scores = static_cast<float*>(workspace);
   if (int rc = launch(rrt::select_kernel_ptr(args->dtype, args->head_dim, plan.tiles, plan.split), plan.grid,
-                      rrt::kBlocksBlock, &plan.p, stream, "paged_block_select", plan.lds))
+                      plan.block, &plan.p, stream, "paged_block_select", plan.lds))
     return rc;
   if (!plan.split) return TOPK_OK;
   return launch(rrt::pick_kernel_ptr(), (int64_t)args->num_rows * args->num_kv_heads, rrt::kPickBlock, &plan.p, stream,

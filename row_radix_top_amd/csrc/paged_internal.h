@@ -156,7 +156,8 @@ struct PoolParams {
 };
 enum { kPoolClear, kPoolHold, kPoolFree, kPoolMoves, kPoolRename };
 
-constexpr int kBlocksBlock = 256;  // threads of a workgroup of the bounds and of the choice
+constexpr int kBlocksBlock = 256;  // threads of a workgroup of the bounds,
+constexpr int kSelectBlock = 512;  // at most, of the choice (split: of kBlocksBlock)
 constexpr int kPickBlock = 1024;   // and of a choice from the workspace
 constexpr int32_t kMostBlocks = 32768;  // of a row that a choice is made from
 
