@@ -155,6 +155,12 @@ struct PoolParams {
   Divisor page;
 };
 enum { kPoolClear, kPoolHold, kPoolFree, kPoolMoves, kPoolRename };
+// What one workgroup does in one launch: rows of a fork, pages of a pool, and
+// entries of a table that it reads or writes.
+constexpr int kSmallBlock = 1024;
+constexpr int32_t kSmallRows = 64, kSmallPages = 8192;
+constexpr int64_t kSmallEntries = 16384;
+enum { kSmallFork, kSmallFree, kSmallCompact };
 
 constexpr int kBlocksBlock = 256;  // threads of a workgroup of the bounds,
 constexpr int kSelectBlock = 512;  // at most, of the choice (split: of kBlocksBlock)
@@ -252,6 +258,7 @@ const void* append_kernel_ptr(int dtype, int store, bool wide);
 const void* fork_kernel_ptr(bool write);
 const void* copy_kernel_ptr(int bytes);
 const void* pool_kernel_ptr(int step);
+const void* small_kernel_ptr(int what);
 // What a row of the attention over a cache reads: all its positions (kOneRow: a
 // sequence has one row; kManyRows: several, which share the reads but may end at
 // different places), or chosen positions, or chosen blocks.

@@ -100,6 +100,45 @@ __global__ void __launch_bounds__(kBlock) fork_write_kernel(ForkParams p) {
   if (stop == p.num_rows && tid == 0) p.pages[0] = before;
 }
 
+// Few rows (kSmallRows, and kSmallEntries of their tables): both steps by one
+// workgroup, a row a wavefront, as launches are what such a call takes: 25.2 us for
+// a call of eight rows and its copy in three of them.
+__global__ void __launch_bounds__(kSmallBlock) fork_small_kernel(ForkParams p) {
+  constexpr int W = kSmallBlock / 64;
+  __shared__ int32_t copied[kSmallRows];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int32_t q = -1, n = 0;  // of row `lane`
+  if (lane < p.num_rows) n = kept(p, table_tokens(p.table_width, p.page_size), lane, &q);
+  for (int32_t i = w; i < p.num_rows; i += W) {
+    const int32_t m = __builtin_amdgcn_readlane(n, i), parent = __builtin_amdgcn_readlane(q, i);
+    const int32_t j = (int32_t)divide((uint32_t)m, p.page), part = m - j * p.page_size;
+    const int32_t last = part != 0 ? p.table[(int64_t)parent * p.table_stride + j] : -1;
+    const int32_t left = n - j * p.page_size;
+    bool other = false;
+    if (last >= 0 && lane != i && left > 0 && (left >= p.page_size || lane < i))
+      other = p.table[(int64_t)q * p.table_stride + j] == last;
+    const bool copy = __builtin_amdgcn_ballot_w64(other) != 0;
+    if (lane == 0) {
+      p.out_lengths[i] = m;
+      p.src[i] = copied[i] = copy ? last : -1;
+      p.tokens[i] = copy ? part : 0;
+    }
+  }
+  __syncthreads();
+  const uint64_t marks = __builtin_amdgcn_ballot_w64(lane < p.num_rows && copied[lane] >= 0);
+  for (int32_t i = w; i < p.num_rows; i += W) {
+    const int32_t before = __builtin_popcountll(marks & ((1ull << i) - 1ull));
+    const bool copy = (marks >> i) & 1u;
+    const int32_t got = copy && before < p.num_free ? p.free_pages[before] : -1;
+    if (lane == 0) p.dst[i] = got;
+    const int32_t need = pages_of(__builtin_amdgcn_readlane(n, i), p.page);
+    const int32_t* from = p.table + (int64_t)(need > 0 ? __builtin_amdgcn_readlane(q, i) : 0) * p.table_stride;
+    int32_t* to = p.out_table + (int64_t)i * p.out_stride;
+    for (int32_t j = lane; j < p.table_width; j += 64) to[j] = j >= need ? -1 : copy && j == need - 1 ? got : from[j];
+  }
+  if (threadIdx.x == 0) p.pages[0] = __builtin_popcountll(marks);
+}
+
 // ---------------------------------------------------------------------------
 // Copy.  A workgroup takes a piece of one page of one cache; V bytes a thread
 // and step.  Bound by its bytes.
@@ -253,6 +292,106 @@ __global__ void __launch_bounds__(kBlock) rename_kernel(PoolParams p) {
   }
 }
 
+// A small pool (kSmallPages) and a small table (kSmallEntries): everything by one
+// workgroup, with the counts in LDS, as launches are what such a call takes (a pool
+// of a few hundred pages: free, compact and copy 50 us in eight of them).
+template <bool COMPACT>
+__global__ void __launch_bounds__(kSmallBlock) small_pool_kernel(PoolParams p) {
+  constexpr int EACH = kSmallPages / kSmallBlock, W = kSmallBlock / 64;
+  __shared__ int32_t refs[kSmallPages];  // then, compact: the move of a page from the limit on, or -1
+  __shared__ int32_t to_page[COMPACT ? kSmallPages / 2 : 1];
+  __shared__ int32_t sums[W], lows[W];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int32_t i = tid; i < kSmallPages; i += kSmallBlock) refs[i] = 0;
+  __syncthreads();
+  for (int32_t s = w; s < p.num_seqs; s += W) {
+    const int32_t need = held_entries(p, s);
+    const int32_t* row = p.table + (int64_t)s * p.table_stride;
+    for (int32_t j = lane; j < need; j += 64) {
+      const int32_t page = row[j];
+      if ((uint32_t)page < (uint32_t)p.num_pages) atomicAdd(&refs[page], 1);
+    }
+  }
+  __syncthreads();
+  // A thread looks after EACH pages.  before: held ones before them.
+  const int32_t first = tid * EACH;
+  uint32_t held = 0;
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) held |= (refs[first + e] != 0 ? 1u : 0u) << e;
+  int32_t upto = __builtin_popcount(held);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int32_t x = __shfl_up(upto, off);
+    if (lane >= off) upto += x;
+  }
+  if (lane == 63) sums[w] = upto;
+  __syncthreads();
+  int32_t before = upto - __builtin_popcount(held), live = 0;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    if (k < w) before += sums[k];
+    live += sums[k];
+  }
+  if constexpr (!COMPACT) {
+    if (tid == 0) p.count[0] = p.num_pages - live;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const int32_t page = first + e;
+      if (page >= p.num_pages) break;
+      p.refs[page] = refs[page];
+      if ((held >> e) & 1u) p.free_pages[p.num_pages - live + before++] = -1;
+      else p.free_pages[page - before] = page;
+    }
+  } else {
+    const int32_t limit = p.limit < 0 ? live : p.limit;
+    const int32_t mine = limit - first;  // of the thread's pages, below the limit
+    int32_t low = __builtin_popcount(mine >= EACH ? held : mine <= 0 ? 0u : held & ((1u << mine) - 1u));
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) low += __shfl_xor(low, off);
+    if (lane == 0) lows[w] = low;
+    __syncthreads();
+    low = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) low += lows[k];
+    const int32_t holes = limit - low, movers = live - low, moves = holes < movers ? holes : movers;
+    if (tid == 0) p.moves[0] = moves, p.live[0] = live;
+    for (int32_t k = moves + tid; k < p.num_pages / 2; k += kSmallBlock) p.src[k] = -1, p.dst[k] = -1;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const int32_t page = first + e;
+      if (page >= p.num_pages) break;
+      const bool is = (held >> e) & 1u;
+      if (page < limit) {
+        const int32_t k = page - before;
+        if (!is && k < moves) p.dst[k] = to_page[k] = page;
+      } else {
+        const int32_t k = before - low;
+        if (is && k < moves) p.src[k] = page;
+        refs[page] = is && k < moves ? k : -1;
+      }
+      before += is ? 1 : 0;
+    }
+    __syncthreads();
+    for (int32_t s = w; s < p.num_seqs; s += W) {
+      const int32_t need = held_entries(p, s);
+      const int32_t* row = p.table + (int64_t)s * p.table_stride;
+      int32_t* to = p.out_table + (int64_t)s * p.out_stride;
+      for (int32_t j = lane; j < p.table_width; j += 64) {
+        int32_t page = row[j];
+        if (j < need && page >= limit && page < p.num_pages) {
+          const int32_t k = refs[page];
+          if (k >= 0) page = to_page[k];
+        }
+        to[j] = page;
+      }
+    }
+  }
+}
+
+const void* small_kernel_ptr(int what) {
+  return what == kSmallFork ? (const void*)&fork_small_kernel : what == kSmallFree ? (const void*)&small_pool_kernel<false>
+                                                              : (const void*)&small_pool_kernel<true>;
+}
 const void* fork_kernel_ptr(bool write) {
   return write ? (const void*)&fork_write_kernel : (const void*)&fork_mark_kernel;
 }

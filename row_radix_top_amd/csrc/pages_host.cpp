@@ -40,6 +40,10 @@ rrt::PoolParams pool_params(const int32_t* block_table, int64_t table_stride, in
   return p;
 }
 
+bool small_pool(const rrt::PoolParams& p) {
+  return p.num_pages <= rrt::kSmallPages && (int64_t)p.num_seqs * p.table_width <= rrt::kSmallEntries;
+}
+
 // Clears the bitmap (and the counts) and sets what the table holds.
 int hold(rrt::PoolParams* p, hipStream_t stream, const char* what) {
   const int64_t words = p->refs != nullptr ? p->num_pages : p->words;
@@ -81,6 +85,8 @@ int paged_fork(const int32_t* block_table, int64_t table_stride, int32_t table_w
   // Each workgroup counts the marks before its rows: 1024 of them at most.
   p.rows_each = (int32_t)std::max<int64_t>(1, ceil_div(num_rows, 1024));
   p.page = rrt::divisor_of(page_size);
+  if (num_rows <= rrt::kSmallRows && (int64_t)num_rows * table_width <= rrt::kSmallEntries)
+    return launch(rrt::small_kernel_ptr(rrt::kSmallFork), 1, rrt::kSmallBlock, &p, stream, "paged_fork");
   if (num_rows > 0)
     if (int rc = launch(rrt::fork_kernel_ptr(false), ceil_div(num_rows, kBlock / 64), kBlock, &p, stream, "paged_fork"))
       return rc;
@@ -150,8 +156,9 @@ int paged_free(const int32_t* block_table, int64_t table_stride, int32_t table_w
   rrt::PoolParams p = pool_params(block_table, table_stride, table_width, lengths, num_seqs, page_size, num_pages);
   p.bits = static_cast<uint32_t*>(workspace);
   p.refs = refs, p.free_pages = free_pages, p.count = count;
-  if (num_pages > 0)
-    if (int rc = hold(&p, stream, "paged_free")) return rc;
+  if (small_pool(p))
+    return launch(rrt::small_kernel_ptr(rrt::kSmallFree), 1, rrt::kSmallBlock, &p, stream, "paged_free");
+  if (int rc = hold(&p, stream, "paged_free")) return rc;
   return launch(rrt::pool_kernel_ptr(rrt::kPoolFree), std::max<int64_t>(1, ceil_div(num_pages, kBlock)), kBlock, &p,
                 stream, "paged_free");
 }
@@ -187,8 +194,9 @@ int paged_compact(const int32_t* block_table, int64_t table_stride, int32_t tabl
   p.out_table = out_table, p.out_stride = out_stride;
   p.src = src, p.dst = dst, p.moves = moves, p.live = live;
   p.limit = limit;
-  if (num_pages > 0)
-    if (int rc = hold(&p, stream, "paged_compact")) return rc;
+  if (small_pool(p))
+    return launch(rrt::small_kernel_ptr(rrt::kSmallCompact), 1, rrt::kSmallBlock, &p, stream, "paged_compact");
+  if (int rc = hold(&p, stream, "paged_compact")) return rc;
   if (int rc = launch(rrt::pool_kernel_ptr(rrt::kPoolMoves), std::max<int64_t>(1, ceil_div(num_pages, kBlock)), kBlock,
                       &p, stream, "paged_compact"))
     return rc;

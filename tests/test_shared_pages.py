@@ -322,3 +322,34 @@ def test_refusals_of_tensors():
     ]:
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("pages", [8190, 8191, 8192, 8193])
+def test_pools_about_what_one_workgroup_takes(pages):
+    rng = np.random.default_rng(pages)
+    table = rng.integers(-2, pages + 2, size=(5, 700))
+    note(f"pool of {pages}")
+    for limit in (None, 0, 1500, pages - 1, pages):
+        check_pool(table, [700, 4, 0, 699, 64], 1, pages, limit)
+
+
+@pytest.mark.parametrize("width", [4095, 4096, 4097])
+def test_tables_about_what_one_workgroup_takes(width):
+    rng = np.random.default_rng(width)
+    for pages in (0, 1, 33, 64, 257, 1025):
+        table = rng.integers(-2, pages + 2, size=(4, width))
+        note(f"pool of {pages} width={width}")
+        for limit in {None, 0, pages // 2, pages}:
+            check_pool(table, [9, 4, 0, width], 1, pages, limit)
+
+
+@pytest.mark.parametrize("rows,width", [(63, 7), (64, 7), (65, 7), (64, 256), (64, 257), (1, 16384), (1, 16385)])
+@pytest.mark.parametrize("cut", [False, True])
+def test_forks_about_what_one_workgroup_takes(rows, width, cut):
+    rng = np.random.default_rng(rows + width)
+    table, lengths, free, _ = batch(rng, 9, width, 3)
+    parents = rng.integers(-1, 10, size=rows)
+    keep = rng.integers(-2, width * 3 + 3, size=rows) if cut else None
+    note(f"fork rows={rows} width={width} cut={cut}")
+    check_fork(table, lengths, parents, keep, free, 3)
+    check_fork(table, lengths, parents, keep, free[:2], 3)
