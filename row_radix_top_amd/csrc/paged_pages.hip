@@ -55,17 +55,14 @@ __global__ void __launch_bounds__(kBlock) fork_mark_kernel(ForkParams p) {
   const int32_t last = part != 0 ? p.table[(int64_t)parent * p.table_stride + j] : -1;
   bool copy = false;
   if (last >= 0) {
-    // Four rows a lane and turn: three reads, one behind the other, are most of the time.
-    for (int32_t r0 = 0; r0 < p.num_rows; r0 += 256) {
+    for (int32_t r0 = 0; r0 < p.num_rows; r0 += 64) {
+      const int32_t r = r0 + lane;
       bool other = false;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int32_t r = r0 + k * 64 + lane;
-        if (r >= p.num_rows || r == i) continue;
+      if (r < p.num_rows && r != i) {
         int32_t q;
         const int32_t n = kept(p, most, r, &q);
         const int32_t left = n - j * p.page_size;  // tokens that it holds from that page on
-        if (left > 0 && (left >= p.page_size || r < i)) other |= p.table[(int64_t)q * p.table_stride + j] == last;
+        if (left > 0 && (left >= p.page_size || r < i)) other = p.table[(int64_t)q * p.table_stride + j] == last;
       }
       if (__builtin_amdgcn_ballot_w64(other) != 0) {
         copy = true;
