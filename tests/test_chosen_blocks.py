@@ -211,6 +211,16 @@ def test_choices_of_long_rows(have):
     c.check_select(have + 5)
 
 
+@pytest.mark.parametrize("heads,kv,seqs,have", [(33, 33, 2, 4096), (136, 17, 4, 4096), (136, 17, 4, 2049)])
+def test_choices_whose_scores_fill_a_workgroup(heads, kv, seqs, have):
+    """Nine rows a sequence, of one page a position: eight of them share a workgroup, with up to 128 KB of scores."""
+    rng = np.random.default_rng(have + heads)
+    rows = rng.integers(have - 150, have + 1, size=(seqs, 9))
+    rows[0, 0], rows[-1, 3], rows[-1, -1] = have, 0, 7
+    c = Keys(rows, heads=heads, kv=kv, dim=64, page=1, width=have, seed=heads)
+    c.check_select(33)
+
+
 def test_the_most_blocks_there_are():
     c = Keys([32768, 32001], heads=1, kv=1, dim=64, page=1, seed=7)
     c.check_select(2000)
