@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kBlocksBlock) bounds_kernel(BoundsParams p) {
 //
 // 64 rows of up to 1024 blocks, 64 heads on 8, bf16: 26 us for 71 MB of bounds (11
 // at a large read's rate): the chain of lengths, table, bounds, then the longest
-// rows.  1024 rows of 1400 to 3125 blocks in four sequences, 32 heads on 4, fp16: 98 us,
-// of which the pick is 28; eight rows' scores fill most of a CU's LDS, so its eight
+// rows.  1024 rows of 1400 to 3125 blocks in four sequences, 32 heads on 4, fp16: 96 us,
+// of which the pick is 23; eight rows' scores fill most of a CU's LDS, so its eight
 // wavefronts score, then pick, with nothing beside them (four rows to a workgroup and
 // two workgroups a CU: 106).
 // ---------------------------------------------------------------------------
@@ -204,13 +204,24 @@ __device__ __forceinline__ void pick(const float* scores, int32_t n, int32_t k, 
   };
   // k reach t, and fewer reach `end`.
   uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)low), end = (uint32_t)__builtin_amdgcn_readfirstlane((int)high) + 1u;
-  if (reach(kInfKey) >= k) t = kInfKey, end = kInfKey + 1u;
-  while (end - t > 1u) {
+  int32_t c = reach(kInfKey);
+  if (c >= k) t = kInfKey, end = kInfKey + 1u;
+  while (end - t > 1u && c != k) {
     const uint32_t want = t + (end - t) / 2;
-    const int32_t c = reach(want);
+    c = reach(want);
     if (c >= k) t = want;
     else end = want;
-    if (c == k) break;
+  }
+  if (TEAM == 1 && c == k) {  // no ties to part
+    int32_t rank = 0;
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      const bool in = key[i] >= t;
+      const uint64_t all = __builtin_amdgcn_ballot_w64(in);
+      if (in) out[rank + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] = base + i * 64;
+      rank += __builtin_popcountll(all);
+    }
+    return;
   }
   int32_t above = 0, level = 0;
 #pragma unroll
