@@ -37,7 +37,7 @@ namespace rrt {
 // start (3 us for the shares, 8 until the first tiles are there: every workgroup
 // asks at once) and 34 MB of parts (6).  Two wavefronts a SIMD: eight to a
 // workgroup, alone on its CU with four buffers of each, took as long (98).
-// Twelve groups of 1 to 32 rows, 40 heads on 8, e4m3: 72 to 75 us.  Eight rows
+// Twelve groups of 1 to 32 rows, 40 heads on 8, e4m3: 72 to 79 us.  Eight rows
 // behind 2000 tokens: 13 us, the chain of dependent reads.
 // ---------------------------------------------------------------------------
 constexpr float kLazyStep = 8.0f;

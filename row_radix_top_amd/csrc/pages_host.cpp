@@ -76,6 +76,8 @@ int paged_fork(const int32_t* block_table, int64_t table_stride, int32_t table_w
                         (const void*)out_lengths, (const void*)src, (const void*)dst, (const void*)tokens,
                         (const void*)pages})
     REQUIRE(aligned(p, 4), "all arrays must be 4-byte aligned");
+  REQUIRE(num_rows == 0 || num_seqs == 0 || (out_table != block_table && out_lengths != lengths),
+          "a fork's table and lengths are not those that it goes on from");
   rrt::ForkParams p{};
   p.table = block_table, p.lengths = lengths, p.parents = parents, p.keep = keep, p.free_pages = free_pages;
   p.out_table = out_table, p.out_lengths = out_lengths, p.src = src, p.dst = dst, p.tokens = tokens, p.pages = pages;

@@ -59,6 +59,12 @@ def test_fork_refuses(changes, text):
     assert text in binding.last_error()
 
 
+@pytest.mark.parametrize("changes", [dict(), dict(out_table=512), dict(out_lengths=512)])
+def test_fork_refuses_to_write_over_what_it_reads(changes):
+    assert _call("paged_fork", FORK, FORK_BASE, changes) == EINVAL
+    assert "goes on from" in binding.last_error()
+
+
 def _copy(pairs=2, num_pages=4, src=256, dst=256, tokens=None, count=1, **cache):
     q = pages.PagedPages(256, 1024, 64, 0, 16, 1, 64)
     for k, v in cache.items():
