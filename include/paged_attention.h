@@ -349,7 +349,9 @@ int paged_bounds(const paged_bounds_args* args, hipStream_t stream);
  * Q_hd = q_hd / s_h rounded to nearest even: whole numbers but for the scales,
  * so that equal inputs give equal choices everywhere.  Ties go to the lower
  * block.  Blocks [0, first) and the last `last` of the row come before all
- * others, blocks without a page after all others.  NaN in q counts as 0.
+ * others, blocks without a page after all others.  NaN in q counts as 0 and an
+ * infinity as the type's largest value; a score past fp32's range counts as its
+ * largest (smallest) finite number, one that is NaN (by its scale) as the smallest.
  *
  *   q            [num_rows, num_heads, head_dim], strides multiples of 16 bytes.
  *   lengths      int32 [num_rows]: row r has ceil(lengths[r] / page_size)

@@ -1,5 +1,7 @@
 // Bounds of a cache's pages in 8 bits, and the choice of pages by them.
 
+#include <cfloat>
+
 #include "paged_device.hpp"
 
 namespace rrt {
@@ -127,7 +129,9 @@ __global__ void __launch_bounds__(kBlocksBlock) bounds_kernel(BoundsParams p) {
 // heads a key-value head up (more than 16 heads: one row, several sixteens; places
 // without a head repeat the first).  A lane holds four of them for one block, so
 // the largest head is a maximum in the lane and over at most four lanes, and a
-// block's scale, page and place are the lane's own.  (Blocks along the other side:
+// block's scale, page and place are the lane's own.  Infinities mark the blocks that
+// are always taken and those without a page, so a score that passes fp32's range (an
+// infinite query or key) is kept as the largest number there is.  (Blocks along the other side:
 // a block's four numbers each need shuffles and four maxima across lanes, 148 us
 // for 1024 rows of 1250 to 3125 blocks.)
 //
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kSelectBlock, 2) select_kernel(SelectParams p)
           for (int r = 0; r < 4; ++r) {
             if (r > 0 && r * hp2 >= 4) break;
             const int32_t j = per > 16 ? 0 : ((t * 16 + g * 4) >> hp2_log) + r;
-            float z = y[r] * scale;
+            float z = __builtin_amdgcn_fmed3f(y[r] * scale, -FLT_MAX, FLT_MAX);  // NaN: the smallest
             if (ends) {
               const int32_t n = __shfl(mine, j & 63);
               z = at < a.first || at >= n - a.last ? INFINITY : z;

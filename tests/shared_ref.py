@@ -107,14 +107,17 @@ def scores(q, bound, scale, largest):
     whole = np.clip(np.rint(q / np.where(by == 0, np.float32(1), by)[:, None]), -127, 127).astype(np.int64)
     hi, lo = bound[:, 0].astype(np.int64), bound[:, 1].astype(np.int64)
     total = np.maximum(whole, 0) @ hi.T + np.minimum(whole, 0) @ lo.T
-    with np.errstate(over="ignore"):
+    most = np.finfo(np.float32).max
+    with np.errstate(over="ignore", invalid="ignore"):
         each = (total.astype(np.float32) * by[:, None]).astype(np.float32).max(axis=0)
-        return (each * scale.astype(np.float32)).astype(np.float32)
+        score = (each * scale.astype(np.float32)).astype(np.float32)
+    return np.where(np.isnan(score), -most, np.clip(score, -most, most))
 
 
 def choose(score, there, k, first, last):
     """The k best of one row's blocks, ascending, -1 past the last."""
     n = len(score)
     b = np.arange(n)
-    x = np.where(there, np.where((b < first) | (b >= n - last), np.inf, score), -np.inf)
-    return padded(np.sort(np.argsort(-x, kind="stable")[:k]), k)
+    rank = np.where(there, np.where((b < first) | (b >= n - last), 0, 1), 2)  # always taken; by its score; no page
+    order = np.lexsort((b, np.where(rank == 1, -score, 0), rank))
+    return padded(np.sort(order[:k]), k)
