@@ -312,8 +312,9 @@ int paged_prefix_attention(const paged_attention_args* args, const int32_t* grou
  *   starts       int32 [num_seqs + 1], as paged_layout gives them: sequence s
  *                has starts[s + 1] - starts[s] new tokens, its last ones.
  *   lengths      int32 [num_seqs], tokens after the step.
- *   num_tokens   the most new tokens there are, paged_layout's capacity; pages
- *                of tokens past it are left as they were.
+ *   num_tokens   the most new tokens there are, paged_layout's capacity; tokens
+ *                past it were not written: they count in no bounds, and pages
+ *                that hold no other new tokens are left as they were.
  *   bounds       int8 [num_pages, num_kv_heads, 2, head_dim], page and head
  *                strides given (in bytes), 16-byte aligned.
  *   scales       fp32 [num_pages, num_kv_heads], rows scales_stride apart.

@@ -58,7 +58,8 @@ def paged_bounds(k_cache, block_table, starts, lengths, bounds, scales, *, num_t
 
     Called after the step's paged_append: starts (int32 [num_seqs + 1]) and
     lengths (int32 [num_seqs]) as paged_layout gives and takes them, num_tokens
-    its capacity.  See paged_bounds in paged_attention.h."""
+    its capacity: new tokens past it count in no bounds.  See paged_bounds in
+    paged_attention.h."""
     lib = load()
     if k_cache.requires_grad:
         _no_gradients("paged_bounds")

@@ -26,7 +26,9 @@ __device__ __forceinline__ float as_e4m3(uint32_t w, int i) {
 //
 // Which page: sequence s gets floor(starts[s] / P) + 2 s as its first unit, and so
 // at least floor(new / P) + 2 of them, as many as `new` tokens at any offset may
-// touch; the search for the unit's sequence probes 64 at a time.
+// touch; the search for the unit's sequence probes 64 at a time.  Of a step that is
+// longer than num_tokens the tokens past it were never written: a sequence ends for
+// its bounds before the first of them.
 // ---------------------------------------------------------------------------
 template <typename T, bool F8, int D>
 __global__ void __launch_bounds__(kBlocksBlock) bounds_kernel(BoundsParams p) {
@@ -51,13 +53,15 @@ __global__ void __launch_bounds__(kBlocksBlock) bounds_kernel(BoundsParams p) {
   const int64_t most = table_tokens(a.table_width, a.page_size);
   const int32_t len = clamp_to(a.lengths[s], most);
   const int64_t fresh = (int64_t)a.starts[s + 1] - a.starts[s];
-  if (fresh <= 0 || len == 0) return;
+  const int32_t room = a.num_tokens - clamp_to(a.starts[s], a.num_tokens);  // for the sequence's new tokens
+  if (fresh <= 0 || len == 0 || room == 0) return;
   const int32_t held = fresh < len ? len - (int32_t)fresh : 0;
+  const int32_t end = len - held < room ? len : held + room;
   const int64_t j = (int64_t)divide((uint32_t)held, p.page) + (u - first_unit(s));
-  if (j < 0 || j * a.page_size >= len) return;
+  if (j < 0 || j * a.page_size >= end) return;
   const int32_t page = a.block_table[(int64_t)s * a.table_stride + j];
   if ((uint32_t)page >= (uint32_t)a.num_pages) return;
-  const int32_t left = len - (int32_t)j * a.page_size, count = left < a.page_size ? left : a.page_size;
+  const int32_t left = end - (int32_t)j * a.page_size, count = left < a.page_size ? left : a.page_size;
 
   float hi[E], lo[E];
 #pragma unroll
