@@ -135,8 +135,9 @@ struct ForkParams {
 
 struct CopyParams {
   const int32_t *src, *dst, *tokens;
-  int32_t num_pages, num_caches;
-  int32_t pieces;  // workgroups of a page and cache
+  int32_t num_pairs, num_pages, num_caches;
+  int32_t pieces;       // workgroups of a page and cache
+  int32_t pair_groups;  // and along the pairs
   paged_pages cache[PAGED_COPY_CACHES];
   Divisor row[PAGED_COPY_CACHES], each[PAGED_COPY_CACHES];  // by a row's steps, and a token's
 };
