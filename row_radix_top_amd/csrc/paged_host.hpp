@@ -30,7 +30,7 @@ using rrt::set_error;
     std::snprintf(buf, sizeof(buf), "%s: no kernel instance for these arguments", what);
     return set_error(TOPK_EINVAL, buf);
   }
-  if (grid > INT32_MAX) {
+  if (grid * block > (int64_t)UINT32_MAX) {  // threads of a launch are counted in 32 bits
     std::snprintf(buf, sizeof(buf), "%s: %lld workgroups are more than one launch takes", what, (long long)grid);
     return set_error(TOPK_EINVAL, buf);
   }
