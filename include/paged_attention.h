@@ -150,8 +150,8 @@ int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* par
  *   pages        int32 [1]: pages that the call needs; more than num_free
  *                means that the free list ran out.
  *
- * The outputs do not overlap the inputs.  A table entry below 0 is no page: it
- * is passed on, never copied.
+ * The outputs overlap neither the inputs nor one another (refused).  A table
+ * entry below 0 is no page: it is passed on, never copied.
  */
 int paged_fork(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lengths,
                int32_t num_seqs, const int32_t* parents, const int32_t* keep, int32_t num_rows,

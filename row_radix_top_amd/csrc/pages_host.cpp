@@ -2,6 +2,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 
 #include "paged_host.hpp"
 
@@ -28,6 +29,40 @@ int check_table(const int32_t* block_table, int64_t table_stride, int32_t table_
   REQUIRE(num_seqs == 0 || (block_table != nullptr && lengths != nullptr), "null block_table or lengths");
   REQUIRE(aligned(block_table, 4) && aligned(lengths, 4), "all arrays must be 4-byte aligned");
   return TOPK_OK;
+}
+
+// An array of the caller's: rows of `width` entries, `stride` apart.
+struct Span {
+  const void* data;
+  int64_t rows, stride, width;
+};
+Span list_of(const void* data, int64_t n) { return {data, 1, n, n}; }
+
+// Whether two arrays share an entry.  Views of one buffer that lie between one
+// another (two tables side by side) do not.
+bool meet(const Span& a, const Span& b) {
+  if (a.data == nullptr || b.data == nullptr || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const int64_t at = (int64_t)(reinterpret_cast<uintptr_t>(a.data) / 4), to = (int64_t)(reinterpret_cast<uintptr_t>(b.data) / 4);
+  if (at >= to + (b.rows - 1) * b.stride + b.width || to >= at + (a.rows - 1) * a.stride + a.width) return false;
+  if (a.rows > b.rows) return meet(b, a);
+  for (int64_t i = 0; i < a.rows; ++i) {
+    // The first row of b that ends behind this one's beginning.
+    const int64_t x = at + i * a.stride, past = x - to - b.width;
+    const int64_t j = past < 0 ? 0 : b.rows == 1 ? 1 : past / b.stride + 1;
+    if (j < b.rows && to + j * b.stride < x + a.width) return true;
+  }
+  return false;
+}
+
+// Whether an output shares an entry with another one or with an input.
+bool overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span* p = o + 1; p != outputs.end(); ++p)
+      if (meet(*o, *p)) return true;
+    for (const Span& in : inputs)
+      if (meet(*o, in)) return true;
+  }
+  return false;
 }
 
 // A bitmap of the pool, whole 16 bytes.
@@ -85,8 +120,11 @@ int paged_fork(const int32_t* block_table, int64_t table_stride, int32_t table_w
                         (const void*)out_lengths, (const void*)src, (const void*)dst, (const void*)tokens,
                         (const void*)pages})
     REQUIRE(aligned(p, 4), "all arrays must be 4-byte aligned");
-  REQUIRE(num_rows == 0 || num_seqs == 0 || (out_table != block_table && out_lengths != lengths),
-          "a fork's table and lengths are not those that it goes on from");
+  REQUIRE(!overlap({{out_table, num_rows, out_stride, table_width}, list_of(out_lengths, num_rows), list_of(src, num_rows),
+                    list_of(dst, num_rows), list_of(tokens, num_rows), list_of(pages, 1)},
+                   {{block_table, num_seqs, table_stride, table_width}, list_of(lengths, num_seqs), list_of(parents, num_rows),
+                    list_of(keep, num_rows), list_of(free_pages, num_free)}),
+          "a fork's outputs overlap one another or what it goes on from (table, lengths, parents, keep, free_pages)");
   rrt::ForkParams p{};
   p.table = block_table, p.lengths = lengths, p.parents = parents, p.keep = keep, p.free_pages = free_pages;
   p.out_table = out_table, p.out_lengths = out_lengths, p.src = src, p.dst = dst, p.tokens = tokens, p.pages = pages;
@@ -164,6 +202,10 @@ int paged_free(const int32_t* block_table, int64_t table_stride, int32_t table_w
           "null free_pages, refs or count");
   REQUIRE(aligned(free_pages, 4) && aligned(refs, 4) && aligned(count, 4), "all arrays must be 4-byte aligned");
   if (int rc = check_workspace(workspace, (size_t)bitmap_words(num_pages) * 4)) return rc;
+  REQUIRE(!overlap({list_of(free_pages, num_pages), list_of(refs, num_pages), list_of(count, 1),
+                    list_of(workspace, bitmap_words(num_pages))},
+                   {{block_table, num_seqs, table_stride, table_width}, list_of(lengths, num_seqs)}),
+          "free_pages, refs, count and workspace overlap one another or the table or lengths");
   rrt::PoolParams p = pool_params(block_table, table_stride, table_width, lengths, num_seqs, page_size, num_pages);
   p.bits = static_cast<uint32_t*>(workspace);
   p.refs = refs, p.free_pages = free_pages, p.count = count;
@@ -199,6 +241,15 @@ int paged_compact(const int32_t* block_table, int64_t table_stride, int32_t tabl
   size_t bytes = 0;
   if (int rc = paged_compact_workspace_size(num_pages, &bytes)) return rc;
   if (int rc = check_workspace(workspace, bytes)) return rc;
+  const Span table = {block_table, num_seqs, table_stride, table_width}, renamed = {out_table, num_seqs, out_stride, table_width};
+  const Span rows = list_of(lengths, num_seqs);
+  REQUIRE(!overlap({list_of(src, num_pages / 2), list_of(dst, num_pages / 2), list_of(moves, 1), list_of(live, 1),
+                    list_of(workspace, (int64_t)bytes / 4), renamed},
+                   {rows}) &&
+              (out_table == block_table ||
+               !overlap({table}, {list_of(src, num_pages / 2), list_of(dst, num_pages / 2), list_of(moves, 1),
+                                  list_of(live, 1), list_of(workspace, (int64_t)bytes / 4), renamed})),
+          "src, dst, moves, live, workspace and out_table overlap one another or the table or lengths");
   rrt::PoolParams p = pool_params(block_table, table_stride, table_width, lengths, num_seqs, page_size, num_pages);
   p.bits = static_cast<uint32_t*>(workspace);
   p.rank = reinterpret_cast<int32_t*>(p.bits + p.words);
