@@ -114,8 +114,6 @@ def _pages_of(x, num_pages: int, tokens: bool, dev: int) -> PagedPages:
     for n, by in zip(reversed(shape[2 if tokens else 1:]), reversed(stride[2 if tokens else 1:])):
         if n == 1:
             continue
-        if by == 0:
-            raise ValueError("a cache's elements must not share memory")
         if outer == 1 and by == width:
             width *= n
         elif outer == 1 or by == outer * outer_step:
@@ -125,6 +123,13 @@ def _pages_of(x, num_pages: int, tokens: bool, dev: int) -> PagedPages:
             raise ValueError("a cache's token must be contiguous, or rows of contiguous elements one stride apart")
     if num_pages > 0 and x.numel() == 0:
         raise ValueError("a cache must not be empty")
+    if not x.is_contiguous():
+        # Every step passes what lies within it.
+        span = width
+        for by, n in sorted(((outer_step, outer), (step, count), (stride[0], num_pages))):
+            if n > 1 and by < span:
+                raise ValueError("a cache's elements must not share memory")
+            span += by * (n - 1)
     return PagedPages(x.data_ptr(), stride[0] * size, step * size, outer_step * size, count, outer, width * size)
 
 
