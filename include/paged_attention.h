@@ -287,7 +287,8 @@ int paged_attention(const paged_attention_args* args, void* workspace, hipStream
  * A sequence with a row shorter than that takes no part and is attended whole,
  * by itself, as is one that no group holds.  args->chosen is NULL; max_splits
  * holds for the shared and for the own positions of a row, at most 32 parts
- * each.  num_groups = 0 is paged_attention.
+ * each.  num_groups = 0 is paged_attention.  A workspace's size holds for any
+ * other number of groups too, none among them, if it was asked for with one or more.
  */
 int paged_prefix_attention_workspace_size(const paged_attention_args* args, int32_t num_groups, hipStream_t stream,
                                           size_t* bytes);

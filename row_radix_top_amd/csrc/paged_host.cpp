@@ -653,10 +653,15 @@ int paged_prefix_attention_workspace_size(const paged_attention_args* args, int3
                                           size_t* bytes) {
   REQUIRE(bytes != nullptr, "null bytes");
   REQUIRE(num_groups >= 0, "num_groups must be >= 0");
-  if (num_groups == 0) return paged_attention_workspace_size(args, stream, bytes);
+  // A step without groups, which is paged_attention, is served too.
+  if (int rc = paged_attention_workspace_size(args, stream, bytes)) return rc;
+  if (num_groups == 0) return TOPK_OK;
   const int32_t* any = reinterpret_cast<const int32_t*>(16);
   PrefixPlan plan;
-  return plan_prefix(args, any, any, num_groups, stream, &plan, bytes);
+  size_t grouped = 0;
+  if (int rc = plan_prefix(args, any, any, num_groups, stream, &plan, &grouped)) return rc;
+  *bytes = std::max(*bytes, grouped);
+  return TOPK_OK;
 }
 
 int paged_prefix_attention(const paged_attention_args* args, const int32_t* group_starts, const int32_t* shared,
