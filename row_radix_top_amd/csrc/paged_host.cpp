@@ -224,7 +224,6 @@ int plan_prefix(const paged_attention_args* a, const int32_t* group_starts, cons
                 hipStream_t stream, PrefixPlan* out, size_t* reserve = nullptr) {
   if (int rc = check_attention(a, false)) return rc;
   REQUIRE(a->chosen == nullptr, "chosen must be NULL");
-  REQUIRE(num_groups >= 1, "num_groups must be >= 0");
   REQUIRE(group_starts != nullptr && shared != nullptr, "null group_starts or shared");
   REQUIRE(aligned(group_starts, 4) && aligned(shared, 4), "group_starts and shared must be 4-byte aligned");
   std::memset(out, 0, sizeof(*out));
