@@ -80,8 +80,9 @@ typedef enum {
  *   row_lengths  int32 [capacity]: position + 1, the length that topk_ragged
  *                and the attention take for the token's row.  Past: 0.
  *   row_seqs     int32 [capacity]: the token's sequence.  Past: -1.
- *   pages        int32 [1]: pages that the step needs; more than num_free
- *                means that the free list ran out.
+ *   pages        int32 [1]: pages that the step needs; more than the free
+ *                list has means that it ran out.  (It has num_free, or the
+ *                `count` of paged_free, whose list is padded with -1.)
  *
  * Tokens past `capacity` are not written; starts and the table are whole
  * all the same.  num_seqs = 0 fills the outputs with their padding.
@@ -147,8 +148,8 @@ int paged_append(const int32_t* slots, int32_t num_tokens, const paged_part* par
  *   src, dst, tokens   int32 [num_rows]: for a row with a new last page that
  *                page's number before and now and how many of its tokens count,
  *                as paged_copy takes them; -1, -1, 0 for all others.
- *   pages        int32 [1]: pages that the call needs; more than num_free
- *                means that the free list ran out.
+ *   pages        int32 [1]: pages that the call needs; more than the free
+ *                list has (as for paged_layout) means that it ran out.
  *
  * The outputs overlap neither the inputs nor one another (refused).  A table
  * entry below 0 is no page: it is passed on, never copied.

@@ -236,7 +236,9 @@ def paged_layout(lengths, new_tokens, free_pages, block_table, *, page_size: int
     step and how many of them are new.  block_table (int32 [num_seqs, width])
     is updated in place: the pages the new tokens need are taken from
     free_pages (int32) in order.  Returns a Layout of `capacity` rows; tokens
-    past it are not written.  See paged_layout in paged_attention.h.
+    past it are not written.  Where its pages are more than free_pages has (its
+    entries, or paged_free's count, whose list is padded with -1), the list ran
+    out and tokens have no place.  See paged_layout in paged_attention.h.
     """
     lib = load()
     if _elsewhere(lengths, stream):

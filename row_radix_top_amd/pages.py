@@ -79,6 +79,9 @@ def paged_fork(block_table, lengths, parents, free_pages, *, page_size: int, kee
 
     block_table (int32 [num_sequences, width]) and lengths stay as they are;
     rows that nothing goes on from are given up (paged_free finds their pages).
+    Where fork.pages is more than free_pages has (its entries, or paged_free's
+    count, whose list is padded with -1), the list ran out: a row without its
+    last page has -1 there.
     """
     lib = load()
     if _elsewhere(lengths, stream):
