@@ -257,7 +257,7 @@ RRT_HD int32_t low_tile(const PrefillParams& p, int32_t seq, int32_t local, int3
 const void* layout_kernel_ptr();
 const void* append_kernel_ptr(int dtype, int store, bool wide);
 const void* fork_kernel_ptr(bool write);
-const void* copy_kernel_ptr(int bytes);
+const void* copy_kernel_ptr(int bytes, bool many);
 const void* pool_kernel_ptr(int step);
 const void* small_kernel_ptr(int what);
 // What a row of the attention over a cache reads: all its positions (kOneRow: a

@@ -142,10 +142,9 @@ __global__ void __launch_bounds__(kSmallBlock) fork_small_kernel(ForkParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Copy.  A workgroup takes a piece of one cache's pages, of one pair or, where
-// there are more pairs than a launch takes, of every pair_groups-th: it looks at 64
-// of those at a time, as a compaction's list is mostly empty.  V bytes a thread and
-// step.  Bound by its bytes: 0.87 GB there and 0.87 GB back in 358 us, 4.9 TB/s
+// Copy.  A workgroup takes a piece of one cache's pages, of one pair or (MANY) of
+// every pair_groups-th: it looks at 64 of those at a time, as a compaction's list is
+// mostly empty.  V bytes a thread and step.  Bound by its bytes: 0.87 GB there and 0.87 GB back in 358 us, 4.9 TB/s
 // where a large copy reaches 5.1; 49 MB each way in 20 us.
 // ---------------------------------------------------------------------------
 template <int V>
@@ -163,33 +162,45 @@ struct Piece<1> {
   using type = uint8_t;
 };
 
-template <int V>
+template <int V, bool MANY>
 __global__ void __launch_bounds__(kBlock) copy_kernel(CopyParams p) {
   using type = typename Piece<V>::type;
   const uint32_t b = blockIdx.x;
   const uint32_t piece = b % (uint32_t)p.pieces, c = b / (uint32_t)p.pieces % (uint32_t)p.num_caches;
-  const int lane = threadIdx.x & 63;
+  const uint32_t first = b / (uint32_t)p.pieces / (uint32_t)p.num_caches;
   const paged_pages& q = p.cache[c];
   const Divisor row = p.row[c], each = p.each[c];  // steps of a row, and of a token
   const uint32_t step = (uint32_t)p.pieces * kBlock;
-  for (int64_t i0 = b / (uint32_t)p.pieces / (uint32_t)p.num_caches; i0 < p.num_pairs; i0 += (int64_t)p.pair_groups * 64) {
-    const int64_t i = i0 + (int64_t)lane * p.pair_groups;
-    int32_t from = -1, to = -1, tokens = q.tokens;
-    if (i < p.num_pairs) {
-      from = p.src[i], to = p.dst[i];
-      if (p.tokens != nullptr) tokens = clamp_to(p.tokens[i], q.tokens);
-    }
-    const bool real = (uint32_t)from < (uint32_t)p.num_pages && (uint32_t)to < (uint32_t)p.num_pages && from != to;
-    for (uint64_t left = __builtin_amdgcn_ballot_w64(real); left != 0; left &= left - 1) {
-      const int l = __builtin_ctzll(left);
-      const uint32_t items = (uint32_t)__builtin_amdgcn_readlane(tokens, l) * each.by;
-      const char* src = (const char*)q.data + (int64_t)__builtin_amdgcn_readlane(from, l) * q.page_stride;
-      char* dst = (char*)q.data + (int64_t)__builtin_amdgcn_readlane(to, l) * q.page_stride;
+  auto real = [&](int32_t from, int32_t to) {
+    return (uint32_t)from < (uint32_t)p.num_pages && (uint32_t)to < (uint32_t)p.num_pages && from != to;
+  };
+  auto copy = [&](int32_t from, int32_t to, int32_t tokens) __attribute__((always_inline)) {
+    const uint32_t items = (uint32_t)tokens * each.by;
+    const char* src = (const char*)q.data + (int64_t)from * q.page_stride;
+    char* dst = (char*)q.data + (int64_t)to * q.page_stride;
 #pragma unroll 4
-      for (uint32_t x = piece * kBlock + threadIdx.x; x < items; x += step) {
-        const uint32_t t = divide(x, each), y = x - t * each.by, o = divide(y, row);
-        const int64_t at = t * q.token_stride + o * q.outer_stride + (int64_t)(y - o * row.by) * V;
-        *(type*)(dst + at) = *(const type*)(src + at);
+    for (uint32_t x = piece * kBlock + threadIdx.x; x < items; x += step) {
+      const uint32_t t = divide(x, each), y = x - t * each.by, o = divide(y, row);
+      const int64_t at = t * q.token_stride + o * q.outer_stride + (int64_t)(y - o * row.by) * V;
+      *(type*)(dst + at) = *(const type*)(src + at);
+    }
+  };
+  if constexpr (!MANY) {
+    const int32_t from = p.src[first], to = p.dst[first];
+    if (!real(from, to)) return;
+    copy(from, to, p.tokens == nullptr ? q.tokens : clamp_to(p.tokens[first], q.tokens));
+  } else {
+    const int lane = threadIdx.x & 63;
+    for (int64_t i0 = first; i0 < p.num_pairs; i0 += (int64_t)p.pair_groups * 64) {
+      const int64_t i = i0 + (int64_t)lane * p.pair_groups;
+      int32_t from = -1, to = -1, tokens = q.tokens;
+      if (i < p.num_pairs) {
+        from = p.src[i], to = p.dst[i];
+        if (p.tokens != nullptr) tokens = clamp_to(p.tokens[i], q.tokens);
+      }
+      for (uint64_t left = __builtin_amdgcn_ballot_w64(real(from, to)); left != 0; left &= left - 1) {
+        const int l = __builtin_ctzll(left);
+        copy(__builtin_amdgcn_readlane(from, l), __builtin_amdgcn_readlane(to, l), __builtin_amdgcn_readlane(tokens, l));
       }
     }
   }
@@ -413,9 +424,12 @@ const void* small_kernel_ptr(int what) {
 const void* fork_kernel_ptr(bool write) {
   return write ? (const void*)&fork_write_kernel : (const void*)&fork_mark_kernel;
 }
-const void* copy_kernel_ptr(int bytes) {
-  return bytes == 16 ? (const void*)&copy_kernel<16> : bytes == 4 ? (const void*)&copy_kernel<4> : (const void*)&copy_kernel<1>;
+template <bool MANY>
+const void* copy_bytes(int bytes) {
+  return bytes == 16 ? (const void*)&copy_kernel<16, MANY> : bytes == 4 ? (const void*)&copy_kernel<4, MANY>
+                                                                       : (const void*)&copy_kernel<1, MANY>;
 }
+const void* copy_kernel_ptr(int bytes, bool many) { return many ? copy_bytes<true>(bytes) : copy_bytes<false>(bytes); }
 const void* pool_kernel_ptr(int step) {
   switch (step) {
     case kPoolClear: return (const void*)&clear_kernel;

@@ -10,15 +10,17 @@ namespace {
 
 constexpr int kBlock = rrt::kPagesBlock;
 constexpr int64_t kRowPiece = 4 * kBlock;  // table entries of a workgroup
-// Workgroups of a copy along its pairs, times those of a page and the caches, at
-// most (a launch takes fewer than 2^24, and a list may be half a large pool).  us with a
-// workgroup for each pair, with 2^12, 2^13, 2^14 and 2^15 in all:
-//   2 caches, 34662 pairs, 13700 of them moves   378  366  361  358  355
-//   2 caches, 2^17 pairs, 10 moves                90   14   14   14   22
-//   8 caches, 2^17 pairs, 60000 moves            623  449  421  412  405
-//   32 caches, 2^18 pairs, 10 moves             2710  193  198  188  171
-//   8 caches, 512 pairs, 500 moves, 64 KB pages  109  109  105  113  112
-constexpr int32_t kCopyGroups = 1 << 13;
+// Workgroups of a copy (pairs times caches times pieces of a page) up to which each
+// pair has its own, and that stride over the pairs of a longer list: a launch takes
+// fewer than 2^24, and a list may be half a large pool.  us with one to a pair, and
+// striding with 2^13, 2^14 and 2^15:
+//   2 caches, 34662 pairs, 13700 of them moves   377  361  357  355
+//   2 caches, 2^17 pairs, 10 moves                90   15   15   20
+//   8 caches, 2^17 pairs, 60000 moves            623  421  411  404
+//   32 caches, 2^18 pairs, 10 moves             2700  199  185  163
+// A fork of 512 rows and its copy, 2^14 workgroups: 33.4 with one to a pair, 34.8
+// striding, as pairs come by vector loads then.
+constexpr int32_t kCopyGroups = 1 << 14;
 
 int check_table(const int32_t* block_table, int64_t table_stride, int32_t table_width, const int32_t* lengths,
                 int32_t num_seqs, int32_t page_size) {
@@ -180,8 +182,10 @@ int paged_copy(const int32_t* src, const int32_t* dst, const int32_t* tokens, in
     // Four steps of every thread for a whole page.
     p.pieces = (int32_t)std::min<int64_t>(ceil_div(bytes, (int64_t)v * kBlock * 4), 1024);
     const int32_t inner = p.num_caches * p.pieces;
-    p.pair_groups = std::min(num_pairs, std::max(1, kCopyGroups / inner));
-    if (int rc = launch(rrt::copy_kernel_ptr(v), (int64_t)p.pair_groups * inner, kBlock, &p, stream, "paged_copy")) return rc;
+    const bool many = num_pairs > std::max(1, kCopyGroups / inner);
+    p.pair_groups = many ? std::max(1, kCopyGroups / inner) : num_pairs;
+    if (int rc = launch(rrt::copy_kernel_ptr(v, many), (int64_t)p.pair_groups * inner, kBlock, &p, stream, "paged_copy"))
+      return rc;
   }
   return TOPK_OK;
 }
