@@ -306,8 +306,9 @@ int paged_prefix_attention(const paged_attention_args* args, const int32_t* grou
  * tokens in the cache:  with hi_d, lo_d the largest and smallest key value of
  * dim d over a page's tokens and s = max_d max(|hi_d|, |lo_d|) * (1 / 127),
  *   bounds[page, head] = [ceil(hi_d / s) .., floor(lo_d / s) ..], scales = s
- * (in fp32, 1 / 127 rounded first; clamped to [-127, 127]; all zeros where s is 0).  NaN is
- * passed over, infinities count as the type's largest value.  The scale of an
+ * (in fp32, 1 / 127 rounded first; clamped to [-127, 127], so that a key may lie
+ * outside by 2^-23 of the largest magnitude, 2^-10 where s is subnormal; all zeros
+ * where s is 0, as it is for zeros alone).  NaN is passed over, infinities count as the type's largest value.  The scale of an
  * e4m3 cache is not part of it: it multiplies all of a head's scores.
  *
  *   k            the key cache, as for paged_attention.
