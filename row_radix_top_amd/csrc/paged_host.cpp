@@ -438,7 +438,13 @@ int plan_select(const paged_select_args* a, hipStream_t stream, SelectPlan* out,
   } else {
     p.parts = 1;
     out->lds = (size_t)row_bytes * p.unit_rows;
-    if (out->lds > kFusedLds / 2) out->block = rrt::kSelectBlock;  // one to a CU
+    // One to a CU, so that nothing else hides its waits: eight wavefronts.  us with four and
+    // with eight of them, 32 heads on 4, rows of one sequence that share a workgroup:
+    //   16 x 32 rows of 4096 blocks, 4 x 256 of 4096        141   92, 259  171
+    //   64 rows alone of 1024 (64 heads on 8), of 4096       32   41, 106  136
+    // (Rows that share one would take eight below that size too: 16 x 32 of 512 29  23, of
+    // 2048 66  47.)
+    if (out->lds > kFusedLds / 2) out->block = rrt::kSelectBlock;
   }
   out->grid = units * p.parts;
   if (reserve == nullptr) return TOPK_OK;
