@@ -36,7 +36,8 @@ __device__ __forceinline__ int32_t pages_of(int32_t n, const Divisor& page) {
 // free pages, in order (each workgroup counts the marks before its rows by
 // itself), and writes the table.  512 rows of 64 pages: 9.4 + 4.0 us, reads that
 // wait for one another (parent, length, entry; four rows a lane side by side took
-// as long).
+// as long).  Each row looks at every other: a call of 2048 rows takes 27 us, of 8192
+// 152, of 32768 3.9 ms.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int32_t kept(const ForkParams& p, int64_t most, int32_t i, int32_t* parent) {
   const int32_t q = p.parents[i];
@@ -144,8 +145,9 @@ __global__ void __launch_bounds__(kSmallBlock) fork_small_kernel(ForkParams p) {
 // ---------------------------------------------------------------------------
 // Copy.  A workgroup takes a piece of one cache's pages, of one pair or (MANY) of
 // every pair_groups-th: it looks at 64 of those at a time, as a compaction's list is
-// mostly empty.  V bytes a thread and step.  Bound by its bytes: 0.87 GB there and 0.87 GB back in 358 us, 4.9 TB/s
-// where a large copy reaches 5.1; 49 MB each way in 20 us.
+// mostly empty.  V bytes a thread and step, the same for all caches of a launch: what
+// their addresses, strides and rows all allow.  Bound by its bytes: 0.88 GB there and
+// 0.88 GB back in 343 us, 5.1 TB/s, a large copy's rate; 49 MB each way in 20 us.
 // ---------------------------------------------------------------------------
 template <int V>
 struct Piece;
@@ -213,6 +215,8 @@ __global__ void __launch_bounds__(kBlock) copy_kernel(CopyParams p) {
 // pages by itself: 32 pages a word, 32 KB for a pool of 256 K pages, from L2.
 // 2048 rows of up to 128 pages of 32 tokens: clear 4.9 us, hold 12 (adds that meet
 // in memory), free 4.6, moves 5, rename 5; launches and one trip to memory each.
+// Calls for pools of 2^18, 2^20 and 2^22 pages (131 K, 524 K and 2.1 M entries): free
+// 20, 62 and 519 us, compact 22, 64 and 534, as every workgroup counts the bitmap.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kBlock) clear_kernel(PoolParams p) {
   const int64_t step = (int64_t)gridDim.x * kBlock, at = (int64_t)blockIdx.x * kBlock + threadIdx.x;

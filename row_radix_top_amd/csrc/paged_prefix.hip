@@ -23,7 +23,8 @@ namespace rrt {
 // operand (16 tokens, one chunk) nor the transposed reads of the values (4 tokens
 // x 4 chunks) meet a bank twice.  Keys have three buffers (two where tiles are
 // of 128 tokens or pages of other than 16), values two.  (e4m3: raw bytes wait in
-// LDS and are widened from there into the tiles.)
+// LDS and are widened from there into the tiles, by writes that do meet: 8 % of the
+// cycles that a CU is at work.)
 //
 // The weights are relative to a reference that follows the running maximum
 // lazily: only a score that passes it by 2^8 moves it (they then stay below 2^8,
@@ -32,12 +33,12 @@ namespace rrt {
 // parts stay fp32.
 //
 // Bound by the two products where 32 rows and more share: 64 rows of 64 heads on 8
-// behind 32768 tokens, bf16: 91 us for 69 GFLOP (43 at the rate of a large product),
+// behind 32768 tokens, bf16: 90 to 101 us with the clock (82 at best) for 69 GFLOP (43 at the rate of a large product),
 // of which 65 are the loop, matrix units busy two thirds of it; the rest is the
 // start (3 us for the shares, 8 until the first tiles are there: every workgroup
 // asks at once) and 34 MB of parts (6).  Two wavefronts a SIMD: eight to a
 // workgroup, alone on its CU with four buffers of each, took as long (98).
-// Twelve groups of 1 to 32 rows, 40 heads on 8, e4m3: 72 to 79 us.  Eight rows
+// Twelve groups of 1 to 32 rows, 40 heads on 8, e4m3: 70 to 79 us (66 at best).  Eight rows
 // behind 2000 tokens: 13 us, the chain of dependent reads.
 // ---------------------------------------------------------------------------
 constexpr float kLazyStep = 8.0f;
