@@ -46,6 +46,10 @@ bool meet(const Span& a, const Span& b) {
   if (a.data == nullptr || b.data == nullptr || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
   const int64_t at = (int64_t)(reinterpret_cast<uintptr_t>(a.data) / 4), to = (int64_t)(reinterpret_cast<uintptr_t>(b.data) / 4);
   if (at >= to + (b.rows - 1) * b.stride + b.width || to >= at + (a.rows - 1) * a.stride + a.width) return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {
+    const int64_t off = ((at - to) % b.stride + b.stride) % b.stride;  // of a's rows from the b row before
+    if (off >= b.width && off + a.width <= b.stride) return false;
+  }
   if (a.rows > b.rows) return meet(b, a);
   for (int64_t i = 0; i < a.rows; ++i) {
     // The first row of b that ends behind this one's beginning.
