@@ -308,8 +308,9 @@ int paged_prefix_attention(const paged_attention_args* args, const int32_t* grou
  *   bounds[page, head] = [ceil(hi_d / s) .., floor(lo_d / s) ..], scales = s
  * (in fp32, 1 / 127 rounded first; clamped to [-127, 127], so that a key may lie
  * outside by 2^-23 of the largest magnitude, 2^-10 where s is subnormal; all zeros
- * where s is 0, as it is for zeros alone).  NaN is passed over, infinities count as the type's largest value.  The scale of an
- * e4m3 cache is not part of it: it multiplies all of a head's scores.
+ * where s is 0, as it is for zeros alone).  NaN is passed over, infinities count
+ * as the type's largest value.  The scale of an e4m3 cache is not part of it: it
+ * multiplies all of a head's scores.
  *
  *   k            the key cache, as for paged_attention.
  *   starts       int32 [num_seqs + 1], as paged_layout gives them: sequence s
